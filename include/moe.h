@@ -133,7 +133,8 @@ typedef struct {
 /* Operation ids for moe_workspace_bytes(). */
 enum { MOE_OP_ROUTE = 0, MOE_OP_PERMUTE = 1, MOE_OP_GROUPED_FFN = 2, MOE_OP_REFILL_SCORE = 3,
        MOE_OP_GROUPED_FFN_NVFP4 = 4, /* grouped FFN of an NVFP4 bank (adds the quantised input) */
-       MOE_OP_ROUTE_PERMUTE = 5 };
+       MOE_OP_ROUTE_PERMUTE = 5,
+       MOE_OP_GROUPED_FFN_A8 = 6 };
 
 /*
  * Router: logits, softmax, top-k, renormalised gates.
@@ -379,6 +380,60 @@ moe_status moe_router_norm_keep(const uint16_t *w_router, int32_t E, int32_t H, 
  */
 moe_status moe_nvfp4_quantize(const uint16_t *x, int32_t T, int32_t n, float act_scale,
                               uint16_t *out, void *stream);
+
+/*
+ * FP8 activation quantisation of T rows of n values (bf16 or fp32, by
+ * x_dtype; row stride x_stride >= n in elements), per row and group of 128
+ * values, the last group of a row holding the n % 128 left over, all in fp32:
+ *   s    = max(amax, 448 * 2^-126) / 448,  amax = the group's largest |x|
+ *   code = the E4M3 rounding (nearest, ties to even) of the fp32 quotient x / s
+ * so that x is about e4m3(code) * s; a group of zeros gets codes 0.  A group
+ * that holds an infinity or a NaN gets s = inf or NaN.  codes [T][n] and
+ * scales [T][ceil(n/128)] fp32 are contiguous and may not overlap x.  This is
+ * the form moe_fp8_matmul reads; moe_grouped_ffn_a8 quantises by itself.
+ * n % 16 == 0, a row stride of whole 16-byte pieces, x and codes 16-byte
+ * aligned (MOE_ERR_UNSUPPORTED otherwise); T < 0, n < 1 or a stride below n ->
+ * MOE_ERR_SHAPE; a null pointer with T > 0 -> MOE_ERR_NULL.
+ */
+moe_status moe_fp8_quantize(const void *x, int32_t x_dtype, int32_t T, int32_t n, int64_t x_stride,
+                            uint8_t *codes, float *scales, void *stream);
+
+/*
+ * Product of two E4M3 matrices with a scale for each block of 128 inputs:
+ *   y[m][n] = sum_kb a_scales[m][kb] * w_scales[n/128][kb]
+ *                    * sum_{i in block kb} e4m3(a[m][i]) * e4m3(w[n][i])
+ * accumulated in fp32 and rounded once to out_dtype.  With bf16 outputs the
+ * products of a block run on the FP8 matrix cores, which cut the products of
+ * every 8 consecutive inputs below 2^-13 of the largest (about 1e-5 of the
+ * result in all); with fp32 outputs they run in full fp32 precision on the
+ * bf16 matrix cores, at half the rate.  a [M][K] and w [N][K]
+ * (one row per output, as in the FP8 banks) have row strides lda, ldw >= K in
+ * bytes; a_scales [M][ceil(K/128)] and w_scales [ceil(N/128)][ceil(K/128)] are
+ * contiguous fp32; y has row stride ldy >= N in elements; it may not overlap
+ * the inputs, and nothing past column N of a row is written.  Any M and N;
+ * K, lda and ldw multiples of 16 and the strides at most 4 MiB; a and w
+ * 16-byte aligned, the rest aligned to its element (MOE_ERR_UNSUPPORTED
+ * otherwise).  A row of a that holds a NaN (or whose scale is one) gives NaN
+ * in that row of y only.  No workspace.
+ */
+moe_status moe_fp8_matmul(const uint8_t *a, const float *a_scales, const uint8_t *w, const float *w_scales,
+                          int32_t M, int32_t N, int32_t K, int64_t lda, int64_t ldw, int32_t out_dtype,
+                          void *y, int64_t ldy, void *stream);
+
+/*
+ * moe_grouped_ffn of an FP8 bank (MOE_W_FP8_BLOCK) with the activations in
+ * FP8 as well: x and the SwiGLU product h are quantised as moe_fp8_quantize
+ * does (h per row and group of 128 inner columns, from its fp32 values), and
+ * all three products run on the FP8 matrix cores as moe_fp8_matmul computes
+ * them for bf16 outputs (for fp32 rows too).  Same arguments, layouts and errors as moe_grouped_ffn; any other
+ * format -> MOE_ERR_UNSUPPORTED, as are T * hidden >= 2^32 values.  A row of
+ * x that holds an infinity or a NaN gives NaN in its own rows only.
+ * Workspace: moe_workspace_bytes(MOE_OP_GROUPED_FFN_A8, T, k, E, H, F).
+ */
+moe_status moe_grouped_ffn_a8(const uint16_t *x, int32_t T, int32_t k, const moe_experts *ex,
+                              const int32_t *expert_offsets, const int32_t *sorted_pair,
+                              int32_t out_dtype, void *rows, void *ws, size_t ws_bytes,
+                              void *stream);
 
 /* Scratch bytes an operation needs (0 when none).  For MOE_OP_GROUPED_FFN,
  * k is the pairs per token and E the bank's expert count; an NVFP4 bank needs

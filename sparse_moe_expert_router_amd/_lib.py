@@ -30,6 +30,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 OP_ROUTE, OP_PERMUTE, OP_GROUPED_FFN, OP_REFILL_SCORE, OP_GROUPED_FFN_NVFP4, OP_ROUTE_PERMUTE = 0, 1, 2, 3, 4, 5
+OP_GROUPED_FFN_A8 = 6
 W_BF16, W_AWQ, W_FP8, W_NVFP4, W_AWQ_OM = 0, 1, 2, 3, 4
 OUT_BF16, OUT_F32 = 0, 1
 
@@ -37,7 +38,7 @@ EXPORTS = ["moe_route", "moe_permute", "moe_route_permute", "moe_grouped_ffn", "
            "moe_grouped_ffn_noalloc_max_bytes", "moe_layer", "moe_layer_workspace_bytes", "moe_combine",
            "moe_refill_score",
            "moe_refill_finalize", "moe_prune_slice", "moe_router_norm_keep",
-           "moe_nvfp4_quantize", "moe_awq_to_output_major", "moe_workspace_bytes", "moe_status_string",
+           "moe_nvfp4_quantize", "moe_fp8_quantize", "moe_fp8_matmul", "moe_grouped_ffn_a8", "moe_awq_to_output_major", "moe_workspace_bytes", "moe_status_string",
            "moe_last_hip_error"]
 
 
@@ -71,7 +72,7 @@ def lib():
         raise MoeError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
                        "(python sparse_moe_expert_router_amd/build.py)")
     L = ctypes.CDLL(LIB_PATH)
-    P, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     sig = {
         "moe_route": [P, P, i32, i32, i32, i32, i32, P, P, P, P, P, sz, P],
         "moe_permute": [P, i32, i32, i32, P, P, P, P, sz, P],
@@ -84,6 +85,9 @@ def lib():
         "moe_prune_slice": [P, i32, P, P, i32, ctypes.POINTER(_Experts), ctypes.POINTER(_Experts), P],
         "moe_router_norm_keep": [P, i32, i32, i32, P, P, P],
         "moe_nvfp4_quantize": [P, i32, i32, ctypes.c_float, P, P],
+        "moe_fp8_quantize": [P, i32, i32, i32, i64, P, P, P],
+        "moe_fp8_matmul": [P, P, P, P, i32, i32, i32, i64, i64, i32, P, i64, P],
+        "moe_grouped_ffn_a8": [P, i32, i32, ctypes.POINTER(_Experts), P, P, i32, P, P, sz, P],
         "moe_awq_to_output_major": [ctypes.POINTER(_Experts), ctypes.POINTER(_Experts), P],
         "moe_layer": [P, i32, P, i32, ctypes.POINTER(_Experts), ctypes.POINTER(_Experts), P, P, P, P, sz, P,
                       P, ctypes.POINTER(P)],
@@ -119,6 +123,30 @@ def _ptr(t):
 
 def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+class _Device:
+    """Runs the library's calls on a tensor's device: its index and its current
+    stream, with that device current while the call is made."""
+
+    def __init__(self, t):
+        if t.device.type != "cuda":
+            raise MoeError(f"expected a GPU tensor, got one on {t.device}")
+        self.index = t.device.index
+        self.stream = torch._C._cuda_getCurrentRawStream(self.index)
+
+    def call(self, name, *args):
+        f = getattr(lib(), name)
+        if self.index == torch.cuda.current_device():
+            _check(name, f(*args))
+        else:
+            with torch.cuda.device(self.index):
+                _check(name, f(*args))
+
+
+def _require(ok, name, what):
+    if not ok:
+        raise MoeError(f"{name}: {what}")
 
 
 def workspace_bytes(op, T, k, E, H, F=0) -> int:
@@ -349,6 +377,86 @@ def nvfp4_quantize(x, act_scale: float, out=None):
     _check("moe_nvfp4_quantize", lib().moe_nvfp4_quantize(_ptr(x), T, n, float(act_scale), _ptr(out),
                                                           _stream()))
     return out
+
+
+def fp8_quantize(x, codes=None, scales=None):
+    """FP8 activation quantisation of x [T, n] (bf16 or fp32, n % 16 == 0, rows may be strided):
+    returns (codes uint8 E4M3 [T, n], scales fp32 [T, ceil(n/128)]), one scale per row and 128 values."""
+    name = "moe_fp8_quantize"
+    _require(x.dim() == 2 and x.dtype in (torch.bfloat16, torch.float32) and (x.shape[1] <= 1 or x.stride(1) == 1),
+             name, "x must be a bf16 or fp32 matrix with contiguous rows")
+    T, n = x.shape
+    if codes is None:
+        codes = torch.empty((T, n), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty((T, -(-n // 128)), dtype=torch.float32, device=x.device)
+    _require(codes.shape == x.shape and codes.dtype == torch.uint8 and codes.is_contiguous(), name,
+             "codes must be contiguous uint8 of x's shape")
+    _require(scales.shape == (T, -(-n // 128)) and scales.dtype == torch.float32 and scales.is_contiguous(), name,
+             "scales must be contiguous fp32 [T, ceil(n/128)]")
+    _require(codes.device == x.device and scales.device == x.device, name, "tensors on different devices")
+    d = _Device(x)
+    d.call(name, x.data_ptr(), OUT_F32 if x.dtype == torch.float32 else OUT_BF16, T, n,
+           x.stride(0) if T > 1 else n, codes.data_ptr(), scales.data_ptr(), d.stream)
+    return codes, scales
+
+
+def fp8_matmul(a_codes, a_scales, w_codes, w_scales, out_dtype=None, y=None):
+    """y [M, N] = (a . a_scales) (w . w_scales)^T of E4M3 codes a [M, K] and w [N, K] (uint8, K % 16 == 0, rows
+    may be strided), scales fp32 [M, ceil(K/128)] and [ceil(N/128), ceil(K/128)]; fp32 sums, one rounding.
+    y's dtype, or out_dtype (OUT_BF16 unless given), says whether y is bf16 or fp32; y's rows may be strided."""
+    name = "moe_fp8_matmul"
+    _require(a_codes.dim() == 2 and w_codes.dim() == 2 and a_codes.dtype == torch.uint8 and
+             w_codes.dtype == torch.uint8, name, "codes must be uint8 matrices")
+    M, K = a_codes.shape
+    N = w_codes.shape[0]
+    kb = -(-K // 128)
+    _require(w_codes.shape[1] == K and (K <= 1 or (a_codes.stride(1) == 1 and w_codes.stride(1) == 1)), name,
+             "a and w must have the same number of inputs, contiguous in each row")
+    _require(a_scales.shape == (M, kb) and w_scales.shape == (-(-N // 128), kb) and
+             a_scales.dtype == torch.float32 and w_scales.dtype == torch.float32 and a_scales.is_contiguous() and
+             w_scales.is_contiguous(), name,
+             "scales must be contiguous fp32 [M, ceil(K/128)] and [ceil(N/128), ceil(K/128)]")
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.float32 if out_dtype == OUT_F32 else torch.bfloat16,
+                        device=a_codes.device)
+    f32 = y.dtype == torch.float32
+    _require(y.shape == (M, N) and (f32 or y.dtype == torch.bfloat16) and (N <= 1 or y.stride(1) == 1) and
+             out_dtype in (None, OUT_F32 if f32 else OUT_BF16), name,
+             "y must be [M, N] of out_dtype with contiguous rows")
+    _require(all(t.device == a_codes.device for t in (a_scales, w_codes, w_scales, y)), name,
+             "tensors on different devices")
+    d = _Device(a_codes)
+    d.call(name, a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(), M, N, K,
+           a_codes.stride(0) if M > 1 else K, w_codes.stride(0) if N > 1 else K, OUT_F32 if f32 else OUT_BF16,
+           y.data_ptr(), y.stride(0) if M > 1 else N, d.stream)
+    return y
+
+
+def grouped_ffn_a8(x, k: int, bank: dict, offsets=None, sorted_pair=None, out_dtype=OUT_BF16, ws=None, rows=None):
+    """grouped_ffn of an "fp8" bank with the activations quantised to FP8 too (x and the SwiGLU product, per row
+    and 128 values): rows [T*k, H] in grouped order (identity order when offsets is None)."""
+    name = "moe_grouped_ffn_a8"
+    _require(bank["fmt"] == "fp8", name, f"needs an fp8 bank, got {bank['fmt']}")
+    E, H, F = bank_dims(bank)
+    _require(x.dim() == 2 and x.shape[1] == H and x.dtype == torch.bfloat16 and x.is_contiguous(), name,
+             "x must be contiguous bf16 [T, H]")
+    T = x.shape[0]
+    dt = torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
+    if rows is None:
+        rows = torch.empty((T * k, H), dtype=dt, device=x.device)
+    _require(rows.shape == (T * k, H) and rows.dtype == dt and rows.is_contiguous(), name,
+             "rows must be contiguous [T*k, H] of out_dtype")
+    if offsets is not None and sorted_pair is not None:
+        _require(offsets.shape == (E + 1,) and sorted_pair.shape == (T * k,) and offsets.dtype == torch.int32 and
+                 sorted_pair.dtype == torch.int32 and offsets.is_contiguous() and sorted_pair.is_contiguous(), name,
+                 "offsets and sorted_pair must be int32 [E+1] and [T*k]")
+    st = experts_struct(bank)
+    buf, n = _ws(ws, x.device).get(workspace_bytes(OP_GROUPED_FFN_A8, T, k, E, H, F))
+    d = _Device(x)
+    d.call(name, x.data_ptr(), T, k, ctypes.byref(st), _ptr(offsets), _ptr(sorted_pair), out_dtype,
+           rows.data_ptr(), _ptr(buf), n, d.stream)
+    return rows
 
 
 def awq_to_output_major(bank: dict) -> dict:

@@ -620,6 +620,55 @@ moe_status moe_nvfp4_quantize(const uint16_t* x, int32_t T, int32_t n, float act
     return hip_status(moe::launch_nvfp4_quantize(x, T, n, act_scale, out, static_cast<hipStream_t>(stream)));
 }
 
+moe_status moe_fp8_quantize(const void* x, int32_t x_dtype, int32_t T, int32_t n, int64_t x_stride, uint8_t* codes,
+                            float* scales, void* stream) {
+    if (T < 0 || n < 1 || x_stride < n) return MOE_ERR_SHAPE;
+    if (x_dtype != MOE_OUT_BF16 && x_dtype != MOE_OUT_F32) return MOE_ERR_UNSUPPORTED;
+    const int f32 = x_dtype == MOE_OUT_F32;
+    if (n % 16 || x_stride % (f32 ? 4 : 8)) return MOE_ERR_UNSUPPORTED;
+    if ((int64_t)T * (((int64_t)n + 127) / 128) * 8 > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (!x || !codes || !scales) return MOE_ERR_NULL;
+    if (!aligned16(x) || !aligned16(codes) || (uintptr_t)scales % 4) return MOE_ERR_UNSUPPORTED;
+    return hip_status(moe::launch_fp8_quantize(x, f32, T, n, x_stride, codes, scales, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_fp8_matmul(const uint8_t* a, const float* a_scales, const uint8_t* w, const float* w_scales, int32_t M,
+                          int32_t N, int32_t K, int64_t lda, int64_t ldw, int32_t out_dtype, void* y, int64_t ldy,
+                          void* stream) {
+    if (M < 0 || N < 1 || K < 1 || lda < K || ldw < K || ldy < N) return MOE_ERR_SHAPE;
+    if (out_dtype != MOE_OUT_BF16 && out_dtype != MOE_OUT_F32) return MOE_ERR_UNSUPPORTED;
+    // rows are read in 16-byte pieces; a tile's rows are addressed with 31 bits
+    if (K % 16 || lda % 16 || ldw % 16 || lda > (1 << 22) || ldw > (1 << 22)) return MOE_ERR_UNSUPPORTED;
+    if (((int64_t)M + 15) / 16 * (((int64_t)N + 15) / 16) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (M == 0) return MOE_OK;
+    if (!a || !a_scales || !w || !w_scales || !y) return MOE_ERR_NULL;
+    const int f32 = out_dtype == MOE_OUT_F32;
+    if (!aligned16(a) || !aligned16(w) || (uintptr_t)a_scales % 4 || (uintptr_t)w_scales % 4 ||
+        (uintptr_t)y % (f32 ? 4 : 2))
+        return MOE_ERR_UNSUPPORTED;
+    return hip_status(moe::launch_fp8_matmul(a, a_scales, w, w_scales, M, N, K, lda, ldw, f32, y, ldy,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_grouped_ffn_a8(const uint16_t* x, int32_t T, int32_t k, const moe_experts* ex,
+                              const int32_t* expert_offsets, const int32_t* sorted_pair, int32_t out_dtype, void* rows,
+                              void* ws, size_t ws_bytes, void* stream) {
+    moe::FfnArgs f;
+    size_t need = 0;
+    moe_status st = ffn_prepare(x, T, k, ex, expert_offsets, sorted_pair, out_dtype, rows, &f, &need);
+    if (st != MOE_OK) return st;
+    if (ex->gate.fmt != MOE_W_FP8_BLOCK) return MOE_ERR_UNSUPPORTED;
+    // quantised rows are addressed with 32 bits
+    if ((uint64_t)T * ex->hidden >= (1ull << 32)) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    need = moe::ffn_a8_ws_bytes(T, k, ex->num_experts, ex->hidden, ex->inter);
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+    if (!ws) return MOE_ERR_NULL;
+    if (!aligned16(ws)) return MOE_ERR_UNSUPPORTED;
+    return hip_status(moe::launch_ffn_a8(f, ws, static_cast<hipStream_t>(stream)));
+}
+
 size_t moe_workspace_bytes(int32_t op, int32_t T, int32_t k, int32_t E, int32_t H, int32_t F) {
     if (T <= 0 || k <= 0 || E <= 0) return 0;
     switch (op) {
@@ -628,6 +677,7 @@ size_t moe_workspace_bytes(int32_t op, int32_t T, int32_t k, int32_t E, int32_t 
         case MOE_OP_GROUPED_FFN: return moe::ffn_ws_bytes(T, k, E, H, F, MOE_W_AWQ_G32_OM);
         case MOE_OP_GROUPED_FFN_NVFP4: return moe::ffn_ws_bytes(T, k, E, H, F, MOE_W_NVFP4);
         case MOE_OP_ROUTE_PERMUTE: return route_permute_ws(T, k, E, H);
+        case MOE_OP_GROUPED_FFN_A8: return moe::ffn_a8_ws_bytes(T, k, E, H, F);
         case MOE_OP_REFILL_SCORE: return moe::refill_ws_bytes(T, k);
         default: return 0;
     }

@@ -1,0 +1,103 @@
+// FP8 (OCP E4M3) pieces shared by the activation quantiser and the W8A8
+// kernels (not part of the ABI).
+//
+// Quantisation, per row and group of 128 values (the last group of a row may
+// be shorter), all in fp32:
+//   s    = max(amax, 448 * 2^-126) / 448    (448 is the largest E4M3 value)
+//   code = E4M3 rounding (nearest, ties to even) of the fp32 quotient x / s
+// The lower bound keeps s a normal number: a group of zeros gets codes 0 and
+// s = 2^-126.  amax is taken over the magnitudes' bit patterns, where a NaN
+// is larger than an infinity and that larger than any number, so a group that
+// holds one gets s = NaN or inf and stands for NaN wherever it is used.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kFp8Block = 128;             // values per scale
+constexpr uint32_t kOob = 0x80000000u;     // a buffer offset past every buffer used here (they stay below 2 GiB)
+
+// Number of scales of a row of n values.
+__host__ __device__ __forceinline__ int fp8_blocks(int n) { return (n + kFp8Block - 1) / kFp8Block; }
+
+// Scale of a group from the bit pattern of its largest magnitude.
+__device__ __forceinline__ float fp8_scale(uint32_t amax_bits) {
+    const float a = __uint_as_float(amax_bits);
+    const float lo = 0x1.cp-118f;         // 448 * 2^-126
+    return __fdiv_rn(a < lo ? lo : a, 448.0f);
+}
+
+// Four quotients to four E4M3 codes, v0 in the low byte (v_cvt_pk_fp8_f32:
+// nearest, ties to even; |x / s| <= 448 up to its own rounding, which E4M3
+// rounds back to 448).
+__device__ __forceinline__ uint32_t fp8_pack4(float v0, float v1, float v2, float v3, float s) {
+    int w = 0;
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(__fdiv_rn(v0, s), __fdiv_rn(v1, s), w, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(__fdiv_rn(v2, s), __fdiv_rn(v3, s), w, true);
+    return (uint32_t)w;
+}
+
+// Bit pattern of |v|.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// 16 x 16 x 128 E4M3 product of one block, no accumulator: lane l of `rows`
+// holds 32 values of row l % 16, lane l of `cols` the same 32 inputs of column
+// l % 16; result i of lane l is row 4 (l / 16) + i, column l % 16.  Which 32
+// of the 128 inputs a lane group l / 16 holds does not matter as long as both
+// operands agree.
+//
+// The FP8 MFMA (kExact = false) does not add its products in full fp32: a
+// probe of single products shows that the eight products of eight consecutive
+// values of a lane are aligned to the largest exponent among them and cut
+// toward zero below 2^-13 of it (16 x 16 x 32 alike); the sums of eight are
+// then added in fp32.  On normally distributed data that is an error of
+// 1.4e-5 of the result, two orders below the rounding to bf16, so outputs
+// that are rounded to bf16 or E4M3 take it.  fp32 outputs take kExact: the
+// E4M3 values widened to bf16 (exact) and four bf16 MFMAs of 32 inputs, whose
+// sums keep fp32 precision, at half the rate.
+typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ bf16x8_t fp8_to_bf16x8(int lo, int hi) {
+    const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+    const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+    const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+    const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+    const bf16x4_t ab = __builtin_shufflevector(a, b, 0, 1, 2, 3), cd = __builtin_shufflevector(c, d, 0, 1, 2, 3);
+    return __builtin_shufflevector(ab, cd, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+template <bool kExact>
+__device__ __forceinline__ f32x4_t mfma_fp8(i32x8_t rows, i32x8_t cols) {
+    f32x4_t z = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (!kExact) {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(rows, cols, z, 0, 0, 0, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8_to_bf16x8(rows[2 * i], rows[2 * i + 1]),
+                                                        fp8_to_bf16x8(cols[2 * i], cols[2 * i + 1]), z, 0, 0, 0);
+        return z;
+    }
+}
+
+__device__ __forceinline__ i32x8_t join8(i32x4_t a, i32x4_t b) {
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t fp8_rsrc(const void* p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
+}
+
+__device__ __forceinline__ i32x4_t buf_load16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
+    return __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, 0));
+}
+
+__device__ __forceinline__ float buf_load_f32(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, (int)voff, (int)soff, 0));
+}
+
+}  // namespace moe

@@ -1,0 +1,40 @@
+// Internal interface of the W8A8 kernels (fp8_skinny.hip, fp8_ffn.hip).
+#pragma once
+
+#include "kernels.h"
+
+namespace moe {
+
+// y [M][N] = (a . sa) (w . sw)^T; leading dimensions in elements.
+struct Fp8Dense {
+    const uint8_t* a;   // [M][K], row stride lda
+    const float* sa;    // [M][ceil(K/128)]
+    const uint8_t* w;   // [N][K], row stride ldw
+    const float* sw;    // [ceil(N/128)][ceil(K/128)]
+    int M, N, K;
+    int64_t lda, ldw, ldy;
+    void* y;
+    int out_f32;
+    int vec;            // 1: y's base and stride allow stores of four neighbouring outputs
+};
+
+// Grouped SwiGLU experts on quantised rows.
+struct Fp8Ffn {
+    int T, k, H, F, E, P;
+    const int32_t* offsets;      // [E+1] or nullptr (identity: E == 1)
+    const int32_t* sorted_pair;  // [P] or nullptr
+    const int32_t* tiles;        // tiles[0] = count, then (expert, first row) pairs
+    const uint8_t *gate, *up, *down;
+    const float *sgate, *sup, *sdown;
+    const uint8_t* xq;           // [T][H]
+    const float* xs;             // [T][H/128]
+    uint8_t* hq;                 // [P][F]
+    float* hs;                   // [P][F/128]
+    void* rows;                  // [P][H]
+    int out_f32;
+};
+
+hipError_t launch_fp8_skinny(const Fp8Dense& p, hipStream_t s);
+hipError_t launch_fp8_skinny_ffn(const Fp8Ffn& p, int max_tiles, hipStream_t s);
+
+}  // namespace moe

@@ -64,6 +64,14 @@ hipError_t launch_nvfp4_quantize(const uint16_t* x, int T, int n, float act_scal
                                  hipStream_t s);
 hipError_t launch_ffn(const FfnArgs& a, void* ws, hipStream_t s);
 
+// ---- FP8 products with activations in FP8 (fp8_quant.hip, fp8_ffn.hip)
+hipError_t launch_fp8_quantize(const void* x, int x_f32, int T, int n, int64_t stride, uint8_t* codes, float* scales,
+                               hipStream_t s);
+hipError_t launch_fp8_matmul(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, int M, int N, int K,
+                             int64_t lda, int64_t ldw, int out_f32, void* y, int64_t ldy, hipStream_t s);
+size_t ffn_a8_ws_bytes(int T, int k, int E, int H, int F);
+hipError_t launch_ffn_a8(const FfnArgs& f, void* ws, hipStream_t s);
+
 // ---- combine (combine.hip); pair_to_row == nullptr: row of pair p is p
 hipError_t launch_combine(const void* rows, int rows_f32, const int32_t* pair_to_row,
                           const float* gate, int T, int k, int H, const uint16_t* shared,

@@ -1,0 +1,304 @@
+"""FP8 quantisation, block-scaled products and W8A8 experts on the GPU against their 64-bit forms (a8_ref)."""
+import pytest
+import torch
+
+import sparse_moe_expert_router_amd as moe
+from tests import a8_ref as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+# ------------------------------------------------------------------ quantiser
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,n", [(1, 16), (1, 128), (3, 144), (7, 688), (64, 2560), (1025, 640), (2, 8208)])
+def test_quantize_is_bit_exact(T, n, dtype):
+    x = (torch.randn((T, n), generator=_gen(T * n)) * torch.exp2(torch.randint(-20, 20, (T, 1), generator=_gen(1)).float())).to(dtype)
+    x[0, :16] = 0
+    codes, s = moe.fp8_quantize(x.to(DEV))
+    rc, rs = R.quantize(x.double())
+    assert torch.equal(s.cpu().double(), rs)
+    assert torch.equal(codes.cpu(), rc)
+
+
+def test_quantize_every_bf16_magnitude_and_ties():
+    # each row: one group whose largest value is a bf16 number, with every bf16 below it in two binades and far below
+    amax = torch.arange(0x3F80, 0x4000, dtype=torch.int16).view(torch.bfloat16).double()     # [1, 2)
+    below = torch.cat([torch.arange(0x3C00, 0x3F80, dtype=torch.int16).view(torch.bfloat16).double(), torch.zeros(1).double()])
+    cols = below.view(-1)
+    n = 127
+    rows = []
+    for i in range(0, cols.numel(), n):
+        part = torch.nn.functional.pad(cols[i:i + n], (0, n - cols[i:i + n].numel()))
+        rows.append(torch.cat([amax[:, None], part[None].expand(amax.numel(), n)], 1))
+    x = torch.cat(rows).bfloat16()
+    x[1::2] = -x[1::2]
+    codes, s = moe.fp8_quantize(x.to(DEV))
+    rc, rs = R.quantize(x.double())
+    assert torch.equal(s.cpu().double(), rs) and torch.equal(codes.cpu(), rc)
+
+
+def test_quantize_special_values():
+    x = torch.zeros((6, 256))
+    x[1, 0] = 1e-40                      # below the smallest scale's range: codes of a tiny group
+    x[2, 5] = float("inf")
+    x[3, 200] = float("nan")
+    x[4, 0], x[4, 1] = 3e38, -3e38
+    x[5, :] = -0.0
+    codes, s = moe.fp8_quantize(x.to(DEV))
+    codes, s = codes.cpu(), s.cpu()
+    v = R.decode(codes) * R.spread(s.double(), 256)
+    assert (codes[0] == 0).all() and (s[0] == 2.0 ** -126).all()
+    assert torch.isfinite(v[[0, 1, 4, 5]]).all() and (v[1].abs() <= 1e-38).all()
+    assert torch.isnan(v[2, :128]).all() and (v[2, 128:] == 0).all()
+    assert (v[3, :128] == 0).all() and torch.isnan(v[3, 128:]).all()
+    assert v[4, 0] > 2.9e38 and v[4, 1] < -2.9e38
+
+
+def test_quantize_strided_rows_and_empty():
+    wide = torch.randn((9, 512), generator=_gen(3)).bfloat16().to(DEV)
+    x = wide[:, 64:64 + 160]
+    codes, s = moe.fp8_quantize(x)
+    rc, rs = R.quantize(x.cpu().double())
+    assert torch.equal(codes.cpu(), rc) and torch.equal(s.cpu().double(), rs)
+    c0, s0 = moe.fp8_quantize(torch.empty((0, 128), dtype=torch.bfloat16, device=DEV))
+    assert c0.shape == (0, 128) and s0.shape == (0, 1)
+
+
+# ------------------------------------------------------------------ product
+
+def _codes(shape, g):
+    c = torch.randint(0, 256, shape, generator=g, dtype=torch.int64)
+    return torch.where((c & 127) == 127, c - 1, c).to(torch.uint8)      # every finite code
+
+
+def _check_product(y, a, sa, w, sw):
+    a, sa, w, sw = (t.to(DEV) for t in (a, sa, w, sw))
+    K = a.shape[1]
+    av = R.decode(a) * R.spread(sa.double(), K)
+    wv = R.weights(w, sw)
+    ref, bound = R.product(av, wv, K, y.dtype == torch.float32)
+    half = torch.finfo(y.dtype).eps / 2
+    err = (y.double() - ref).abs()
+    lim = bound + half * (ref.abs() + bound)
+    assert (err <= lim).all(), f"largest excess {(err - lim).max():.3e} at {(err - lim).argmax()}"
+    # signs are random here: the errors of the outputs together (fp32: 128 2^-23 of each, as the products)
+    assert err.norm() <= (half + (2.0 ** -16 if y.dtype == torch.float32 else 2.0 ** -10)) * ref.norm()
+
+
+SHAPES = [(1, 16, 16), (1, 1, 128), (1, 2560, 2560), (5, 33, 144), (16, 128, 640), (17, 130, 1296), (31, 257, 128), (33, 1000, 272),
+          (77, 1000, 1296), (128, 256, 256), (129, 300, 384), (200, 640, 2560), (256, 256, 128), (257, 513, 1040), (300, 1280, 512),
+          (513, 129, 2064), (1000, 384, 640), (2048, 264, 1152)]
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_matmul(M, N, K, out):
+    g = _gen(M + 3 * N + 7 * K)
+    a, w = _codes((M, K), g), _codes((N, K), g)
+    kb = -(-K // 128)
+    sa = torch.rand((M, kb), generator=g) + 0.1
+    sw = torch.rand((-(-N // 128), kb), generator=g) * 0.01 - 0.005
+    y = torch.empty((M, N), dtype=out, device=DEV)
+    moe.fp8_matmul(a.to(DEV), sa.to(DEV), w.to(DEV), sw.to(DEV), y=y)
+    _check_product(y, a, sa, w, sw)
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 50, 144), (40, 260, 272), (300, 600, 400)])
+def test_matmul_strided_and_untouched_surroundings(M, N, K):
+    g = _gen(M)
+    A, W = _codes((M + 2, K + 64), g), _codes((N, K + 32), g)
+    # what lies between the rows is NaN: it must not be used
+    A[:, :16], A[:, 16 + K:], W[:, K:] = 127, 127, 127
+    a, w = A.to(DEV)[1:M + 1, 16:16 + K], W.to(DEV)[:, :K]
+    kb = -(-K // 128)
+    sa, sw = torch.rand((M, kb), generator=g), torch.rand((-(-N // 128), kb), generator=g)
+    big = torch.full((M + 2, N + 13), 7.0, dtype=torch.bfloat16, device=DEV)
+    y = big[1:M + 1, 3:3 + N]
+    moe.fp8_matmul(a, sa.to(DEV), w, sw.to(DEV), y=y)
+    _check_product(y, a.cpu(), sa, w.cpu(), sw)
+    assert (big[0] == 7).all() and (big[-1] == 7).all() and (big[:, :3] == 7).all() and (big[:, 3 + N:] == 7).all()
+
+
+@pytest.mark.parametrize("M", [2, 40, 600])
+def test_matmul_nan_stays_in_its_row_and_column(M):
+    N, K = 400, 384
+    g = _gen(5)
+    a, w = _codes((M, K), g), _codes((N, K), g)
+    a[1, 200], w[17, 3] = 127, 255
+    sa, sw = torch.rand((M, 3), generator=g), torch.rand((4, 3), generator=g)
+    y = moe.fp8_matmul(a.to(DEV), sa.to(DEV), w.to(DEV), sw.to(DEV), out_dtype=moe.OUT_F32).cpu()
+    bad = torch.zeros((M, N), dtype=torch.bool)
+    bad[1], bad[:, 17] = True, True
+    assert torch.equal(torch.isnan(y), bad)
+
+
+def test_matmul_no_rows():
+    y = moe.fp8_matmul(torch.empty((0, 256), dtype=torch.uint8, device=DEV), torch.empty((0, 2), device=DEV),
+                       torch.zeros((64, 256), dtype=torch.uint8, device=DEV), torch.ones((1, 2), device=DEV))
+    assert y.shape == (0, 64)
+
+
+# ------------------------------------------------------------------ experts
+
+def _bank(E, H, F, seed):
+    g = _gen(seed)
+    out = {"fmt": "fp8"}
+    for n, o, i in (("gate", F, H), ("up", F, H), ("down", H, F)):
+        out[n + "_codes"] = _codes((E, o, i), g)
+        out[n + "_bscales"] = (torch.rand((E, o // 128, i // 128), generator=g) + 0.5) * 2e-4
+    return out
+
+
+def _gpu(bank):
+    return {k: v if isinstance(v, str) else v.to(DEV) for k, v in bank.items()}
+
+
+def _check_experts(rows, x, k, bank, off, sp):
+    x, sp = x.to(DEV), sp.to(DEV)
+    codes, s = R.quantize(x.double())
+    xq = R.decode(codes) * R.spread(s, x.shape[1])
+    half = torch.finfo(rows.dtype).eps / 2
+    got = rows.double()
+    total = 0
+    for e in range(off.numel() - 1):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if lo == hi:
+            continue
+        tok = sp[lo:hi].long() // k
+        w = [R.weights(bank[n + "_codes"][e].to(DEV), bank[n + "_bscales"][e].to(DEV)) for n in ("gate", "up", "down")]
+        ref, bound = R.expert_a8(xq[tok], *w)
+        err = (got[lo:hi] - ref).abs()
+        lim = bound + half * (ref.abs() + bound)
+        assert (err <= lim).all(), f"expert {e}: largest excess {(err - lim).max():.3e}"
+        total = total + torch.stack([(got[lo:hi] - ref).square().sum(), ref.square().sum()])
+    # The bound allows for every near tie of h at once.  Together: h is off by about 2^-14 (the cut products of
+    # full-range random codes), so a share of 2 * 16 * 2^-14 = 2^-9 of its codes, the steps of E4M3 being 2^-3
+    # to 2^-4 apart, is a step off: sqrt(2^-9) 2^-3.5 = 2^-8 of the rows; twice that.  An average over codes a
+    # step off: of 768 codes (six rows) 1.5 are expected, and one of them alone can be 2^-3 of the largest term
+    # of a row, so it is held only where 2^16 codes (128 expected) make it one.
+    if got.shape[0] * w[0].shape[0] >= 1 << 16:
+        assert total[0].sqrt() <= (half + 2.0 ** -7) * total[1].sqrt()
+
+
+def _sorted(idx, E):
+    flat = idx.reshape(-1)
+    sp = torch.sort(flat, stable=True).indices.int()
+    off = torch.cat([torch.zeros(1, dtype=torch.int64), torch.bincount(flat, minlength=E).cumsum(0)]).int()
+    return off, sp
+
+
+FFN = [(1, 256, 128, 4, 2), (5, 128, 256, 16, 3), (16, 384, 128, 8, 2), (40, 256, 384, 3, 2), (70, 512, 128, 2, 1), (300, 256, 256, 4, 2),
+       (700, 384, 128, 3, 3), (1100, 128, 128, 2, 2)]
+
+
+@pytest.mark.parametrize("out", [moe.OUT_BF16, moe.OUT_F32])
+@pytest.mark.parametrize("T,H,F,E,k", FFN)
+def test_experts(T, H, F, E, k, out):
+    g = _gen(T + H)
+    x = torch.randn((T, H), generator=g).bfloat16()
+    bank = _bank(E, H, F, 9)
+    idx = torch.rand((T, E), generator=g).topk(k, 1).indices
+    off, sp = _sorted(idx, E)
+    rows = moe.grouped_ffn_a8(x.to(DEV), k, _gpu(bank), off.to(DEV), sp.to(DEV), out_dtype=out)
+    _check_experts(rows, x, k, bank, off, sp)
+
+
+@pytest.mark.parametrize("T", [64, 700])
+def test_experts_all_tokens_on_one_and_empty_experts(T):
+    H, F, E = 256, 128, 9
+    x = torch.randn((T, H), generator=_gen(2)).bfloat16()
+    bank = _bank(E, H, F, 3)
+    off, sp = _sorted(torch.full((T, 1), 4), E)
+    rows = moe.grouped_ffn_a8(x.to(DEV), 1, _gpu(bank), off.to(DEV), sp.to(DEV))
+    _check_experts(rows, x, 1, bank, off, sp)
+
+
+@pytest.mark.parametrize("T", [1, 20, 513])
+def test_experts_identity(T):
+    x = torch.randn((T, 384), generator=_gen(4)).bfloat16()
+    bank = _bank(1, 384, 256, 5)
+    rows = moe.grouped_ffn_a8(x.to(DEV), 1, _gpu(bank))
+    _check_experts(rows, x, 1, bank, torch.tensor([0, T]), torch.arange(T).int())
+
+
+@pytest.mark.parametrize("T", [6, 400])
+def test_experts_nan_row_stays_alone(T):
+    H, F, E, k = 256, 128, 4, 2
+    x = torch.randn((T, H), generator=_gen(6)).bfloat16()
+    x[3, 17], x[5, 0] = float("inf"), float("nan")
+    bank = _bank(E, H, F, 3)
+    idx = torch.rand((T, E), generator=_gen(7)).topk(k, 1).indices
+    off, sp = _sorted(idx, E)
+    rows = moe.grouped_ffn_a8(x.to(DEV), k, _gpu(bank), off.to(DEV), sp.to(DEV)).cpu()
+    tok = sp.long() // k
+    bad = (tok == 3) | (tok == 5)
+    assert torch.isnan(rows[bad]).all() and torch.isfinite(rows[~bad]).all()
+
+
+def test_experts_zero_rows_give_zero():
+    bank = _bank(2, 128, 128, 1)
+    off, sp = _sorted(torch.tensor([[0], [1], [1]]), 2)
+    rows = moe.grouped_ffn_a8(torch.zeros((3, 128), dtype=torch.bfloat16, device=DEV), 1, _gpu(bank), off.to(DEV), sp.to(DEV))
+    assert (rows == 0).all()
+
+
+@pytest.mark.parametrize("T", [8, 300])
+def test_route_experts_combine_together(T):
+    """The layer of separate calls with W8A8 experts: route, permute, experts, combine."""
+    H, F, E, k = 512, 256, 32, 4
+    g = _gen(T)
+    x = torch.randn((T, H), generator=g).bfloat16()
+    wr = (torch.randn((E, H), generator=g) * 0.05).bfloat16()
+    bank = _bank(E, H, F, 21)
+    gb = _gpu(bank)
+    idx, tl, gate, off, sp, p2r = moe.route_permute(x.to(DEV), wr.to(DEV), k)
+    rows = moe.grouped_ffn_a8(x.to(DEV), k, gb, off, sp)
+    y = moe.combine(rows, p2r, gate)
+    _check_experts(rows, x, k, bank, off.cpu(), sp.cpu())
+    ref = (rows.cpu().double()[p2r.cpu().long()].view(T, k, H) * gate.cpu().double()[..., None]).sum(1)
+    bound = (rows.cpu().double()[p2r.cpu().long()].view(T, k, H) * gate.cpu().double()[..., None]).abs().sum(1) * (k + 1) * 2.0 ** -24
+    assert ((y.cpu().double() - ref).abs() <= bound + 2.0 ** -8 * (ref.abs() + bound)).all()
+
+
+@pytest.mark.parametrize("T,E", [(16, 16), (600, 2)])
+def test_replays_of_a_captured_call(T, E):
+    H, F, k = 256, 128, 2
+    bank = _gpu(_bank(E, H, F, 2))
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device=DEV)
+    off, sp = _sorted(torch.rand((T, E), generator=_gen(8)).topk(k, 1).indices, E)
+    off, sp = off.to(DEV), sp.to(DEV)
+    ws = moe.Workspace(x.device)
+    rows = torch.empty((T * k, H), dtype=torch.bfloat16, device=DEV)
+    moe.grouped_ffn_a8(x, k, bank, off, sp, ws=ws, rows=rows)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.grouped_ffn_a8(x, k, bank, off, sp, ws=ws, rows=rows)
+    for i in range(4):
+        x.copy_(torch.randn((T, H), generator=_gen(i)).bfloat16())
+        graph.replay()
+        torch.cuda.synchronize()
+        got = rows.clone()
+        want = moe.grouped_ffn_a8(x, k, bank, off, sp)
+        assert torch.equal(got, want)
+
+
+def test_on_a_side_stream():
+    x = torch.randn((33, 256), generator=_gen(1)).bfloat16().to(DEV)
+    bank = _gpu(_bank(1, 256, 128, 2))
+    want = moe.grouped_ffn_a8(x, 1, bank)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c, sc = moe.fp8_quantize(x)
+        got = moe.grouped_ffn_a8(x, 1, bank, ws=moe.Workspace(x.device))
+    s.synchronize()
+    assert torch.equal(got, want)
+    assert torch.equal(c, moe.fp8_quantize(x)[0])
