@@ -100,4 +100,27 @@ __device__ __forceinline__ float buf_load_f32(__amdgpu_buffer_rsrc_t r, uint32_t
     return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, (int)voff, (int)soff, 0));
 }
 
+// Four neighbouring outputs of a row, rounded once.
+__device__ __forceinline__ void fp8_store4(void* row, int out_f32, int n, int N, bool vec, f32x4_t v) {
+    if (out_f32) {
+        float* o = static_cast<float*>(row) + n;
+        if (vec) {
+            *reinterpret_cast<f32x4_t*>(o) = v;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < N) o[j] = v[j];
+        }
+    } else {
+        uint16_t* o = static_cast<uint16_t*>(row) + n;
+        if (vec) {
+            *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < N) o[j] = (uint16_t)f32_to_bf16_bits(v[j]);
+        }
+    }
+}
+
 }  // namespace moe

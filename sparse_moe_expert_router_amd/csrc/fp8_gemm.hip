@@ -1,0 +1,347 @@
+// W8A8 products for many rows: tiles of 32 TF rows x 256 outputs on gfx950's
+// 16 x 16 x 128 FP8 MFMA (fp32 outputs: the bf16 MFMA on widened codes, see
+// mfma_fp8), scales per 128 inputs applied in fp32 after every block:
+//   acc[n][m] += (sa[m][kb] * sw[n / 128][kb]) * sum_{i in kb} w[n][i] a[m][i].
+// Three uses: a dense product, the gate/up pass of the grouped experts (a
+// tile holds 128 gate and the same 128 up columns; SwiGLU and quantisation in
+// the epilogue) and their down pass.
+//
+// A workgroup is 8 waves, 4 along the outputs x 2 along the rows; a wave owns
+// 64 outputs x 16 TF rows.  One step is one block of 128 inputs.
+//  - Rows go from memory straight into LDS (16-byte buffer loads to LDS), up
+//    to three steps ahead, 128 bytes a row, 16-byte pieces XOR-swizzled.  The
+//    4 waves along the outputs share them.
+//  - Weights go straight into registers, kW steps ahead: each byte is
+//    used by two waves only, and through LDS its traffic (64 KB written, 192
+//    KB read per step of a 256 x 256 tile) would take as long as the MFMAs.
+//  - Row scales are staged in LDS eight steps at a time.
+// The weights are the MFMA's row operand: a lane ends up with 4 neighbouring
+// outputs of one row, and one row scale per 16 rows covers all 4.
+#include "fp8.h"
+#include "ffn_internal.h"
+#include "fp8_internal.h"
+
+namespace moe {
+
+enum { G_DENSE = 0, G_GATEUP = 1, G_DOWN = 2 };
+
+constexpr int kGThreads = 512, kGWaves = 8;
+constexpr int kGN = 256;       // outputs of a tile (gate/up: 128 of each)
+constexpr int kGStages = 4;    // LDS stages of rows
+
+// LDS of a tile of BT rows, in bytes.
+template <int TF>
+struct GemmLds {
+    static constexpr int BT = 32 * TF;
+    static constexpr int A = BT * 128;                   // one stage of rows
+    static constexpr int SA = kGStages * A;              // row scales [2][8][BT]
+    static constexpr int SW = SA + 2 * 8 * BT * 4;       // weight scales [2][2][8]
+    static constexpr int ROW = SW + 2 * 2 * 8 * 4;       // byte offsets of the rows' scales [BT]
+    static constexpr int AMAX = ROW + BT * 4;            // gate/up: group maxima [4][BT]
+    static constexpr int TOTAL = AMAX + 4 * BT * 4;
+};
+
+// 16-byte piece c of row r sits at piece c ^ g_swz(r): 8 consecutive rows, and
+// the even (or odd) rows of 16, take 8 different pieces.
+__device__ __forceinline__ int g_swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+template <int n>
+__device__ __forceinline__ void wait_vm() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
+}
+
+template <int TF, int MODE, bool kExact, int kW>
+__global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d, const Fp8Ffn p) {
+    using L = GemmLds<TF>;
+    constexpr int BT = L::BT;
+    constexpr int NA = BT / 64;   // row loads of a wave per step
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wv & 3, wt = wv >> 2, g = lane >> 4, l16 = lane & 15;
+
+    // ---- the tile: rows [m0, m1), outputs from n0
+    int e = 0, m0, m1, n0;
+    if (MODE == G_DENSE) {
+        const int mt = (d.M + BT - 1) / BT, nt = (d.N + kGN - 1) / kGN;
+        const int l = xcd_remap(blockIdx.x, mt * nt);
+        if (l < 0) return;
+        // groups of 4 row tiles, all output tiles of a group in turn
+        const int grp = l / (4 * nt), rem = l - grp * 4 * nt, gm = min(4, mt - 4 * grp);
+        m0 = (4 * grp + rem % gm) * BT;
+        n0 = rem / gm * kGN;
+        m1 = min(m0 + BT, d.M);
+    } else {
+        const int nt = MODE == G_GATEUP ? p.F / 128 : (p.H + kGN - 1) / kGN;
+        const int l = xcd_remap(blockIdx.x, p.tiles[0] * nt);
+        if (l < 0) return;
+        const int i = l / nt;
+        n0 = (l - i * nt) * (MODE == G_GATEUP ? 128 : kGN);
+        e = p.tiles[1 + 3 * i];
+        m0 = p.tiles[2 + 3 * i];
+        m1 = min(p.tiles[3 + 3 * i], p.P);
+        if (m0 < 0 || m0 >= m1) return;
+    }
+    const int K = MODE == G_DENSE ? d.K : MODE == G_GATEUP ? p.H : p.F;
+    const int KB = (K + 127) / 128;
+    const int N = MODE == G_DENSE ? d.N : MODE == G_GATEUP ? p.F : p.H;
+    const int mr = m1 - m0;
+    const bool tail = MODE == G_DENSE && K % 128 != 0;
+
+    // ---- buffers
+    const uint32_t lda = MODE == G_DENSE ? (uint32_t)d.lda : (uint32_t)K;
+    const uint32_t ldw = MODE == G_DENSE ? (uint32_t)d.ldw : (uint32_t)K;
+    const __amdgpu_buffer_rsrc_t ra =
+        MODE == G_DENSE    ? fp8_rsrc(d.a + (size_t)m0 * lda, (uint32_t)(min(mr, BT) - 1) * lda + (uint32_t)K)
+        : MODE == G_GATEUP ? fp8_rsrc(p.xq, (uint32_t)p.T * (uint32_t)K)
+                           : fp8_rsrc(p.hq + (size_t)m0 * K, (uint32_t)mr * (uint32_t)K);
+    const __amdgpu_buffer_rsrc_t rs =
+        MODE == G_DENSE    ? fp8_rsrc(d.sa + (size_t)m0 * KB, (uint32_t)min(mr, BT) * (uint32_t)KB * 4u)
+        : MODE == G_GATEUP ? fp8_rsrc(p.xs, (uint32_t)p.T * (uint32_t)KB * 4u)
+                           : fp8_rsrc(p.hs + (size_t)m0 * KB, (uint32_t)mr * (uint32_t)KB * 4u);
+    const uint32_t wrows = MODE == G_GATEUP ? 128u : (uint32_t)min(N - n0, kGN);
+    const uint32_t wbytes = (wrows - 1) * ldw + (uint32_t)K;
+    const size_t wbase = MODE == G_DENSE ? (size_t)n0 * ldw : ((size_t)e * N + n0) * K;
+    const __amdgpu_buffer_rsrc_t rw0 = fp8_rsrc((MODE == G_DENSE ? d.w : MODE == G_GATEUP ? p.gate : p.down) + wbase, wbytes);
+    const __amdgpu_buffer_rsrc_t rw1 = MODE == G_GATEUP ? fp8_rsrc(p.up + wbase, wbytes) : rw0;
+    // two rows of weight scales: the gate's and the up's, or those of the tile's two blocks of 128 outputs
+    const int NB = (N + 127) / 128;
+    const size_t sbase = ((size_t)e * NB + n0 / 128) * KB;
+    const uint32_t sbytes = (uint32_t)KB * 4u;
+    const __amdgpu_buffer_rsrc_t rsw0 =
+        fp8_rsrc((MODE == G_DENSE ? d.sw : MODE == G_GATEUP ? p.sgate : p.sdown) + sbase, sbytes);
+    const __amdgpu_buffer_rsrc_t rsw1 =
+        MODE == G_GATEUP ? fp8_rsrc(p.sup + sbase, sbytes)
+                         : fp8_rsrc((MODE == G_DENSE ? d.sw : p.sdown) + sbase + (n0 / 128 + 1 < NB ? KB : 0), sbytes);
+
+    // ---- rows: load i of wave wv fills rows 8 (8 i + wv) .. +7 of a stage, lane
+    // = 8 (row % 8) + piece position; the piece read is position ^ g_swz(row)
+    auto source_row = [&](int r) {  // row of the source matrix (relative to its base) behind row r of the tile
+        if (MODE == G_DENSE) return (uint32_t)r;
+        const int q = min(r, mr - 1);
+        if (MODE == G_DOWN) return (uint32_t)q;
+        return (uint32_t)(p.sorted_pair ? min(max(p.sorted_pair[m0 + q] / p.k, 0), p.T - 1) : m0 + q);
+    };
+    uint32_t aoff[NA];
+    int apiece = 0;
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+        const int r = 8 * (8 * i + wv) + (lane >> 3);
+        apiece = (lane & 7) ^ g_swz(r);  // the same for every i: rows 64 apart
+        aoff[i] = source_row(r) * lda + 16u * (uint32_t)apiece;
+    }
+    uint32_t* rowoff = reinterpret_cast<uint32_t*>(smem + L::ROW);
+    for (int r = tid; r < BT; r += kGThreads)
+        rowoff[r] = (MODE == G_DENSE && r >= mr) ? kOob : source_row(r) * (uint32_t)KB * 4u;
+
+    // ---- weights: fragment f of a wave is 16 outputs, lane output l16, pieces g and g + 4
+    uint32_t woff[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+        const int r = MODE == G_GATEUP ? 32 * wn + 16 * (f & 1) + l16 : 64 * wn + 16 * f + l16;
+        woff[f] = (uint32_t)r * ldw + 16u * (uint32_t)g;
+    }
+    const int rest = K - (KB - 1) * 128;  // inputs of the last block
+
+    i32x8_t w[kW + 1][4];
+    auto load_w = [&](i32x8_t (&dst)[4], int j) {
+        j = min(j, KB - 1);
+        const bool cut = tail && j == KB - 1;
+        const bool z0 = cut && 16 * g >= rest, z1 = cut && 16 * g + 64 >= rest;
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            const __amdgpu_buffer_rsrc_t r = f >= 2 ? rw1 : rw0;
+            dst[f] = join8(buf_load16(r, z0 ? kOob : woff[f], (uint32_t)j * 128u),
+                           buf_load16(r, z1 ? kOob : woff[f] + 64u, (uint32_t)j * 128u));
+        }
+    };
+    auto load_a = [&](int j) {
+        uint8_t* st = smem + (j % kGStages) * L::A;
+        j = min(j, KB - 1);
+        const bool z = tail && j == KB - 1 && 16 * apiece >= rest;
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + (8 * i + wv) * 1024), 16,
+                                                     (int)(z ? kOob : aoff[i]), j * 128, 0, 0);
+    };
+    // scales of blocks 8 c .. 8 c + 7: wave v loads block 8 c + v of every row
+    auto load_s = [&](int c) {
+        const int kb = min(8 * c + wv, KB - 1);
+        float* sa = reinterpret_cast<float*>(smem + L::SA) + (c & 1) * 8 * BT + wv * BT;
+#pragma unroll
+        for (int t = 0; t < NA; ++t)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(sa + 64 * t), 4, (int)rowoff[64 * t + lane], kb * 4,
+                                                     0, 0);
+        if (wv < 2 && lane < 8) {
+            float* sw = reinterpret_cast<float*>(smem + L::SW) + (c & 1) * 16 + wv * 8;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(wv ? rsw1 : rsw0, (lds_void*)sw, 4, min(8 * c + lane, KB - 1) * 4, 0,
+                                                     0, 0);
+        }
+    };
+
+    f32x4_t acc[4][TF];
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+        for (int t = 0; t < TF; ++t) acc[f][t] = f32x4_t{};
+
+    __syncthreads();  // rowoff
+    load_s(0);
+    load_a(0);
+    load_a(1);
+    if (kW > 1) load_w(w[0], 0);
+    if (kW > 1) load_w(w[1], 1);
+    if (kW == 1) load_w(w[0], 0);
+    load_a(2);
+
+    // LDS byte offset of the lane's pieces of row 16 t + l16 of the wave's rows
+    const int ar = (wt * 16 * TF + l16) * 128;
+    const int p0 = 16 * (g ^ g_swz(l16)), p1 = 16 * ((g + 4) ^ g_swz(l16));
+
+    auto step = [&](int j, i32x8_t (&cur)[4], i32x8_t (&next)[4]) {
+        // everything up to the weights of step j has landed: rows of step j + 1,
+        // and the scales; then no wave still reads the stage refilled below
+        wait_vm<NA + (kW - 1) * 8>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if ((j & 7) == 0 && j + 8 < KB) load_s(j / 8 + 1);
+        load_w(next, j + kW);
+        load_a(j + 3);
+        const uint8_t* st = smem + (j % kGStages) * L::A + ar;
+        const float* sa = reinterpret_cast<const float*>(smem + L::SA) + ((j >> 3) & 1) * 8 * BT + (j & 7) * BT +
+                          wt * 16 * TF + l16;
+        const float* swp = reinterpret_cast<const float*>(smem + L::SW) + ((j >> 3) & 1) * 16 + (j & 7);
+        const float s0 = MODE == G_GATEUP ? swp[0] : swp[wn >= 2 ? 8 : 0];
+        const float s1 = MODE == G_GATEUP ? swp[8] : s0;
+#pragma unroll
+        for (int t = 0; t < TF; ++t) {
+            const i32x8_t a = join8(*reinterpret_cast<const i32x4_t*>(st + t * 2048 + p0),
+                                    *reinterpret_cast<const i32x4_t*>(st + t * 2048 + p1));
+            const float sr = sa[16 * t];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const f32x4_t v = mfma_fp8<kExact>(cur[f], a);
+                const float c = sr * (f >= 2 ? s1 : s0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(c, v[i], acc[f][t][i]);
+            }
+        }
+        asm volatile("" ::: "memory");
+    };
+    int j = 0;
+    if constexpr (kW == 1) {
+        for (; j + 1 < KB; j += 2) {
+            step(j, w[0], w[1]);
+            step(j + 1, w[1], w[0]);
+        }
+        if (j < KB) step(j, w[0], w[1]);
+    } else {
+        for (; j + 2 < KB; j += 3) {
+            step(j, w[0], w[2]);
+            step(j + 1, w[1], w[0]);
+            step(j + 2, w[2], w[1]);
+        }
+        if (j < KB) step(j, w[0], w[2]);
+        if (j + 1 < KB) step(j + 1, w[1], w[0]);
+    }
+    wait_vm<0>();
+    __syncthreads();  // no load still writes the stages, no wave still reads them
+
+    if constexpr (MODE == G_GATEUP) {
+        // h = silu(gate) up in fp32; its largest magnitude per row over the
+        // group's 128 columns: lanes of a row, then the 4 waves
+        uint32_t* amax = reinterpret_cast<uint32_t*>(smem + L::AMAX);
+#pragma unroll
+        for (int t = 0; t < TF; ++t) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float h = silu(acc[f][t][i]) * acc[f + 2][t][i];
+                    acc[f][t][i] = h;
+                    m = max(m, abs_bits(h));
+                }
+            m = max(m, (uint32_t)__shfl_xor((int)m, 16, kWave));
+            m = max(m, (uint32_t)__shfl_xor((int)m, 32, kWave));
+            if (g == 0) amax[wn * BT + wt * 16 * TF + 16 * t + l16] = m;
+        }
+        __syncthreads();
+        // codes [BT][128] through LDS (rows padded to 144 bytes), then 16 bytes a lane
+        constexpr int LD = 144;
+        static_assert(BT * LD <= kGStages * L::A, "codes fit the row stages");
+#pragma unroll
+        for (int t = 0; t < TF; ++t) {
+            const int r = wt * 16 * TF + 16 * t + l16;
+            const uint32_t m = max(max(amax[r], amax[BT + r]), max(amax[2 * BT + r], amax[3 * BT + r]));
+            const float s = fp8_scale(m);
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+                *reinterpret_cast<uint32_t*>(smem + r * LD + 32 * wn + 16 * f + 4 * g) =
+                    fp8_pack4(acc[f][t][0], acc[f][t][1], acc[f][t][2], acc[f][t][3], s);
+            if (wn == 0 && g == 0 && r < mr) p.hs[(size_t)(m0 + r) * NB + n0 / 128] = s;
+        }
+        __syncthreads();
+        for (int q = tid; q < mr * 8; q += kGThreads) {
+            const int r = q >> 3, c = q & 7;
+            *reinterpret_cast<uint4*>(p.hq + (size_t)(m0 + r) * p.F + n0 + 16 * c) =
+                *reinterpret_cast<const uint4*>(smem + r * LD + 16 * c);
+        }
+    } else {
+        const int out_f32 = MODE == G_DENSE ? d.out_f32 : p.out_f32;
+        const bool vec = MODE == G_DENSE ? d.vec : true;
+        char* y = static_cast<char*>(MODE == G_DENSE ? d.y : p.rows);
+        const int64_t ldy = MODE == G_DENSE ? d.ldy : (int64_t)p.H;
+#pragma unroll
+        for (int t = 0; t < TF; ++t) {
+            const int r = wt * 16 * TF + 16 * t + l16;
+            if (r >= mr) continue;
+            char* row = y + (m0 + r) * ldy * (out_f32 ? 4 : 2);
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const int n = n0 + 64 * wn + 16 * f + 4 * g;
+                if (n < N) fp8_store4(row, out_f32, n, N, vec && n + 3 < N, acc[f][t]);
+            }
+        }
+    }
+}
+
+template <int TF, int MODE, bool kExact, int kW>
+static hipError_t launch_one(const Fp8Dense& d, const Fp8Ffn& p, long tiles, hipStream_t s) {
+    const long grid = (tiles + kXcd - 1) / kXcd * kXcd;
+    const void* fn = reinterpret_cast<const void*>(fp8_gemm_kernel<TF, MODE, kExact, kW>);
+    const hipError_t err = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, GemmLds<TF>::TOTAL);
+    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL((fp8_gemm_kernel<TF, MODE, kExact, kW>), dim3((unsigned)grid), dim3(kGThreads),
+                       GemmLds<TF>::TOTAL, s, d, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_fp8_gemm(const Fp8Dense& d, int bt, hipStream_t s) {
+    const long tiles = (long)((d.M + bt - 1) / bt) * ((d.N + kGN - 1) / kGN);
+    const Fp8Ffn p{};
+    if (d.out_f32) return launch_one<4, G_DENSE, true, 1>(d, p, (long)((d.M + 127) / 128) * ((d.N + kGN - 1) / kGN), s);
+    if (bt == 256) return launch_one<8, G_DENSE, false, 1>(d, p, tiles, s);
+    if (bt == 128) return launch_one<4, G_DENSE, false, 2>(d, p, tiles, s);
+    return launch_one<2, G_DENSE, false, 2>(d, p, tiles, s);
+}
+
+hipError_t launch_fp8_gemm_gateup(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s) {
+    const Fp8Dense d{};
+    const long tiles = max_tiles * (p.F / 128);
+    if (bt == 256) return launch_one<8, G_GATEUP, false, 1>(d, p, tiles, s);
+    if (bt == 128) return launch_one<4, G_GATEUP, false, 2>(d, p, tiles, s);
+    return launch_one<2, G_GATEUP, false, 2>(d, p, tiles, s);
+}
+
+hipError_t launch_fp8_gemm_down(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s) {
+    const Fp8Dense d{};
+    const long tiles = max_tiles * ((p.H + kGN - 1) / kGN);
+    if (bt == 256) return launch_one<8, G_DOWN, false, 1>(d, p, tiles, s);
+    if (bt == 128) return launch_one<4, G_DOWN, false, 2>(d, p, tiles, s);
+    return launch_one<2, G_DOWN, false, 2>(d, p, tiles, s);
+}
+
+}  // namespace moe

@@ -1,4 +1,4 @@
-// Internal interface of the W8A8 kernels (fp8_skinny.hip, fp8_ffn.hip).
+// Internal interface of the W8A8 kernels (fp8_skinny.hip, fp8_gemm.hip, fp8_ffn.hip).
 #pragma once
 
 #include "kernels.h"
@@ -23,7 +23,7 @@ struct Fp8Ffn {
     int T, k, H, F, E, P;
     const int32_t* offsets;      // [E+1] or nullptr (identity: E == 1)
     const int32_t* sorted_pair;  // [P] or nullptr
-    const int32_t* tiles;        // tiles[0] = count, then (expert, first row) pairs
+    const int32_t* tiles;        // tiles[0] = count, then (expert, first row, end row) triples
     const uint8_t *gate, *up, *down;
     const float *sgate, *sup, *sdown;
     const uint8_t* xq;           // [T][H]
@@ -36,5 +36,10 @@ struct Fp8Ffn {
 
 hipError_t launch_fp8_skinny(const Fp8Dense& p, hipStream_t s);
 hipError_t launch_fp8_skinny_ffn(const Fp8Ffn& p, int max_tiles, hipStream_t s);
+
+// Tiles of bt rows (256, 128 or 64) x 256 outputs.
+hipError_t launch_fp8_gemm(const Fp8Dense& d, int bt, hipStream_t s);
+hipError_t launch_fp8_gemm_gateup(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s);
+hipError_t launch_fp8_gemm_down(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s);
 
 }  // namespace moe

@@ -65,29 +65,6 @@ __device__ __forceinline__ void fp8_wave_product(f32x4_t (&acc)[NW][TF], const _
     }
 }
 
-// Four neighbouring outputs of a row, rounded once.
-__device__ __forceinline__ void store4(void* row, int out_f32, int n, int N, bool vec, f32x4_t v) {
-    if (out_f32) {
-        float* o = static_cast<float*>(row) + n;
-        if (vec) {
-            *reinterpret_cast<f32x4_t*>(o) = v;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (n + j < N) o[j] = v[j];
-        }
-    } else {
-        uint16_t* o = static_cast<uint16_t*>(row) + n;
-        if (vec) {
-            *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (n + j < N) o[j] = (uint16_t)f32_to_bf16_bits(v[j]);
-        }
-    }
-}
-
 constexpr int kSkThreads = 512, kSkWaves = kSkThreads / kWave;
 
 // Dense product: a workgroup computes 16 outputs of 16 TF rows; wave v takes the blocks v, v + 8, ... of the inputs.
@@ -126,7 +103,7 @@ __global__ __launch_bounds__(kSkThreads) void fp8_skinny_kernel(const Fp8Dense p
         const int m = 16 * t + l16, n = n0 + 4 * g;
         if (m < mr && n < p.N) {
             char* row = static_cast<char*>(p.y) + (m0 + m) * p.ldy * (p.out_f32 ? 4 : 2);
-            store4(row, p.out_f32, n, p.N, p.vec && n + 3 < p.N, v);
+            fp8_store4(row, p.out_f32, n, p.N, p.vec && n + 3 < p.N, v);
         }
     }
 }
@@ -134,10 +111,9 @@ __global__ __launch_bounds__(kSkThreads) void fp8_skinny_kernel(const Fp8Dense p
 // Rows of tile `i` of the table: expert, first row, end row (at most 16 rows).
 __device__ __forceinline__ bool a8_tile(const Fp8Ffn& p, int i, int* e, int* r0, int* r1) {
     if (i >= p.tiles[0]) return false;
-    *e = p.tiles[1 + 2 * i];
-    *r0 = p.tiles[2 + 2 * i];
-    const int end = p.offsets ? p.offsets[*e + 1] : p.P;
-    *r1 = min(min(*r0 + 16, end), p.P);
+    *e = p.tiles[1 + 3 * i];
+    *r0 = p.tiles[2 + 3 * i];
+    *r1 = min(p.tiles[3 + 3 * i], p.P);
     return *r0 >= 0 && *r0 < *r1;
 }
 
@@ -203,7 +179,7 @@ __global__ __launch_bounds__(kSkThreads) void fp8_skinny_down_kernel(const Fp8Ff
     f32x4_t acc[1][1] = {{f32x4_t{}}};
     fp8_wave_product<1, 1, false>(acc, wr, (uint32_t)l16 * (uint32_t)p.F, ar, aoff, sr, soff, sw, 0, 1, KB, p.F, g);
     if (r0 + l16 < r1)
-        store4(static_cast<char*>(p.rows) + (size_t)(r0 + l16) * p.H * (p.out_f32 ? 4 : 2), p.out_f32, n0 + 4 * g,
+        fp8_store4(static_cast<char*>(p.rows) + (size_t)(r0 + l16) * p.H * (p.out_f32 ? 4 : 2), p.out_f32, n0 + 4 * g,
                p.H, true, acc[0][0]);
 }
 
