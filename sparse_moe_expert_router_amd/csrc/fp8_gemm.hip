@@ -52,7 +52,7 @@ __device__ __forceinline__ void wait_vm() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
 }
 
-template <int TF, int MODE, bool kExact, int kW>
+template <int TF, int MODE, bool kExact, bool kTail, int kW>
 __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d, const Fp8Ffn p) {
     using L = GemmLds<TF>;
     constexpr int BT = L::BT;
@@ -88,7 +88,7 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
     const int KB = (K + 127) / 128;
     const int N = MODE == G_DENSE ? d.N : MODE == G_GATEUP ? p.F : p.H;
     const int mr = m1 - m0;
-    const bool tail = MODE == G_DENSE && K % 128 != 0;
+    const bool tail = kTail && K % 128 != 0;  // the last block is shorter
 
     // ---- buffers
     const uint32_t lda = MODE == G_DENSE ? (uint32_t)d.lda : (uint32_t)K;
@@ -146,25 +146,30 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
     const int rest = K - (KB - 1) * 128;  // inputs of the last block
 
     i32x8_t w[kW + 1][4];
-    auto load_w = [&](i32x8_t (&dst)[4], int j) {
+    // fragment f of step j's weights
+    auto load_w = [&](i32x8_t (&dst)[4], int f, int j) {
+        const __amdgpu_buffer_rsrc_t r = f >= 2 ? rw1 : rw0;
         j = min(j, KB - 1);
-        const bool cut = tail && j == KB - 1;
-        const bool z0 = cut && 16 * g >= rest, z1 = cut && 16 * g + 64 >= rest;
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            const __amdgpu_buffer_rsrc_t r = f >= 2 ? rw1 : rw0;
-            dst[f] = join8(buf_load16(r, z0 ? kOob : woff[f], (uint32_t)j * 128u),
-                           buf_load16(r, z1 ? kOob : woff[f] + 64u, (uint32_t)j * 128u));
-        }
+        if (tail && j == KB - 1)
+            dst[f] = join8(buf_load16(r, 16 * g < rest ? woff[f] : kOob, (uint32_t)j * 128u),
+                           buf_load16(r, 16 * g + 64 < rest ? woff[f] + 64u : kOob, (uint32_t)j * 128u));
+        else
+            dst[f] = join8(buf_load16(r, woff[f], (uint32_t)j * 128u), buf_load16(r, woff[f] + 64u, (uint32_t)j * 128u));
     };
-    auto load_a = [&](int j) {
+    auto load_w4 = [&](i32x8_t (&dst)[4], int j) {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) load_w(dst, f, j);
+    };
+    auto load_a = [&](int i, int j) {
         uint8_t* st = smem + (j % kGStages) * L::A;
         j = min(j, KB - 1);
-        const bool z = tail && j == KB - 1 && 16 * apiece >= rest;
+        uint32_t off = aoff[i];
+        if (tail && j == KB - 1) off = 16 * apiece < rest ? off : kOob;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + (8 * i + wv) * 1024), 16, (int)off, j * 128, 0, 0);
+    };
+    auto load_a_all = [&](int j) {
 #pragma unroll
-        for (int i = 0; i < NA; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + (8 * i + wv) * 1024), 16,
-                                                     (int)(z ? kOob : aoff[i]), j * 128, 0, 0);
+        for (int i = 0; i < NA; ++i) load_a(i, j);
     };
     // scales of blocks 8 c .. 8 c + 7: wave v loads block 8 c + v of every row
     auto load_s = [&](int c) {
@@ -189,62 +194,106 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
 
     __syncthreads();  // rowoff
     load_s(0);
-    load_a(0);
-    load_a(1);
-    if (kW > 1) load_w(w[0], 0);
-    if (kW > 1) load_w(w[1], 1);
-    if (kW == 1) load_w(w[0], 0);
-    load_a(2);
+    load_a_all(0);
+    load_a_all(1);
+#pragma unroll
+    for (int i = 0; i < kW; ++i) load_w4(w[i + 1], i);
+    load_a_all(2);
 
-    // LDS byte offset of the lane's pieces of row 16 t + l16 of the wave's rows
+    // LDS offsets of the lane's two pieces of row l16 of the wave's rows, and of its scales
     const int ar = (wt * 16 * TF + l16) * 128;
-    const int p0 = 16 * (g ^ g_swz(l16)), p1 = 16 * ((g + 4) ^ g_swz(l16));
+    const int p0 = ar + 16 * (g ^ g_swz(l16)), p1 = ar + 16 * ((g + 4) ^ g_swz(l16));
+    const int sr0 = L::SA + (wt * 16 * TF + l16) * 4;
+    const int sw0 = L::SW + (MODE != G_GATEUP && wn >= 2 ? 32 : 0);
+    // rows 16 t + l16 of step j, their scales, and the weights' scales
+    auto read_a = [&](int j, int t) {
+        const uint8_t* st = smem + (j % kGStages) * L::A + t * 2048;
+        return join8(*reinterpret_cast<const i32x4_t*>(st + p0), *reinterpret_cast<const i32x4_t*>(st + p1));
+    };
+    auto read_sa = [&](int j, int t) {
+        return *reinterpret_cast<const float*>(smem + sr0 + (((j >> 3) & 1) * 8 + (j & 7)) * BT * 4 + t * 64);
+    };
+    auto read_sw = [&](int j, int half) {
+        return *reinterpret_cast<const float*>(smem + sw0 + ((j >> 3) & 1) * 64 + (j & 7) * 4 + half * 32);
+    };
 
-    auto step = [&](int j, i32x8_t (&cur)[4], i32x8_t (&next)[4]) {
+    wait_vm<2 * NA + kW * 8>();  // rows of step 0 and the first scales
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+
+    // One step: 4 TF products q = 4 t + f.  The order is fixed: product q is
+    // issued, then product q - 2 (its MFMA done by then) is scaled and added,
+    // so that the matrix cores and the vector units overlap within the wave;
+    // the loads of later steps are spread between them.  The first rows and
+    // scales of a step are read at the end of the step before: its rows landed
+    // by that step's barrier.
+    i32x8_t an;
+    float sn, swn0, swn1 = 0.0f;
+    auto read_first = [&](int j) {
+        an = read_a(j, 0);
+        sn = read_sa(j, 0);
+        swn0 = read_sw(j, 0);
+        if (MODE == G_GATEUP) swn1 = read_sw(j, 1);
+    };
+    read_first(0);
+    for (int j = 0; j < KB; ++j) {
         // everything up to the weights of step j has landed: rows of step j + 1,
         // and the scales; then no wave still reads the stage refilled below
         wait_vm<NA + (kW - 1) * 8>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
+        // the weights' buffers move up one: register copies, so that one loop
+        // body serves every step (bodies for each position of a ring left the
+        // register allocator spilling)
+#pragma unroll
+        for (int i = 0; i < kW; ++i)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) w[i][f] = w[i + 1][f];
+        i32x8_t (&cur)[4] = w[0];
+        i32x8_t (&next)[4] = w[kW];
         if ((j & 7) == 0 && j + 8 < KB) load_s(j / 8 + 1);
-        load_w(next, j + kW);
-        load_a(j + 3);
-        const uint8_t* st = smem + (j % kGStages) * L::A + ar;
-        const float* sa = reinterpret_cast<const float*>(smem + L::SA) + ((j >> 3) & 1) * 8 * BT + (j & 7) * BT +
-                          wt * 16 * TF + l16;
-        const float* swp = reinterpret_cast<const float*>(smem + L::SW) + ((j >> 3) & 1) * 16 + (j & 7);
-        const float s0 = MODE == G_GATEUP ? swp[0] : swp[wn >= 2 ? 8 : 0];
-        const float s1 = MODE == G_GATEUP ? swp[8] : s0;
+        i32x8_t a;
+        f32x4_t v[3];
+        float c0[2], c1[2];   // scales of rows t in slot t & 1
+        float s0 = swn0, s1 = swn1;
+        auto add = [&](int q) {
+            const int t = q / 4, f = q % 4;
+            const float c = MODE == G_GATEUP && f >= 2 ? c1[t & 1] : c0[t & 1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(c, v[q % 3][i], acc[f][t][i]);
+        };
 #pragma unroll
         for (int t = 0; t < TF; ++t) {
-            const i32x8_t a = join8(*reinterpret_cast<const i32x4_t*>(st + t * 2048 + p0),
-                                    *reinterpret_cast<const i32x4_t*>(st + t * 2048 + p1));
-            const float sr = sa[16 * t];
+            a = an;
+            c0[t & 1] = sn * s0;
+            if (MODE == G_GATEUP) c1[t & 1] = sn * s1;
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
-                const f32x4_t v = mfma_fp8<kExact>(cur[f], a);
-                const float c = sr * (f >= 2 ? s1 : s0);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(c, v[i], acc[f][t][i]);
+                const int q = 4 * t + f;
+                v[q % 3] = mfma_fp8<kExact>(cur[f], a);
+                if (f == 1) {
+                    if (t + 1 < TF) {
+                        an = read_a(j, t + 1);
+                        sn = read_sa(j, t + 1);
+                    } else {
+                        read_first(j + 1);
+                    }
+                }
+                // the 4 weight fragments first (the next wait counts on that), then the rows
+                if (TF >= 4) {
+                    if (q % 2 == 0 && q / 2 < 4) load_w(next, q / 2, j + kW);
+                    if (q >= 8 && (q - 8) % 2 == 0 && (q - 8) / 2 < NA) load_a((q - 8) / 2, j + 3);
+                } else {
+                    if (q < 4) load_w(next, q, j + kW);
+                    if (q >= 4 && q - 4 < NA) load_a(q - 4, j + 3);
+                }
+                if (q >= 2) add(q - 2);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
+        add(4 * TF - 2);
+        add(4 * TF - 1);
         asm volatile("" ::: "memory");
-    };
-    int j = 0;
-    if constexpr (kW == 1) {
-        for (; j + 1 < KB; j += 2) {
-            step(j, w[0], w[1]);
-            step(j + 1, w[1], w[0]);
-        }
-        if (j < KB) step(j, w[0], w[1]);
-    } else {
-        for (; j + 2 < KB; j += 3) {
-            step(j, w[0], w[2]);
-            step(j + 1, w[1], w[0]);
-            step(j + 2, w[2], w[1]);
-        }
-        if (j < KB) step(j, w[0], w[2]);
-        if (j + 1 < KB) step(j + 1, w[1], w[0]);
     }
     wait_vm<0>();
     __syncthreads();  // no load still writes the stages, no wave still reads them
@@ -308,40 +357,46 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
     }
 }
 
-template <int TF, int MODE, bool kExact, int kW>
+template <int TF, int MODE, bool kExact, bool kTail, int kW>
 static hipError_t launch_one(const Fp8Dense& d, const Fp8Ffn& p, long tiles, hipStream_t s) {
     const long grid = (tiles + kXcd - 1) / kXcd * kXcd;
-    const void* fn = reinterpret_cast<const void*>(fp8_gemm_kernel<TF, MODE, kExact, kW>);
+    const void* fn = reinterpret_cast<const void*>(fp8_gemm_kernel<TF, MODE, kExact, kTail, kW>);
     const hipError_t err = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, GemmLds<TF>::TOTAL);
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL((fp8_gemm_kernel<TF, MODE, kExact, kW>), dim3((unsigned)grid), dim3(kGThreads),
+    hipLaunchKernelGGL((fp8_gemm_kernel<TF, MODE, kExact, kTail, kW>), dim3((unsigned)grid), dim3(kGThreads),
                        GemmLds<TF>::TOTAL, s, d, p);
     return hipGetLastError();
 }
 
 hipError_t launch_fp8_gemm(const Fp8Dense& d, int bt, hipStream_t s) {
-    const long tiles = (long)((d.M + bt - 1) / bt) * ((d.N + kGN - 1) / kGN);
     const Fp8Ffn p{};
-    if (d.out_f32) return launch_one<4, G_DENSE, true, 1>(d, p, (long)((d.M + 127) / 128) * ((d.N + kGN - 1) / kGN), s);
-    if (bt == 256) return launch_one<8, G_DENSE, false, 1>(d, p, tiles, s);
-    if (bt == 128) return launch_one<4, G_DENSE, false, 2>(d, p, tiles, s);
-    return launch_one<2, G_DENSE, false, 2>(d, p, tiles, s);
+    auto tiles = [&](int rows) { return (long)((d.M + rows - 1) / rows) * ((d.N + kGN - 1) / kGN); };
+    if (d.out_f32) return launch_one<4, G_DENSE, true, true, 1>(d, p, tiles(128), s);
+    // a K of whole blocks needs no checks in the loop; with them the 256-row
+    // tile does not fit the registers, so a ragged K runs 128 rows at most
+    if (d.K % 128) {
+        if (bt == 64) return launch_one<2, G_DENSE, false, true, 2>(d, p, tiles(64), s);
+        return launch_one<4, G_DENSE, false, true, 2>(d, p, tiles(128), s);
+    }
+    if (bt == 256) return launch_one<8, G_DENSE, false, false, 1>(d, p, tiles(256), s);
+    if (bt == 128) return launch_one<4, G_DENSE, false, false, 2>(d, p, tiles(128), s);
+    return launch_one<2, G_DENSE, false, false, 2>(d, p, tiles(64), s);
 }
 
 hipError_t launch_fp8_gemm_gateup(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s) {
     const Fp8Dense d{};
     const long tiles = max_tiles * (p.F / 128);
-    if (bt == 256) return launch_one<8, G_GATEUP, false, 1>(d, p, tiles, s);
-    if (bt == 128) return launch_one<4, G_GATEUP, false, 2>(d, p, tiles, s);
-    return launch_one<2, G_GATEUP, false, 2>(d, p, tiles, s);
+    if (bt == 256) return launch_one<8, G_GATEUP, false, false, 1>(d, p, tiles, s);
+    if (bt == 128) return launch_one<4, G_GATEUP, false, false, 2>(d, p, tiles, s);
+    return launch_one<2, G_GATEUP, false, false, 2>(d, p, tiles, s);
 }
 
 hipError_t launch_fp8_gemm_down(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s) {
     const Fp8Dense d{};
     const long tiles = max_tiles * ((p.H + kGN - 1) / kGN);
-    if (bt == 256) return launch_one<8, G_DOWN, false, 1>(d, p, tiles, s);
-    if (bt == 128) return launch_one<4, G_DOWN, false, 2>(d, p, tiles, s);
-    return launch_one<2, G_DOWN, false, 2>(d, p, tiles, s);
+    if (bt == 256) return launch_one<8, G_DOWN, false, false, 1>(d, p, tiles, s);
+    if (bt == 128) return launch_one<4, G_DOWN, false, false, 2>(d, p, tiles, s);
+    return launch_one<2, G_DOWN, false, false, 2>(d, p, tiles, s);
 }
 
 }  // namespace moe

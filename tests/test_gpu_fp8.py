@@ -93,7 +93,7 @@ def _check_product(y, a, sa, w, sw):
 
 SHAPES = [(1, 16, 16), (1, 1, 128), (1, 2560, 2560), (5, 33, 144), (16, 128, 640), (17, 130, 1296), (31, 257, 128), (33, 1000, 272),
           (77, 1000, 1296), (128, 256, 256), (129, 300, 384), (200, 640, 2560), (256, 256, 128), (257, 513, 1040), (300, 1280, 512),
-          (513, 129, 2064), (1000, 384, 640), (2048, 264, 1152)]
+          (513, 129, 2064), (1000, 384, 640), (2048, 264, 1152), (4100, 4099, 144), (4097, 4200, 128), (2300, 8200, 1280)]
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
