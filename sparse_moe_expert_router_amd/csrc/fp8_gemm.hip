@@ -7,16 +7,22 @@
 // the epilogue) and their down pass.
 //
 // A workgroup is 8 waves, 4 along the outputs x 2 along the rows; a wave owns
-// 64 outputs x 16 TF rows.  One step is one block of 128 inputs.
-//  - Rows go from memory straight into LDS (16-byte buffer loads to LDS), up
-//    to three steps ahead, 128 bytes a row, 16-byte pieces XOR-swizzled.  The
-//    4 waves along the outputs share them.
-//  - Weights go straight into registers, kW steps ahead: each byte is
-//    used by two waves only, and through LDS its traffic (64 KB written, 192
-//    KB read per step of a 256 x 256 tile) would take as long as the MFMAs.
-//  - Row scales are staged in LDS eight steps at a time.
+// 64 outputs x 16 TF rows.  One step is one block of 128 inputs.  Rows and
+// weights both go from memory straight into LDS (16-byte buffer loads to LDS),
+// 128 bytes a row, 16-byte pieces XOR-swizzled, and from there into MFMA
+// operands; the row scales are staged in LDS eight steps at a time.  (Weights
+// loaded straight into operand registers measured slower: neighbouring lanes
+// then read different rows, 64 cache accesses an instruction, and the cache's
+// one access a cycle bounded the kernel: 8192^3 in 676 us.)
 // The weights are the MFMA's row operand: a lane ends up with 4 neighbouring
 // outputs of one row, and one row scale per 16 rows covers all 4.
+//
+// Pipeline: one barrier M_j in the middle of each step j.  A wave holds step
+// j's weights in registers (read at the end of step j - 1), so M_j ends the
+// use of their LDS stage, of the first half of step j's rows and of the second
+// half of step j - 1's.  After M_j the wave issues the loads that refill these,
+// of S steps later (S stages); they are waited for at M_{j + S - 1}, so every
+// load has S - 1 whole steps to land and nothing stops at the step's border.
 #include "fp8.h"
 #include "ffn_internal.h"
 #include "fp8_internal.h"
@@ -27,36 +33,46 @@ enum { G_DENSE = 0, G_GATEUP = 1, G_DOWN = 2 };
 
 constexpr int kGThreads = 512, kGWaves = 8;
 constexpr int kGN = 256;       // outputs of a tile (gate/up: 128 of each)
-constexpr int kGStages = 4;    // LDS stages of rows
-
 // LDS of a tile of BT rows, in bytes.
 template <int TF>
 struct GemmLds {
     static constexpr int BT = 32 * TF;
+    static constexpr int S = TF >= 8 ? 2 : 3;            // stages
     static constexpr int A = BT * 128;                   // one stage of rows
-    static constexpr int SA = kGStages * A;              // row scales [2][8][BT]
+    static constexpr int B = kGN * 128;                  // one stage of weights
+    static constexpr int W = S * A;                      // weights [S][256][128]
+    static constexpr int SA = W + S * B;                 // row scales [2][8][BT]
     static constexpr int SW = SA + 2 * 8 * BT * 4;       // weight scales [2][2][8]
     static constexpr int ROW = SW + 2 * 2 * 8 * 4;       // byte offsets of the rows' scales [BT]
     static constexpr int AMAX = ROW + BT * 4;            // gate/up: group maxima [4][BT]
     static constexpr int TOTAL = AMAX + 4 * BT * 4;
+    static_assert(TOTAL <= 160 * 1024, "LDS of a compute unit");
 };
 
-// 16-byte piece c of row r sits at piece c ^ g_swz(r): 8 consecutive rows, and
-// the even (or odd) rows of 16, take 8 different pieces.
-__device__ __forceinline__ int g_swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+// 16-byte piece c of row r sits at piece c ^ g_swz(r).  A 16-byte LDS read
+// serves 16 lanes at a time, not always neighbouring ones; this swizzle keeps
+// rows 0..15 of one piece on different banks, and also rows 0-3, 12-15 of one
+// piece beside rows 4-11 of the next.
+__device__ __forceinline__ int g_swz(int r) { return (r >> 1) & 7; }
 
 typedef __attribute__((address_space(3))) void lds_void;
 
+// Waits until at most n of the wave's memory loads are under way, and for its
+// LDS reads; then for the other waves.
 template <int n>
-__device__ __forceinline__ void wait_vm() {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(n) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
-template <int TF, int MODE, bool kExact, bool kTail, int kW>
+template <int TF, int MODE, bool kExact>
 __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d, const Fp8Ffn p) {
     using L = GemmLds<TF>;
     constexpr int BT = L::BT;
-    constexpr int NA = BT / 64;   // row loads of a wave per step
+    constexpr int S = L::S;
+    constexpr int NA = BT / 64;   // row loads of a wave per step; 4 weight loads
+    constexpr int NL = NA + 4;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
 
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -88,7 +104,7 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
     const int KB = (K + 127) / 128;
     const int N = MODE == G_DENSE ? d.N : MODE == G_GATEUP ? p.F : p.H;
     const int mr = m1 - m0;
-    const bool tail = kTail && K % 128 != 0;  // the last block is shorter
+    const bool tail = MODE == G_DENSE && K % 128 != 0;  // the last block is shorter
 
     // ---- buffers
     const uint32_t lda = MODE == G_DENSE ? (uint32_t)d.lda : (uint32_t)K;
@@ -116,8 +132,9 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
         MODE == G_GATEUP ? fp8_rsrc(p.sup + sbase, sbytes)
                          : fp8_rsrc((MODE == G_DENSE ? d.sw : p.sdown) + sbase + (n0 / 128 + 1 < NB ? KB : 0), sbytes);
 
-    // ---- rows: load i of wave wv fills rows 8 (8 i + wv) .. +7 of a stage, lane
-    // = 8 (row % 8) + piece position; the piece read is position ^ g_swz(row)
+    // ---- loads: load i of wave wv fills rows 8 (8 i + wv) .. +7 of a stage,
+    // lane = 8 (row % 8) + piece position; the piece read is position ^ g_swz(row)
+    const int lr = 8 * wv + (lane >> 3), piece = (lane & 7) ^ g_swz(lr);  // g_swz: the same for rows 64 apart
     auto source_row = [&](int r) {  // row of the source matrix (relative to its base) behind row r of the tile
         if (MODE == G_DENSE) return (uint32_t)r;
         const int q = min(r, mr - 1);
@@ -125,51 +142,40 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
         return (uint32_t)(p.sorted_pair ? min(max(p.sorted_pair[m0 + q] / p.k, 0), p.T - 1) : m0 + q);
     };
     uint32_t aoff[NA];
-    int apiece = 0;
 #pragma unroll
-    for (int i = 0; i < NA; ++i) {
-        const int r = 8 * (8 * i + wv) + (lane >> 3);
-        apiece = (lane & 7) ^ g_swz(r);  // the same for every i: rows 64 apart
-        aoff[i] = source_row(r) * lda + 16u * (uint32_t)apiece;
-    }
+    for (int i = 0; i < NA; ++i) aoff[i] = source_row(64 * i + lr) * lda + 16u * (uint32_t)piece;
+    // weight rows 64 i + lr; gate/up: 0..127 the gate's, 128..255 the up's
+    const uint32_t woff = (uint32_t)lr * ldw + 16u * (uint32_t)piece;
     uint32_t* rowoff = reinterpret_cast<uint32_t*>(smem + L::ROW);
     for (int r = tid; r < BT; r += kGThreads)
         rowoff[r] = (MODE == G_DENSE && r >= mr) ? kOob : source_row(r) * (uint32_t)KB * 4u;
+    const bool cut = tail && 16 * piece >= K - (KB - 1) * 128;  // nothing of the lane's piece in the last block
 
-    // ---- weights: fragment f of a wave is 16 outputs, lane output l16, pieces g and g + 4
-    uint32_t woff[4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-        const int r = MODE == G_GATEUP ? 32 * wn + 16 * (f & 1) + l16 : 64 * wn + 16 * f + l16;
-        woff[f] = (uint32_t)r * ldw + 16u * (uint32_t)g;
-    }
-    const int rest = K - (KB - 1) * 128;  // inputs of the last block
-
-    i32x8_t w[kW + 1][4];
-    // fragment f of step j's weights
-    auto load_w = [&](i32x8_t (&dst)[4], int f, int j) {
-        const __amdgpu_buffer_rsrc_t r = f >= 2 ? rw1 : rw0;
+    auto load_w = [&](int i, int j) {
+        uint8_t* st = smem + L::W + (j % S) * L::B;
         j = min(j, KB - 1);
-        if (tail && j == KB - 1)
-            dst[f] = join8(buf_load16(r, 16 * g < rest ? woff[f] : kOob, (uint32_t)j * 128u),
-                           buf_load16(r, 16 * g + 64 < rest ? woff[f] + 64u : kOob, (uint32_t)j * 128u));
-        else
-            dst[f] = join8(buf_load16(r, woff[f], (uint32_t)j * 128u), buf_load16(r, woff[f] + 64u, (uint32_t)j * 128u));
-    };
-    auto load_w4 = [&](i32x8_t (&dst)[4], int j) {
-#pragma unroll
-        for (int f = 0; f < 4; ++f) load_w(dst, f, j);
+        uint32_t off = woff + (uint32_t)(MODE == G_GATEUP ? i & 1 : i) * 64u * ldw;
+        if (tail && j == KB - 1) off = cut ? kOob : off;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(MODE == G_GATEUP && i >= 2 ? rw1 : rw0,
+                                                 (lds_void*)(st + (8 * i + wv) * 1024), 16, (int)off, j * 128, 0, 0);
     };
     auto load_a = [&](int i, int j) {
-        uint8_t* st = smem + (j % kGStages) * L::A;
+        uint8_t* st = smem + (j % S) * L::A;
         j = min(j, KB - 1);
         uint32_t off = aoff[i];
-        if (tail && j == KB - 1) off = 16 * apiece < rest ? off : kOob;
+        if (tail && j == KB - 1) off = cut ? kOob : off;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + (8 * i + wv) * 1024), 16, (int)off, j * 128, 0, 0);
     };
-    auto load_a_all = [&](int j) {
-#pragma unroll
-        for (int i = 0; i < NA; ++i) load_a(i, j);
+    // load n of the group issued after M_j: 4 of the weights of step j + S, then
+    // the rows: first halves (of each row wave's rows) of step j + S, second
+    // halves of step j + S - 1.  The first group of all has no second halves.
+    auto load_group = [&](int n, int j) {
+        if (n < 4) {
+            load_w(n, j + S);
+        } else {
+            const int second = ((64 * (n - 4) + 8 * wv) / (8 * TF)) & 1;
+            load_a(n - 4, max(j + S - second, 0));
+        }
     };
     // scales of blocks 8 c .. 8 c + 7: wave v loads block 8 c + v of every row
     auto load_s = [&](int c) {
@@ -194,21 +200,25 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
 
     __syncthreads();  // rowoff
     load_s(0);
-    load_a_all(0);
-    load_a_all(1);
 #pragma unroll
-    for (int i = 0; i < kW; ++i) load_w4(w[i + 1], i);
-    load_a_all(2);
+    for (int j = -S; j < 0; ++j)
+#pragma unroll
+        for (int n = 0; n < NL; ++n) load_group(n, j);
 
-    // LDS offsets of the lane's two pieces of row l16 of the wave's rows, and of its scales
+    // LDS offsets of the lane's two pieces of row l16 of the wave's rows, of
+    // weight row l16 of its outputs, and of its scales
+    const int x0 = 16 * (g ^ g_swz(l16)), x1 = 16 * ((g + 4) ^ g_swz(l16));
     const int ar = (wt * 16 * TF + l16) * 128;
-    const int p0 = ar + 16 * (g ^ g_swz(l16)), p1 = ar + 16 * ((g + 4) ^ g_swz(l16));
+    const int br = L::W + ((MODE == G_GATEUP ? 32 * wn : 64 * wn) + l16) * 128;
     const int sr0 = L::SA + (wt * 16 * TF + l16) * 4;
     const int sw0 = L::SW + (MODE != G_GATEUP && wn >= 2 ? 32 : 0);
-    // rows 16 t + l16 of step j, their scales, and the weights' scales
-    auto read_a = [&](int j, int t) {
-        const uint8_t* st = smem + (j % kGStages) * L::A + t * 2048;
-        return join8(*reinterpret_cast<const i32x4_t*>(st + p0), *reinterpret_cast<const i32x4_t*>(st + p1));
+    auto read_a = [&](int j, int t) {  // rows 16 t + l16 of step j
+        const uint8_t* st = smem + (j % S) * L::A + ar + t * 2048;
+        return join8(*reinterpret_cast<const i32x4_t*>(st + x0), *reinterpret_cast<const i32x4_t*>(st + x1));
+    };
+    auto read_w = [&](int j, int f) {
+        const uint8_t* st = smem + (j % S) * L::B + br + (MODE == G_GATEUP && f >= 2 ? 128 + 16 * (f - 2) : 16 * f) * 128;
+        return join8(*reinterpret_cast<const i32x4_t*>(st + x0), *reinterpret_cast<const i32x4_t*>(st + x1));
     };
     auto read_sa = [&](int j, int t) {
         return *reinterpret_cast<const float*>(smem + sr0 + (((j >> 3) & 1) * 8 + (j & 7)) * BT * 4 + t * 64);
@@ -217,17 +227,7 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
         return *reinterpret_cast<const float*>(smem + sw0 + ((j >> 3) & 1) * 64 + (j & 7) * 4 + half * 32);
     };
 
-    wait_vm<2 * NA + kW * 8>();  // rows of step 0 and the first scales
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-
-    // One step: 4 TF products q = 4 t + f.  The order is fixed: product q is
-    // issued, then product q - 2 (its MFMA done by then) is scaled and added,
-    // so that the matrix cores and the vector units overlap within the wave;
-    // the loads of later steps are spread between them.  The first rows and
-    // scales of a step are read at the end of the step before: its rows landed
-    // by that step's barrier.
-    i32x8_t an;
+    i32x8_t w[4], an;
     float sn, swn0, swn1 = 0.0f;
     auto read_first = [&](int j) {
         an = read_a(j, 0);
@@ -235,27 +235,22 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
         swn0 = read_sw(j, 0);
         if (MODE == G_GATEUP) swn1 = read_sw(j, 1);
     };
+    wait_and_meet<(S - 1) * NL>();
+#pragma unroll
+    for (int f = 0; f < 4; ++f) w[f] = read_w(0, f);
     read_first(0);
+
+    // One step: 4 TF products q = 4 t + f.  The order is fixed: product q is
+    // issued, then product q - 2 (its MFMA done by then) is scaled and added,
+    // so that the matrix cores and the vector units overlap within the wave.
+    // Rows are read one group of 16 ahead, the next step's weights into each
+    // register block after its last use.
+    constexpr int kMeet = TF / 2 - 1;  // the group of rows before which the waves meet
     for (int j = 0; j < KB; ++j) {
-        // everything up to the weights of step j has landed: rows of step j + 1,
-        // and the scales; then no wave still reads the stage refilled below
-        wait_vm<NA + (kW - 1) * 8>();
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        // the weights' buffers move up one: register copies, so that one loop
-        // body serves every step (bodies for each position of a ring left the
-        // register allocator spilling)
-#pragma unroll
-        for (int i = 0; i < kW; ++i)
-#pragma unroll
-            for (int f = 0; f < 4; ++f) w[i][f] = w[i + 1][f];
-        i32x8_t (&cur)[4] = w[0];
-        i32x8_t (&next)[4] = w[kW];
-        if ((j & 7) == 0 && j + 8 < KB) load_s(j / 8 + 1);
         i32x8_t a;
         f32x4_t v[3];
         float c0[2], c1[2];   // scales of rows t in slot t & 1
-        float s0 = swn0, s1 = swn1;
+        const float s0 = swn0, s1 = swn1;
         auto add = [&](int q) {
             const int t = q / 4, f = q % 4;
             const float c = MODE == G_GATEUP && f >= 2 ? c1[t & 1] : c0[t & 1];
@@ -264,14 +259,19 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
         };
 #pragma unroll
         for (int t = 0; t < TF; ++t) {
+            if (t == kMeet) {
+                wait_and_meet<(S - 2) * NL>();
+                if ((j & 7) == 0 && j + 8 < KB) load_s(j / 8 + 1);
+            }
             a = an;
             c0[t & 1] = sn * s0;
             if (MODE == G_GATEUP) c1[t & 1] = sn * s1;
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
                 const int q = 4 * t + f;
-                v[q % 3] = mfma_fp8<kExact>(cur[f], a);
-                if (f == 1) {
+                v[q % 3] = mfma_fp8<kExact>(w[f], a);
+                if (t + 1 == TF) w[f] = read_w(j + 1, f);
+                if (f == 0) {
                     if (t + 1 < TF) {
                         an = read_a(j, t + 1);
                         sn = read_sa(j, t + 1);
@@ -279,24 +279,15 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
                         read_first(j + 1);
                     }
                 }
-                // the 4 weight fragments first (the next wait counts on that), then the rows
-                if (TF >= 4) {
-                    if (q % 2 == 0 && q / 2 < 4) load_w(next, q / 2, j + kW);
-                    if (q >= 8 && (q - 8) % 2 == 0 && (q - 8) / 2 < NA) load_a((q - 8) / 2, j + 3);
-                } else {
-                    if (q < 4) load_w(next, q, j + kW);
-                    if (q >= 4 && q - 4 < NA) load_a(q - 4, j + 3);
-                }
+                if (q >= 4 * kMeet && q - 4 * kMeet < NL) load_group(q - 4 * kMeet, j);
                 if (q >= 2) add(q - 2);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
         add(4 * TF - 2);
         add(4 * TF - 1);
-        asm volatile("" ::: "memory");
     }
-    wait_vm<0>();
-    __syncthreads();  // no load still writes the stages, no wave still reads them
+    wait_and_meet<0>();  // no load still writes LDS, no wave still reads it
 
     if constexpr (MODE == G_GATEUP) {
         // h = silu(gate) up in fp32; its largest magnitude per row over the
@@ -320,7 +311,7 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
         __syncthreads();
         // codes [BT][128] through LDS (rows padded to 144 bytes), then 16 bytes a lane
         constexpr int LD = 144;
-        static_assert(BT * LD <= kGStages * L::A, "codes fit the row stages");
+        static_assert(BT * LD <= L::SA, "codes fit the stages");
 #pragma unroll
         for (int t = 0; t < TF; ++t) {
             const int r = wt * 16 * TF + 16 * t + l16;
@@ -357,13 +348,13 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
     }
 }
 
-template <int TF, int MODE, bool kExact, bool kTail, int kW>
+template <int TF, int MODE, bool kExact>
 static hipError_t launch_one(const Fp8Dense& d, const Fp8Ffn& p, long tiles, hipStream_t s) {
     const long grid = (tiles + kXcd - 1) / kXcd * kXcd;
-    const void* fn = reinterpret_cast<const void*>(fp8_gemm_kernel<TF, MODE, kExact, kTail, kW>);
+    const void* fn = reinterpret_cast<const void*>(fp8_gemm_kernel<TF, MODE, kExact>);
     const hipError_t err = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, GemmLds<TF>::TOTAL);
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL((fp8_gemm_kernel<TF, MODE, kExact, kTail, kW>), dim3((unsigned)grid), dim3(kGThreads),
+    hipLaunchKernelGGL((fp8_gemm_kernel<TF, MODE, kExact>), dim3((unsigned)grid), dim3(kGThreads),
                        GemmLds<TF>::TOTAL, s, d, p);
     return hipGetLastError();
 }
@@ -371,32 +362,26 @@ static hipError_t launch_one(const Fp8Dense& d, const Fp8Ffn& p, long tiles, hip
 hipError_t launch_fp8_gemm(const Fp8Dense& d, int bt, hipStream_t s) {
     const Fp8Ffn p{};
     auto tiles = [&](int rows) { return (long)((d.M + rows - 1) / rows) * ((d.N + kGN - 1) / kGN); };
-    if (d.out_f32) return launch_one<4, G_DENSE, true, true, 1>(d, p, tiles(128), s);
-    // a K of whole blocks needs no checks in the loop; with them the 256-row
-    // tile does not fit the registers, so a ragged K runs 128 rows at most
-    if (d.K % 128) {
-        if (bt == 64) return launch_one<2, G_DENSE, false, true, 2>(d, p, tiles(64), s);
-        return launch_one<4, G_DENSE, false, true, 2>(d, p, tiles(128), s);
-    }
-    if (bt == 256) return launch_one<8, G_DENSE, false, false, 1>(d, p, tiles(256), s);
-    if (bt == 128) return launch_one<4, G_DENSE, false, false, 2>(d, p, tiles(128), s);
-    return launch_one<2, G_DENSE, false, false, 2>(d, p, tiles(64), s);
+    if (d.out_f32) return launch_one<4, G_DENSE, true>(d, p, tiles(128), s);
+    if (bt == 256) return launch_one<8, G_DENSE, false>(d, p, tiles(256), s);
+    if (bt == 128) return launch_one<4, G_DENSE, false>(d, p, tiles(128), s);
+    return launch_one<2, G_DENSE, false>(d, p, tiles(64), s);
 }
 
 hipError_t launch_fp8_gemm_gateup(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s) {
     const Fp8Dense d{};
     const long tiles = max_tiles * (p.F / 128);
-    if (bt == 256) return launch_one<8, G_GATEUP, false, false, 1>(d, p, tiles, s);
-    if (bt == 128) return launch_one<4, G_GATEUP, false, false, 2>(d, p, tiles, s);
-    return launch_one<2, G_GATEUP, false, false, 2>(d, p, tiles, s);
+    if (bt == 256) return launch_one<8, G_GATEUP, false>(d, p, tiles, s);
+    if (bt == 128) return launch_one<4, G_GATEUP, false>(d, p, tiles, s);
+    return launch_one<2, G_GATEUP, false>(d, p, tiles, s);
 }
 
 hipError_t launch_fp8_gemm_down(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s) {
     const Fp8Dense d{};
     const long tiles = max_tiles * ((p.H + kGN - 1) / kGN);
-    if (bt == 256) return launch_one<8, G_DOWN, false, false, 1>(d, p, tiles, s);
-    if (bt == 128) return launch_one<4, G_DOWN, false, false, 2>(d, p, tiles, s);
-    return launch_one<2, G_DOWN, false, false, 2>(d, p, tiles, s);
+    if (bt == 256) return launch_one<8, G_DOWN, false>(d, p, tiles, s);
+    if (bt == 128) return launch_one<4, G_DOWN, false>(d, p, tiles, s);
+    return launch_one<2, G_DOWN, false>(d, p, tiles, s);
 }
 
 }  // namespace moe
