@@ -20,8 +20,7 @@ static int dense_bt(int M, int N) {
 hipError_t launch_fp8_matmul(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, int M, int N, int K,
                              int64_t lda, int64_t ldw, int out_f32, void* y, int64_t ldy, hipStream_t s) {
     Fp8Dense p{a, sa, w, sw, M, N, K, lda, ldw, ldy, y, out_f32, 0};
-    const int v = out_f32 ? 16 : 8;
-    p.vec = (uintptr_t)y % v == 0 && ldy % 4 == 0;
+    p.vec = (uintptr_t)y % 16 == 0 && ldy % (out_f32 ? 4 : 8) == 0;
     if (M <= kSkinnyRows) return launch_fp8_skinny(p, s);
     return launch_fp8_gemm(p, dense_bt(M, N), s);
 }

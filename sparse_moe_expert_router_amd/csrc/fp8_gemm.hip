@@ -14,8 +14,10 @@
 // loaded straight into operand registers measured slower: neighbouring lanes
 // then read different rows, 64 cache accesses an instruction, and the cache's
 // one access a cycle bounded the kernel: 8192^3 in 676 us.)
-// The weights are the MFMA's row operand: a lane ends up with 4 neighbouring
-// outputs of one row, and one row scale per 16 rows covers all 4.
+// The weights are the MFMA's row operand, so a lane ends up with outputs of one
+// row and one row scale covers them.  A product gives a lane 4 neighbouring
+// operand rows; the weights are laid into LDS in an order (g_order) that makes
+// two products of a lane 8 neighbouring outputs, 16 bytes of bf16.
 //
 // Pipeline: one barrier M_j in the middle of each step j.  A wave holds step
 // j's weights in registers (read at the end of step j - 1), so M_j ends the
@@ -54,6 +56,13 @@ struct GemmLds {
 // rows 0..15 of one piece on different banks, and also rows 0-3, 12-15 of one
 // piece beside rows 4-11 of the next.
 __device__ __forceinline__ int g_swz(int r) { return (r >> 1) & 7; }
+
+// Weight row (of a group of 32) at LDS row r: product (r / 16) of the pair,
+// operand row i = r % 16 = 4 g + j, holds output 8 g + 4 (r / 16) + j.
+__device__ __forceinline__ int g_order(int r) {
+    const int i = r & 15;
+    return (r & ~31) + 8 * (i >> 2) + 4 * ((r >> 4) & 1) + (i & 3);
+}
 
 typedef __attribute__((address_space(3))) void lds_void;
 
@@ -145,7 +154,7 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
 #pragma unroll
     for (int i = 0; i < NA; ++i) aoff[i] = source_row(64 * i + lr) * lda + 16u * (uint32_t)piece;
     // weight rows 64 i + lr; gate/up: 0..127 the gate's, 128..255 the up's
-    const uint32_t woff = (uint32_t)lr * ldw + 16u * (uint32_t)piece;
+    const uint32_t woff = (uint32_t)g_order(lr) * ldw + 16u * (uint32_t)piece;
     uint32_t* rowoff = reinterpret_cast<uint32_t*>(smem + L::ROW);
     for (int r = tid; r < BT; r += kGThreads)
         rowoff[r] = (MODE == G_DENSE && r >= mr) ? kOob : source_row(r) * (uint32_t)KB * 4u;
@@ -317,10 +326,9 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
             const int r = wt * 16 * TF + 16 * t + l16;
             const uint32_t m = max(max(amax[r], amax[BT + r]), max(amax[2 * BT + r], amax[3 * BT + r]));
             const float s = fp8_scale(m);
-#pragma unroll
-            for (int f = 0; f < 2; ++f)
-                *reinterpret_cast<uint32_t*>(smem + r * LD + 32 * wn + 16 * f + 4 * g) =
-                    fp8_pack4(acc[f][t][0], acc[f][t][1], acc[f][t][2], acc[f][t][3], s);
+            *reinterpret_cast<uint2*>(smem + r * LD + 32 * wn + 8 * g) =
+                make_uint2(fp8_pack4(acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3], s),
+                           fp8_pack4(acc[1][t][0], acc[1][t][1], acc[1][t][2], acc[1][t][3], s));
             if (wn == 0 && g == 0 && r < mr) p.hs[(size_t)(m0 + r) * NB + n0 / 128] = s;
         }
         __syncthreads();
@@ -340,9 +348,24 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
             if (r >= mr) continue;
             char* row = y + (m0 + r) * ldy * (out_f32 ? 4 : 2);
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                const int n = n0 + 64 * wn + 16 * f + 4 * g;
-                if (n < N) fp8_store4(row, out_f32, n, N, vec && n + 3 < N, acc[f][t]);
+            for (int f = 0; f < 4; f += 2) {
+                const int n = n0 + 64 * wn + 16 * f + 8 * g;
+                if (n >= N) continue;
+                if (vec && n + 7 < N) {
+                    if (out_f32) {
+                        f32x4_t* o = reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(row) + n);
+                        o[0] = acc[f][t];
+                        o[1] = acc[f + 1][t];
+                    } else {
+                        const u32x4_t o = {pack_bf16x2(acc[f][t][0], acc[f][t][1]), pack_bf16x2(acc[f][t][2], acc[f][t][3]),
+                                           pack_bf16x2(acc[f + 1][t][0], acc[f + 1][t][1]),
+                                           pack_bf16x2(acc[f + 1][t][2], acc[f + 1][t][3])};
+                        *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(row) + n) = o;
+                    }
+                } else {
+                    fp8_store4(row, out_f32, n, N, false, acc[f][t]);
+                    fp8_store4(row, out_f32, n + 4, N, false, acc[f + 1][t]);
+                }
             }
         }
     }

@@ -15,7 +15,7 @@ struct Fp8Dense {
     int64_t lda, ldw, ldy;
     void* y;
     int out_f32;
-    int vec;            // 1: y's base and stride allow stores of four neighbouring outputs
+    int vec;            // 1: y's base and stride allow 16-byte stores (and those of four neighbouring outputs)
 };
 
 // Grouped SwiGLU experts on quantised rows.
