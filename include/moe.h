@@ -275,6 +275,32 @@ size_t moe_layer_workspace_bytes(int32_t T, int32_t k, const moe_experts *expert
                                  const moe_experts *shared);
 
 /*
+ * The whole layer for few tokens, T <= 16, in two kernels: the same function
+ * as moe_layer,
+ *   y[t] = sum_j topk_gate[t][j] * expert(topk_idx[t][j], x[t])
+ *          + shared_scale[t] * shared(x[t])
+ * for decode steps where launches and the waits between them cost as much as
+ * the weights.  Routing is moe_route's, exactly (topk_idx, nullable [T][k],
+ * receives it); everything after it stays in fp32 until y is rounded to bf16
+ * (moe_layer rounds the SwiGLU products and the experts' rows to bf16 on the
+ * way, so the two differ by those roundings).  experts: bf16, FP8 or
+ * output-major AWQ; shared (nullable): one bf16 expert of the same hidden
+ * size; other formats, T > 16 or k > 64 -> MOE_ERR_UNSUPPORTED.  Other
+ * requirements and errors as moe_layer's.  y may not overlap x.
+ *   ws: moe_layer_few_workspace_bytes(T, k, experts, shared) bytes, 16-byte
+ *   aligned, of any content.  Two calls that may run at the same time need
+ *   two workspaces (one call clearing the other's counters can leave y NaN).
+ */
+moe_status moe_layer_few(const uint16_t *x, int32_t T, const uint16_t *w_router, int32_t k,
+                         const moe_experts *experts, const moe_experts *shared, const float *shared_scale,
+                         uint16_t *y, int32_t *topk_idx, void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace bytes of moe_layer_few (0 for T <= 0, T > 16 or an unsupported
+ * bank).  Grows with T. */
+size_t moe_layer_few_workspace_bytes(int32_t T, int32_t k, const moe_experts *experts,
+                                     const moe_experts *shared);
+
+/*
  * Weighted combine (architecture sheet: routed outputs weighted by the
  * renormalised gates, plus the always-on shared expert):
  *   y[t] = sum_{j<k} topk_gate[t][j] * rows[pair_to_row[t*k+j]]

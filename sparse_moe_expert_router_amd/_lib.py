@@ -35,7 +35,8 @@ W_BF16, W_AWQ, W_FP8, W_NVFP4, W_AWQ_OM = 0, 1, 2, 3, 4
 OUT_BF16, OUT_F32 = 0, 1
 
 EXPORTS = ["moe_route", "moe_permute", "moe_route_permute", "moe_grouped_ffn", "moe_grouped_ffn_noalloc",
-           "moe_grouped_ffn_noalloc_max_bytes", "moe_layer", "moe_layer_workspace_bytes", "moe_combine",
+           "moe_grouped_ffn_noalloc_max_bytes", "moe_layer", "moe_layer_workspace_bytes",
+           "moe_layer_few", "moe_layer_few_workspace_bytes", "moe_combine",
            "moe_refill_score",
            "moe_refill_finalize", "moe_prune_slice", "moe_router_norm_keep",
            "moe_nvfp4_quantize", "moe_fp8_quantize", "moe_fp8_matmul", "moe_grouped_ffn_a8", "moe_awq_to_output_major", "moe_workspace_bytes", "moe_status_string",
@@ -92,6 +93,7 @@ def lib():
         "moe_layer": [P, i32, P, i32, ctypes.POINTER(_Experts), ctypes.POINTER(_Experts), P, P, P, P, sz, P,
                       P, ctypes.POINTER(P)],
     }
+    sig["moe_layer_few"] = [P, i32, P, i32, ctypes.POINTER(_Experts), ctypes.POINTER(_Experts), P, P, P, P, sz, P]
     for name, args in sig.items():
         f = getattr(L, name)
         f.argtypes = args
@@ -100,6 +102,8 @@ def lib():
     L.moe_grouped_ffn_noalloc_max_bytes.restype = ctypes.c_size_t
     L.moe_layer_workspace_bytes.argtypes = [i32, i32, ctypes.POINTER(_Experts), ctypes.POINTER(_Experts)]
     L.moe_layer_workspace_bytes.restype = ctypes.c_size_t
+    L.moe_layer_few_workspace_bytes.argtypes = [i32, i32, ctypes.POINTER(_Experts), ctypes.POINTER(_Experts)]
+    L.moe_layer_few_workspace_bytes.restype = ctypes.c_size_t
     L.moe_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
     L.moe_workspace_bytes.restype = ctypes.c_size_t
     L.moe_status_string.argtypes = [ctypes.c_int]
@@ -550,6 +554,75 @@ def layer(x, w_router, k: int, bank: dict, shared: dict | None = None, shared_sc
                                         _ptr(y), _ptr(topk_idx), _ptr(buf), n, _stream(), side,
                                         _events_arg(routed_events)))
     return y
+
+
+FEW_MAX_TOKENS = 16
+
+
+class FewTokenLayer:
+    """The whole layer for at most max_tokens (<= 16) tokens in two kernels
+    (moe_layer_few): the banks' structs and the workspace are made once, and a
+    call on x [T, H] enqueues one step on the current stream of x's device and
+    returns (y [T, H] bf16, topk_idx [T, k] int32).
+
+    bank: "bf16", "fp8" or "awq_om"; shared: a "bf16" bank of one expert, or
+    None.  One object serves one stream at a time (its workspace is one)."""
+
+    def __init__(self, w_router, k: int, bank: dict, shared: dict | None = None, max_tokens: int = FEW_MAX_TOKENS,
+                 ws=None):
+        name = "moe_layer_few"
+        E, H, F = bank_dims(bank)
+        _require(w_router.shape == (E, H) and w_router.dtype == torch.bfloat16 and w_router.is_contiguous(), name,
+                 "w_router must be contiguous bf16 [E, H]")
+        self.w_router, self.k, self.bank, self.shared, self.H = w_router, k, bank, shared, H
+        self.max_tokens = max_tokens
+        self.st = experts_struct(bank)
+        self.sh = experts_struct(shared) if shared is not None else None
+        self._st = ctypes.byref(self.st)
+        self._sh = ctypes.byref(self.sh) if self.sh else None
+        need = int(lib().moe_layer_few_workspace_bytes(max_tokens, k, self._st, self._sh))
+        _require(need > 0, name, "at most 16 tokens, a bf16, fp8 or awq_om bank and a bf16 shared expert")
+        buf, self.ws_n = (ws or Workspace(w_router.device)).get(need)
+        self.ws_buf, self._ws = buf, buf.data_ptr()
+        self._router = w_router.data_ptr()
+        self.device = w_router.device
+
+    def __call__(self, x, shared_scale=None, y=None, topk_idx=None):
+        name = "moe_layer_few"
+        T = x.shape[0]
+        _require(x.shape == (T, self.H) and x.dtype == torch.bfloat16 and x.is_contiguous() and
+                 x.device == self.device, name, "x must be contiguous bf16 [T, H] on the weights' device")
+        _require(T <= self.max_tokens, name, f"{T} tokens, at most {self.max_tokens}")
+        if y is None:
+            y = torch.empty_like(x)
+        else:
+            _require(y.shape == x.shape and y.dtype == x.dtype and y.is_contiguous(), name,
+                     "y must be contiguous bf16 [T, H]")
+        if topk_idx is None:
+            topk_idx = torch.empty((T, self.k), dtype=torch.int32, device=x.device)
+        else:
+            _require(topk_idx.shape == (T, self.k) and topk_idx.dtype == torch.int32 and topk_idx.is_contiguous(),
+                     name, "topk_idx must be contiguous int32 [T, k]")
+        scale = None
+        if shared_scale is not None:
+            _require(shared_scale.shape == (T,) and shared_scale.dtype == torch.float32 and
+                     shared_scale.is_contiguous(), name, "shared_scale must be contiguous fp32 [T]")
+            scale = shared_scale.data_ptr()
+        d = _Device(x)
+        d.call(name, x.data_ptr(), T, self._router, self.k, self._st, self._sh, scale, y.data_ptr(),
+               topk_idx.data_ptr(), self._ws, self.ws_n, d.stream)
+        return y, topk_idx
+
+
+def layer_few(x, w_router, k: int, bank: dict, shared: dict | None = None, shared_scale=None, y=None,
+              topk_idx=None, ws=None):
+    """moe_layer_few in one call: (y [T, H] bf16, topk_idx [T, k] int32) of at most 16 tokens; see FewTokenLayer,
+    which keeps what this makes for every call."""
+    if x.shape[0] == 0:
+        return (torch.empty_like(x) if y is None else y,
+                torch.empty((0, k), dtype=torch.int32, device=x.device) if topk_idx is None else topk_idx)
+    few = FewTokenLayer(w_router, k, bank, shared, x.shape[0], _ws(ws, x.device))
+    return few(x, shared_scale, y, topk_idx)
 
 
 def moe_layer(x, w_router, k: int, bank: dict, shared: dict | None = None, shared_scale=None,

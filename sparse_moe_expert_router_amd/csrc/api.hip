@@ -450,6 +450,40 @@ moe_status moe_layer(const uint16_t* x, int32_t T, const uint16_t* w_router, int
     return hip_status(moe::launch_combine(rows, 0, pairs ? nullptr : p2r, gate, T, k, H, srows, shared_scale, y, s));
 }
 
+size_t moe_layer_few_workspace_bytes(int32_t T, int32_t k, const moe_experts* experts, const moe_experts* shared) {
+    moe_status st = MOE_OK;
+    if (T <= 0 || T > moe::kFewMaxT || k < 1 || !bank_ok(experts, &st) || (shared && !bank_ok(shared, &st)) ||
+        !moe::few_supported(experts, shared))
+        return 0;
+    return moe::few_ws_bytes(T, k, experts, shared);
+}
+
+moe_status moe_layer_few(const uint16_t* x, int32_t T, const uint16_t* w_router, int32_t k, const moe_experts* experts,
+                         const moe_experts* shared, const float* shared_scale, uint16_t* y, int32_t* topk_idx, void* ws,
+                         size_t ws_bytes, void* stream) {
+    moe_status st = MOE_OK;
+    if (T < 0 || k < 1) return MOE_ERR_SHAPE;
+    if (!bank_ok(experts, &st)) return st;
+    const int E = experts->num_experts, H = experts->hidden;
+    if (k > E) return MOE_ERR_SHAPE;
+    if (shared) {
+        if (!bank_ok(shared, &st)) return st;
+        if (shared->num_experts != 1 || shared->hidden != H) return MOE_ERR_SHAPE;
+    } else if (shared_scale) {
+        return MOE_ERR_SHAPE;
+    }
+    if (T > moe::kFewMaxT || k > 64 || !moe::few_supported(experts, shared)) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (!x || !w_router || !y) return MOE_ERR_NULL;
+    if (!aligned16(x) || !aligned16(w_router) || !aligned16(y) || (uintptr_t)shared_scale % 4 || (uintptr_t)topk_idx % 4)
+        return MOE_ERR_UNSUPPORTED;
+    if (ws_bytes < moe::few_ws_bytes(T, k, experts, shared)) return MOE_ERR_WORKSPACE;
+    if (!ws) return MOE_ERR_NULL;
+    if (!aligned16(ws)) return MOE_ERR_UNSUPPORTED;
+    return hip_status(moe::launch_layer_few(x, T, w_router, k, experts, shared, shared_scale, y, topk_idx, ws,
+                                            static_cast<hipStream_t>(stream)));
+}
+
 moe_status moe_combine(const void* rows, int32_t rows_dtype, const int32_t* pair_to_row,
                        const float* topk_gate, int32_t T, int32_t k, int32_t H,
                        const uint16_t* shared, const float* shared_scale, uint16_t* y,

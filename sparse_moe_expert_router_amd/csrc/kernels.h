@@ -72,6 +72,14 @@ hipError_t launch_fp8_matmul(const uint8_t* a, const float* sa, const uint8_t* w
 size_t ffn_a8_ws_bytes(int T, int k, int E, int H, int F);
 hipError_t launch_ffn_a8(const FfnArgs& f, void* ws, hipStream_t s);
 
+// ---- the whole layer for few tokens (few.hip)
+constexpr int kFewMaxT = 16;
+bool few_supported(const moe_experts* ex, const moe_experts* sh);
+size_t few_ws_bytes(int T, int k, const moe_experts* ex, const moe_experts* sh);
+hipError_t launch_layer_few(const uint16_t* x, int T, const uint16_t* router, int k, const moe_experts* ex,
+                            const moe_experts* sh, const float* shared_scale, uint16_t* y, int32_t* topk_idx, void* ws,
+                            hipStream_t s);
+
 // ---- combine (combine.hip); pair_to_row == nullptr: row of pair p is p
 hipError_t launch_combine(const void* rows, int rows_f32, const int32_t* pair_to_row,
                           const float* gate, int T, int k, int H, const uint16_t* shared,
