@@ -11,10 +11,10 @@
 //    kernel's counters.
 //  few_experts_kernel: every workgroup selects the top k of every token by
 //    itself from the logits (cheaper than a third launch or a wait), then takes
-//    a ticket.  The first tickets are gate/up workgroups: they stream gate and
-//    up rows, write gate_tj * h (fp32) and count themselves done.  The others
-//    own 8 outputs each: they load their first down rows, wait for the count,
-//    and sum all experts and the shared one in fp32, in a fixed order.
+//    a ticket.  The first tickets are gate/up workgroups: they write gate_tj h
+//    and count themselves done.  The others own 16 outputs each: they do their
+//    part of the shared expert, load their first down rows, wait for the
+//    count, and sum all experts in fp32, in a fixed order.
 //
 // The wait always ends: a workgroup that waits holds a ticket that was given
 // out after all gate/up tickets, so every gate/up workgroup is already running,
@@ -25,8 +25,14 @@
 // stores and loads of it go past them (agent scope, sc1), and a store has
 // completed before its workgroup counts itself done.
 //
-// Weights stream in 16-byte pieces with the non-temporal hint; a piece is 8
-// bf16, 16 E4M3 or 32 4-bit inputs of one column.
+// The products run on the bf16 16 x 16 x 32 MFMA: 16 weight rows x the 16
+// possible tokens, a token that is not routed to the expert reading zeros
+// (without memory traffic).  Weights stream 16 bytes a lane: 8 bf16, 16 E4M3
+// or 32 4-bit inputs of one row, widened to bf16 exactly; their scales are
+// applied to the fp32 sums, so nothing is rounded but h, kept as the sum of
+// two bf16 (16 bits of mantissa), and y.  Against dot products on the vector
+// units this is a fifth of the instructions, which counts twice at one token,
+// where every instruction runs once and is fetched from memory.
 #include "fp8.h"
 #include "ffn_internal.h"
 #include "select.h"
@@ -36,9 +42,9 @@ namespace moe {
 namespace {
 
 constexpr int kFewThreads = 512, kFewWaves = kFewThreads / kWave;
-constexpr int kFewCols = 8;        // outputs of a down workgroup
 constexpr int kFewMaxPairs = kFewMaxT * 64;
 constexpr int kAgent = 16;         // cache policy of buffer accesses: sc1
+constexpr int kStream = 2;         // non-temporal
 
 enum { F_BF16 = 0, F_FP8 = 1, F_AWQ = 2 };
 
@@ -58,336 +64,434 @@ struct FewArgs {
     int gateup_wgs;
     uint32_t* counters;     // [0] tickets, [32 (1 + i)] done, i < 8
     float* logits;          // [T][E]
-    float* hs;              // [T][Fs]
-    float* h;               // [T k][F], rows grouped by expert
+    uint16_t* hs;           // shared h: bf16 parts [2][T][Fs]
+    uint16_t* h;            // gated h of every pair: bf16 parts [2][T k][F]
     uint16_t* y;            // [T][H]
     int32_t* topk_idx;      // [T][k] or nullptr
 };
 
-// Inputs of a 16-byte piece.
+// A unit is what 64 lanes load of 16 rows with 16 bytes each: lane 16 g + l
+// holds row l.  It feeds FRAGS MFMAs; input 8 bytes.. of lane group g in MFMA j:
+//   bf16  (32 inputs):  8 g
+//   E4M3  (64 inputs):  16 g + 8 j
+//   4-bit (128 inputs): 32 j + 8 g   (after an exchange between lane groups)
 template <int FMT>
-struct Piece {
-    static constexpr int N = FMT == F_BF16 ? 8 : FMT == F_FP8 ? 16 : 32;
+struct Unit {
+    static constexpr int IN = FMT == F_BF16 ? 32 : FMT == F_FP8 ? 64 : 128;
+    static constexpr int FRAGS = FMT == F_BF16 ? 1 : FMT == F_FP8 ? 2 : 4;
+    static constexpr int ROW8 = FMT == F_BF16 ? 16 : FMT == F_FP8 ? 8 : 4;  // bytes of 8 inputs
+    __device__ static __forceinline__ int input(int g, int j) {
+        return FMT == F_BF16 ? 8 * g : FMT == F_FP8 ? 16 * g + 8 * j : 32 * j + 8 * g;
+    }
 };
 
-// One piece of a column and what scales it.
+// 16 rows (outputs o0 ..) of one expert's projection.
 template <int FMT>
-struct Weights {
-    uint4 w;
-    float s;        // E4M3: block scale; 4-bit: group scale
-    float z;        // 4-bit: zero point
+struct Rows {
+    __amdgpu_buffer_rsrc_t w, s, z;
+    uint32_t woff, soff, zoff;
+    int O;
+
+    __device__ __forceinline__ void init(const FewProj& p, int e, int O_, int I, int o0, int lane) {
+        using Un = Unit<FMT>;
+        O = O_;
+        const uint32_t rowb = (uint32_t)(I / 8) * Un::ROW8;
+        const size_t row = (size_t)e * O + o0;
+        w = fp8_rsrc(static_cast<const uint8_t*>(p.w) + row * rowb, 16u * rowb);
+        woff = (uint32_t)(lane & 15) * rowb + 16u * (uint32_t)(lane >> 4);
+        if (FMT == F_FP8) {
+            const int KB = I / 128;
+            s = fp8_rsrc(p.bscales + ((size_t)e * (O / 128) + o0 / 128) * KB, (uint32_t)KB * 4u);
+            soff = 0;
+        }
+        if (FMT == F_AWQ) {
+            // scales and zeros of outputs o0 + 4 g .. + 3, one row of them per group of 32 inputs
+            s = fp8_rsrc(p.scales + (size_t)e * (I / 32) * O, (uint32_t)(I / 32) * (uint32_t)O * 2u);
+            z = fp8_rsrc(p.qzeros + (size_t)e * (I / 32) * (O / 8), (uint32_t)(I / 32) * (uint32_t)O / 2u);
+            soff = (uint32_t)(o0 + 4 * (lane >> 4)) * 2u;
+            zoff = (uint32_t)((o0 + 4 * (lane >> 4)) >> 3) * 4u;
+        }
+    }
 };
 
 template <int FMT>
-__device__ __forceinline__ void load_piece(Weights<FMT>& d, const FewProj& p, size_t e, int O, int I, int o, int c) {
-    constexpr int N = Piece<FMT>::N;
-    const size_t row = e * O + o;
-    d.w = ld_stream(reinterpret_cast<const uint4*>(p.w) + row * (I / N) + c);
-    if (FMT == F_FP8) d.s = p.bscales[(e * (O / 128) + o / 128) * (I / 128) + c / 8];
+struct UnitData {
+    i32x4_t w;
+    float s;                      // E4M3
+    u32x2_t gs[4];                // 4-bit: four fp16 scales per group
+    uint32_t gz[4];               // and their zero words
+};
+
+// Unit u; past the end (u >= n) everything reads zero.
+template <int FMT>
+__device__ __forceinline__ void load_unit(UnitData<FMT>& d, const Rows<FMT>& r, int u, int n) {
+    const bool in = u < n;
+    d.w = __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r.w, in ? (int)(r.woff + 64u * u) : (int)kOob, 0, kStream));
+    if (FMT == F_FP8) d.s = buf_load_f32(r.s, in ? (uint32_t)(u / 2) * 4u : kOob, 0);
     if (FMT == F_AWQ) {
-        const size_t grp = e * (I / 32) + c;
-        d.s = f16_to_f32(p.scales[grp * O + o]);
-        const int c8 = o & 7, nib = (c8 & 1) ? 4 + (c8 >> 1) : (c8 >> 1);  // AWQ order of zero words
-        d.z = (float)(((uint32_t)p.qzeros[grp * (O / 8) + (o >> 3)] >> (4 * nib)) & 15u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t so = r.soff + (uint32_t)(4 * u + j) * (uint32_t)r.O * 2u;
+            const uint32_t zo = r.zoff + (uint32_t)(4 * u + j) * (uint32_t)r.O / 2u;
+            d.gs[j] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r.s, in ? (int)so : (int)kOob, 0, 0));
+            d.gz[j] = __builtin_amdgcn_raw_buffer_load_b32(r.z, in ? (int)zo : (int)kOob, 0, 0);
+        }
     }
 }
 
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-
-// Dot of a piece with bf16 inputs x (N / 8 vectors of 8).
+// The MFMA operands of a unit's weights.
 template <int FMT>
-__device__ __forceinline__ float dot_x(const Weights<FMT>& d, const uint4 (&x)[Piece<FMT>::N / 8]) {
-    float acc = 0.0f;
+__device__ __forceinline__ void unit_frags(const UnitData<FMT>& d, bf16x8_t (&a)[Unit<FMT>::FRAGS]) {
+    if constexpr (FMT == F_BF16) {
+        a[0] = __builtin_bit_cast(bf16x8_t, d.w);
+    } else if constexpr (FMT == F_FP8) {
+        a[0] = fp8_to_bf16x8(d.w[0], d.w[1]);
+        a[1] = fp8_to_bf16x8(d.w[2], d.w[3]);
+    } else {
+        // lane group g holds the four words of group g; MFMA j wants word g of
+        // group j in lane group g: a 4 x 4 transposition between lane groups
+        uint32_t q[4] = {(uint32_t)d.w[0], (uint32_t)d.w[1], (uint32_t)d.w[2], (uint32_t)d.w[3]};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const auto t = __builtin_amdgcn_permlane32_swap(q[i], q[i + 2], false, false);
+            q[i] = t[0];
+            q[i + 2] = t[1];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const auto t = __builtin_amdgcn_permlane16_swap(q[i], q[i + 1], false, false);
+            q[i] = t[0];
+            q[i + 1] = t[1];
+        }
+        // 128 + q is exact in bf16 (bits 0x4300 | q); inputs in the order 0,4,1,5,2,6,3,7
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            u32x4_t v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = ((q[j] >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+            a[j] = __builtin_bit_cast(bf16x8_t, v);
+        }
+    }
+}
+
+// Eight bf16 inputs as an MFMA operand beside unit_frags' order.
+template <int FMT>
+__device__ __forceinline__ bf16x8_t input_frag(u32x4_t x) {
+    if (FMT == F_AWQ) {
+        const u32x4_t v = {__builtin_amdgcn_perm(x[2], x[0], 0x05040100u), __builtin_amdgcn_perm(x[2], x[0], 0x07060302u),
+                           __builtin_amdgcn_perm(x[3], x[1], 0x05040100u), __builtin_amdgcn_perm(x[3], x[1], 0x07060302u)};
+        return __builtin_bit_cast(bf16x8_t, v);
+    }
+    return __builtin_bit_cast(bf16x8_t, x);
+}
+
+__device__ __forceinline__ f32x4_t mfma32(bf16x8_t a, bf16x8_t b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// acc += unit . inputs; b[NB][FRAGS]: the inputs are the sum of NB parts.
+template <int FMT, int NB>
+__device__ __forceinline__ void unit_product(f32x4_t& acc, const UnitData<FMT>& d, const bf16x8_t (&b)[NB][Unit<FMT>::FRAGS]) {
+    constexpr int FR = Unit<FMT>::FRAGS;
+    bf16x8_t a[FR];
+    unit_frags<FMT>(d, a);
     if constexpr (FMT == F_BF16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc = dot2_bf16(word(d.w, i), word(x[0], i), acc);
-        return acc;
+        for (int p = 0; p < NB; ++p) acc = mfma32(a[0], b[p][0], acc);
     } else if constexpr (FMT == F_FP8) {
+        f32x4_t v = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // E4M3 is exact in bf16
-            const int w = (int)word(d.w, i);
-            const uint32_t lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
-            const uint32_t hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
-            acc = dot2_bf16(lo, word(x[i / 2], 2 * (i & 1)), acc);
-            acc = dot2_bf16(hi, word(x[i / 2], 2 * (i & 1) + 1), acc);
-        }
-        return acc * d.s;
+        for (int j = 0; j < FR; ++j)
+#pragma unroll
+            for (int p = 0; p < NB; ++p) v = mfma32(a[j], b[p][j], v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(d.s, v[i], acc[i]);
     } else {
-        // 128 + q is exact in bf16 (bits 0x4300 | q): s (sum (128 + q) x - (128 + z) sum x)
-        float sum = 0.0f;
+        // per group of 32: s (sum (128 + q) x - (128 + z) sum x), the second sum by ones
+        const u32x4_t one4 = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+        const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, one4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w = word(d.w, i);
+        for (int j = 0; j < FR; ++j) {
+            f32x4_t v = {}, sum = {};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                // nibbles j and j + 4 with inputs j and j + 4
-                const uint32_t q = ((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u;
-                const uint32_t lo = word(x[i], j / 2), hi = word(x[i], 2 + j / 2);
-                const uint32_t xx = (j & 1) ? __builtin_amdgcn_perm(hi, lo, 0x07060302u) : __builtin_amdgcn_perm(hi, lo, 0x05040100u);
-                acc = dot2_bf16(q, xx, acc);
-                sum = dot2_bf16(0x3F803F80u, xx, sum);
+            for (int p = 0; p < NB; ++p) {
+                v = mfma32(a[j], b[p][j], v);
+                sum = mfma32(ones, b[p][j], sum);
             }
-        }
-        return d.s * (acc - (128.0f + d.z) * sum);
-    }
-}
-
-// Dot of a piece with fp32 inputs h.
-template <int FMT>
-__device__ __forceinline__ float dot_h(const Weights<FMT>& d, const f32x4_t (&h)[Piece<FMT>::N / 4]) {
-    float acc = 0.0f;
-    if constexpr (FMT == F_BF16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w = word(d.w, i);
-            acc = fmaf(__uint_as_float(w << 16), h[i / 2][2 * (i & 1)], acc);
-            acc = fmaf(__uint_as_float(w & 0xFFFF0000u), h[i / 2][2 * (i & 1) + 1], acc);
-        }
-        return acc;
-    } else if constexpr (FMT == F_FP8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int w = (int)word(d.w, i);
-            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
-            acc = fmaf(lo[0], h[i][0], acc);
-            acc = fmaf(lo[1], h[i][1], acc);
-            acc = fmaf(hi[0], h[i][2], acc);
-            acc = fmaf(hi[1], h[i][3], acc);
-        }
-        return acc * d.s;
-    } else {
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w = word(d.w, i);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float v = h[2 * i + j / 4][j & 3];
-                acc = fmaf((float)((w >> (4 * j)) & 15u), v, acc);
-                sum += v;
-            }
-        }
-        return d.s * (acc - d.z * sum);
-    }
-}
-
-// Sum over aligned groups of L lanes, in every lane of the group.
-template <int L>
-__device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-    for (int m = L / 2; m >= 1; m >>= 1) v += __shfl_xor(v, m, kWave);
-    return v;
-}
-
-__device__ __forceinline__ uint4 load_x8(const uint16_t* x, size_t row, int H, int i) {
-    return *reinterpret_cast<const uint4*>(x + row * H + i);
-}
-
-// Gate and up of the columns of one pass of a wave (64 / L columns, L lanes
-// each) for the tokens token(i), i < n: done(i, column, gate, up) is called in
-// the group's lanes.  U pieces of gate and of up are loaded at a time; columns
-// longer than U L pieces add their parts in `part` (LDS of the wave: 2 floats
-// per token and column of the pass).
-template <int FMT, int L, int U, class Tok, class Done>
-__device__ __forceinline__ void gateup_pass(const FewProj& pg, const FewProj& pu, size_t e, int F, int H, int col,
-                                            const uint16_t* x, int n, float* part, Tok token, Done done) {
-    constexpr int N = Piece<FMT>::N, C = kWave / L;
-    const int lane = threadIdx.x & 63, gl = lane % L, gi = lane / L;
-    const int pieces = H / N, o = min(col + gi, F - 1);
-    const bool one = pieces <= U * L;
-    for (int c0 = 0; c0 < pieces; c0 += U * L) {
-        Weights<FMT> wg[U], wu[U];
-        bool in[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = c0 + u * L + gl;
-            in[u] = c < pieces;
-            load_piece<FMT>(wg[u], pg, e, F, H, o, min(c, pieces - 1));
-            load_piece<FMT>(wu[u], pu, e, F, H, o, min(c, pieces - 1));
-        }
-        for (int i = 0; i < n; ++i) {
-            const int t = token(i);
-            float g = 0.0f, v = 0.0f;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = min(c0 + u * L + gl, pieces - 1);
-                uint4 xv[N / 8];
-#pragma unroll
-                for (int q = 0; q < N / 8; ++q) xv[q] = load_x8(x, (size_t)t, H, c * N + 8 * q);
-                const float a = dot_x<FMT>(wg[u], xv), b = dot_x<FMT>(wu[u], xv);
-                g += in[u] ? a : 0.0f;
-                v += in[u] ? b : 0.0f;
-            }
-            g = group_sum<L>(g);
-            v = group_sum<L>(v);
-            if (!one) {
-                float* q = part + (i * C + gi) * 2;
-                if (c0 > 0) {
-                    g += q[0];
-                    v += q[1];
-                }
-                if (gl == 0) {
-                    q[0] = g;
-                    q[1] = v;
-                }
-            }
-            if (c0 + U * L >= pieces) done(i, col + gi, gl == 0 && col + gi < F, g, v);
-        }
-    }
-}
-
-// Lanes of a column: a column of 2560 inputs takes 5 pieces a lane.
-template <int FMT>
-struct GateUpShape {
-    static constexpr int L = FMT == F_BF16 ? 64 : FMT == F_FP8 ? 32 : 16, C = kWave / L, U = 5;
-};
-// Down: 640 inputs take 5 pieces a lane (4-bit: 3).
-template <int FMT>
-struct DownShape {
-    static constexpr int L = FMT == F_BF16 ? 16 : 8, C = kWave / L, U = FMT == F_AWQ ? 3 : 5;
-};
-
-// Logits of one expert for TT tokens: exact bf16 products summed in fp64.
-template <int TT>
-__device__ __forceinline__ void front_logits(const FewArgs& a, int e, int lane) {
-    double acc[TT];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) acc[t] = 0.0;
-    for (int c = lane * 8; c < a.H; c += kWave * 8) {
-        const uint4 r = *reinterpret_cast<const uint4*>(a.router + (size_t)e * a.H + c);
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const uint4 xv = load_x8(a.x, (size_t)min(t, a.T - 1), a.H, c);
+            // zeros of outputs 4 g + i: AWQ order of the word's nibbles
+            const uint32_t zw = d.gz[j] >> ((threadIdx.x & 16) ? 8 : 0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t w = word(r, i), v = word(xv, i);
-                acc[t] = fma((double)__uint_as_float(w << 16), (double)__uint_as_float(v << 16), acc[t]);
-                acc[t] = fma((double)__uint_as_float(w & 0xFFFF0000u), (double)__uint_as_float(v & 0xFFFF0000u), acc[t]);
+                const float z = (float)((zw >> ((i & 1) * 16 + (i >> 1) * 4)) & 15u) + 128.0f;
+                const float s = f16_to_f32((d.gs[j][i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+                acc[i] = fmaf(s, fmaf(-z, sum[i], v[i]), acc[i]);
+            }
+        }
+    }
+}
+
+// LDS reads and writes of the workgroup's waves are ordered; loads from memory
+// stay under way (unlike __syncthreads).
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Gate and up of 16 columns for the tokens whose byte offset of x is `xoff`
+// (kOob: none; one token a lane l), over the wave's share of the units.
+template <int FMT>
+__device__ __forceinline__ void gateup_units(f32x4_t (&acc)[2], const FewProj& pg, const FewProj& pu, int e, int F, int H,
+                                             int o0, __amdgpu_buffer_rsrc_t rx, uint32_t xoff, int part, int parts) {
+    using Un = Unit<FMT>;
+    constexpr int U = FMT == F_AWQ ? 2 : 5, FR = Un::FRAGS;  // units under way
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    Rows<FMT> rg, ru;
+    rg.init(pg, e, F, H, o0, lane);
+    ru.init(pu, e, F, H, o0, lane);
+    const int n = (H + Un::IN - 1) / Un::IN;
+    const int u0 = n * part / parts, u1 = n * (part + 1) / parts;
+    for (int ub = u0; ub < u1; ub += U) {
+        UnitData<FMT> dg[U], du[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            load_unit<FMT>(dg[i], rg, ub + i, u1);
+            load_unit<FMT>(du[i], ru, ub + i, u1);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            bf16x8_t b[1][FR];
+#pragma unroll
+            for (int j = 0; j < FR; ++j) {
+                const uint32_t in = (uint32_t)((ub + i) * Un::IN + Un::input(g, j));
+                const bool ok = ub + i < u1 && xoff != kOob;
+                b[0][j] = input_frag<FMT>(__builtin_bit_cast(
+                    u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rx, ok ? (int)(xoff + 2u * in) : (int)kOob, 0, 0)));
+            }
+            unit_product<FMT, 1>(acc[0], dg[i], b);
+            unit_product<FMT, 1>(acc[1], du[i], b);
+        }
+    }
+}
+
+// h of four neighbouring columns as two bf16 parts, [2][rows][F].
+__device__ __forceinline__ void store_h(__amdgpu_buffer_rsrc_t r, uint32_t row, uint32_t rows, int F, int col, f32x4_t h,
+                                        int policy) {
+    float lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lo[i] = h[i] - bf16_to_f32(f32_to_bf16_bits(h[i]));
+    const u32x2_t a = {pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])};
+    const u32x2_t b = {pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3])};
+    const uint32_t at = (row * (uint32_t)F + (uint32_t)col) * 2u;
+    if (policy) {
+        __builtin_amdgcn_raw_buffer_store_b64(a, r, (int)at, 0, kAgent);
+        __builtin_amdgcn_raw_buffer_store_b64(b, r, (int)(at + rows * (uint32_t)F * 2u), 0, kAgent);
+    } else {
+        __builtin_amdgcn_raw_buffer_store_b64(a, r, (int)at, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(b, r, (int)(at + rows * (uint32_t)F * 2u), 0, 0);
+    }
+}
+
+// A part of 16 outputs of one expert: units part, ... of its F inputs for the
+// tokens whose byte offset of h is `hoff` (kOob: none); lo: bytes to the second
+// bf16 part.  D units are loaded before `ready` is called.
+template <int FMT, int U, class Ready>
+__device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int e, int H, int F, int o0,
+                                           __amdgpu_buffer_rsrc_t rh, uint32_t hoff, uint32_t lo, int part, int parts,
+                                           Ready ready) {
+    using Un = Unit<FMT>;
+    constexpr int FR = Un::FRAGS;
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    Rows<FMT> rd;
+    rd.init(pd, e, H, F, o0, lane);
+    const int n = (F + Un::IN - 1) / Un::IN;
+    const int u0 = n * part / parts, u1 = n * (part + 1) / parts;
+    for (int ub = u0; ub < u1; ub += U) {
+        UnitData<FMT> d[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) load_unit<FMT>(d[i], rd, ub + i, u1);
+        ready();
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            bf16x8_t b[2][FR];
+#pragma unroll
+            for (int j = 0; j < FR; ++j) {
+                const uint32_t in = (uint32_t)((ub + i) * Un::IN + Un::input(g, j));
+                const bool ok = ub + i < u1 && hoff != kOob;
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    b[p][j] = input_frag<FMT>(__builtin_bit_cast(
+                        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rh, ok ? (int)(hoff + 2u * in + p * lo) : (int)kOob, 0,
+                                                                       kAgent)));
+            }
+            unit_product<FMT, 2>(acc, d[i], b);
+        }
+    }
+}
+
+constexpr int kFrontTokens = 4;  // tokens of a wave
+
+// Logits of one expert for kFrontTokens tokens from t0: exact bf16 products summed in fp64.
+__device__ __forceinline__ void front_logits(const FewArgs& a, int e, int t0, int lane) {
+    double acc[kFrontTokens];
+#pragma unroll
+    for (int t = 0; t < kFrontTokens; ++t) acc[t] = 0.0;
+#pragma unroll 5
+    for (int c = lane * 8; c < a.H; c += kWave * 8) {
+        const u32x4_t r = *reinterpret_cast<const u32x4_t*>(a.router + (size_t)e * a.H + c);
+        u32x4_t x[kFrontTokens];
+#pragma unroll
+        for (int t = 0; t < kFrontTokens; ++t)
+            if (t == 0 || t0 + t < a.T) x[t] = *reinterpret_cast<const u32x4_t*>(a.x + (size_t)(t0 + t) * a.H + c);
+#pragma unroll
+        for (int t = 0; t < kFrontTokens; ++t) {
+            if (t > 0 && t0 + t >= a.T) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[t] = fma((double)__uint_as_float(r[i] << 16), (double)__uint_as_float(x[t][i] << 16), acc[t]);
+                acc[t] = fma((double)__uint_as_float(r[i] & 0xFFFF0000u), (double)__uint_as_float(x[t][i] & 0xFFFF0000u), acc[t]);
             }
         }
     }
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
+    for (int t = 0; t < kFrontTokens; ++t) {
+        if (t0 + t >= a.T) break;
         const double s = wave_sum_f64(acc[t]);
-        if (lane == 0 && t < a.T) a.logits[(size_t)t * a.E + e] = (float)s;
+        if (lane == 0) a.logits[(size_t)(t0 + t) * a.E + e] = (float)s;
     }
 }
 
-constexpr int kFrontThreads = 256, kFrontWaves = kFrontThreads / kWave;
-
-// Wave w of the grid: logits of expert w, or columns of the shared expert.
-template <int TT>
-__global__ __launch_bounds__(kFrontThreads) void few_front_kernel(const FewArgs a) {
-    __shared__ float part[kFrontWaves][kFewMaxT * 2];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+// The first Fs / 16 workgroups: 16 columns each of the shared expert's gate and
+// up, the inputs split over the waves; the others: logits, one wave per expert
+// and kFrontTokens tokens.
+__global__ __launch_bounds__(kFewThreads, 4) void few_front_kernel(const FewArgs a) {
+    __shared__ f32x4_t part[kFewWaves][2][kWave];
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), l16 = lane & 15;
     if (blockIdx.x == 0 && threadIdx.x < 9) a.counters[32 * threadIdx.x] = 0;
-    const int w = blockIdx.x * kFrontWaves + wv;
-    if (w < a.E) {
-        front_logits<TT>(a, w, lane);
-    } else if (w - a.E < a.Fs) {
-        using S = GateUpShape<F_BF16>;
-        gateup_pass<F_BF16, S::L, S::U>(
-            a.sgate, a.sup, 0, a.Fs, a.H, w - a.E, a.x, a.T, part[wv], [](int i) { return i; },
-            [&](int i, int col, bool mine, float g, float u) {
-                if (mine) a.hs[(size_t)i * a.Fs + col] = silu(g) * u * (a.shared_scale ? a.shared_scale[i] : 1.0f);
-            });
+    const int sh = a.Fs / 16;
+    if ((int)blockIdx.x < sh) {
+        const int o0 = blockIdx.x * 16;
+        const __amdgpu_buffer_rsrc_t rx = fp8_rsrc(a.x, (uint32_t)a.T * (uint32_t)a.H * 2u);
+        f32x4_t acc[2] = {};
+        gateup_units<F_BF16>(acc, a.sgate, a.sup, 0, a.Fs, a.H, o0, rx, l16 < a.T ? (uint32_t)(l16 * a.H) * 2u : kOob, wv,
+                             kFewWaves);
+        part[wv][0][lane] = acc[0];
+        part[wv][1][lane] = acc[1];
+        __syncthreads();
+        if (wv == 0 && l16 < a.T) {
+            f32x4_t g = acc[0], u = acc[1], h;
+#pragma unroll
+            for (int q = 1; q < kFewWaves; ++q) {
+                g += part[q][0][lane];
+                u += part[q][1][lane];
+            }
+            const float s = a.shared_scale ? a.shared_scale[l16] : 1.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = silu(g[i]) * u[i] * s;
+            store_h(fp8_rsrc(a.hs, (uint32_t)a.T * (uint32_t)a.Fs * 4u), (uint32_t)l16, (uint32_t)a.T, a.Fs,
+                    o0 + 4 * (lane >> 4), h, 0);
+        }
+        return;
     }
+    const int w = (blockIdx.x - sh) * kFewWaves + wv, groups = (a.T + kFrontTokens - 1) / kFrontTokens;
+    const int e = w / groups;
+    if (e < a.E) front_logits(a, e, (w - e * groups) * kFrontTokens, lane);
 }
 
 struct FewLists {
-    int32_t idx[kFewMaxPairs];    // expert of pair t k + j
+    int32_t idx[kFewMaxPairs];              // expert of pair t k + j
     float gate[kFewMaxPairs];
-    int32_t count[kFewMaxPairs];  // pairs of the expert, at its first pair; 0 elsewhere
-    int32_t order[kFewMaxPairs];  // pairs grouped by expert
-    int32_t first[kFewMaxPairs];  // expert slot: first row in `order`; its expert is that of the row's pair
-    int32_t slots;
+    uint16_t slot_of[1024];                 // expert -> slot
+    uint16_t expert[kFewMaxPairs];          // slot -> expert, ascending
+    uint16_t pair[kFewMaxPairs][kFewMaxT];  // slot, token -> pair, or 0xFFFF
+    int32_t wave_slots[kFewWaves];
+    int32_t ticket;
 };
 
 // Selection and grouping, the same in every workgroup: the top k of every
-// token, then the pairs grouped by expert, experts in the order of their first
-// pair, pairs ascending.  P is at most 16 * 64: every pair looks at all others.
-__device__ __forceinline__ void few_select(const FewArgs& a, FewLists& s) {
+// token, then the touched experts in ascending order, and which pair of which
+// token each of them has.  Returns the number of touched experts.
+__device__ __forceinline__ int few_select(const FewArgs& a, FewLists& s) {
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, P = a.T * a.k;
+    for (int e = threadIdx.x; e < 1024; e += kFewThreads) s.slot_of[e] = 0;
+    const int slots_max = min(P, a.E);
+    for (int i = threadIdx.x; i < slots_max * (kFewMaxT / 2); i += kFewThreads)
+        reinterpret_cast<uint32_t*>(s.pair)[i] = 0xFFFFFFFFu;
     for (int t = wv; t < a.T; t += kFewWaves) {
         if (a.E <= 512) select_token<8>(a.logits, (size_t)t, a.E, a.k, a.k, lane, s.idx, nullptr, s.gate);
         else select_token<16>(a.logits, (size_t)t, a.E, a.k, a.k, lane, s.idx, nullptr, s.gate);
     }
-    if (threadIdx.x == 0) s.slots = 0;
     __syncthreads();
-    int lead[kFewMaxPairs / kFewThreads], rank[kFewMaxPairs / kFewThreads];
+    for (int p = threadIdx.x; p < P; p += kFewThreads) s.slot_of[s.idx[p]] = 1;
+    __syncthreads();
+    // thread i numbers experts 2 i and 2 i + 1
+    const uint32_t two = reinterpret_cast<const uint32_t*>(s.slot_of)[threadIdx.x];
+    const uint64_t m0 = __ballot(two & 1u), m1 = __ballot(two >> 16);
+    const uint64_t below = (1ull << lane) - 1;
+    int at = __popcll(m0 & below) + __popcll(m1 & below);
+    if (lane == 0) s.wave_slots[wv] = __popcll(m0) + __popcll(m1);
+    __syncthreads();
+    int slots = 0;
 #pragma unroll
-    for (int r = 0; r < kFewMaxPairs / kFewThreads; ++r) {
-        const int p = threadIdx.x + r * kFewThreads;
-        lead[r] = rank[r] = 0;
-        if (p >= P) continue;
-        const int e = s.idx[p];
-        int before = 0, all = 0, f = p;
-        for (int q = 0; q < P; ++q) {
-            const bool same = s.idx[q] == e;
-            all += same;
-            before += same && q < p;
-            f = same && q < f ? q : f;
-        }
-        lead[r] = f;
-        rank[r] = before;
-        s.count[p] = before == 0 ? all : 0;
+    for (int q = 0; q < kFewWaves; ++q) {
+        if (q < wv) at += s.wave_slots[q];
+        slots += s.wave_slots[q];
+    }
+    if (two & 1u) {
+        s.slot_of[2 * threadIdx.x] = (uint16_t)at;
+        s.expert[at++] = (uint16_t)(2 * threadIdx.x);
+    }
+    if (two >> 16) {
+        s.slot_of[2 * threadIdx.x + 1] = (uint16_t)at;
+        s.expert[at] = (uint16_t)(2 * threadIdx.x + 1);
     }
     __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kFewMaxPairs / kFewThreads; ++r) {
-        const int p = threadIdx.x + r * kFewThreads;
-        if (p >= P) continue;
-        int start = 0, slot = 0;
-        for (int q = 0; q < lead[r]; ++q) {
-            const int c = s.count[q];
-            start += c;
-            slot += c > 0;
-        }
-        s.order[start + rank[r]] = p;
-        if (rank[r] == 0) {
-            s.first[slot] = start;
-            atomicAdd(&s.slots, 1);
-        }
-    }
+    for (int p = threadIdx.x; p < P; p += kFewThreads) s.pair[s.slot_of[s.idx[p]]][p / a.k] = (uint16_t)p;
     __syncthreads();
+    return __builtin_amdgcn_readfirstlane(slots);
 }
 
 template <int FMT>
 __global__ __launch_bounds__(kFewThreads, 4) void few_experts_kernel(const FewArgs a) {
     __shared__ FewLists s;
-    __shared__ float acc[kFewWaves][kFewMaxT][kFewCols];   // down: sums; gate/up: parts of long columns
-    __shared__ int s_ticket, s_ok;
+    __shared__ f32x4_t part[2][kFewWaves][2][kWave];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int l16 = lane & 15, g4 = 4 * (lane >> 4);
     const int P = a.T * a.k;
-    int ticket = 0;
-    if (threadIdx.x == 0) ticket = (int)__hip_atomic_fetch_add(a.counters, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    few_select(a, s);
-    if (threadIdx.x == 0) s_ticket = ticket;
-    __syncthreads();
-    ticket = s_ticket;
-    const int slots = s.slots;
+    if (threadIdx.x == 0)
+        s.ticket = (int)__hip_atomic_fetch_add(a.counters, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int slots = few_select(a, s);
+    const int ticket = __builtin_amdgcn_readfirstlane(s.ticket);
     const __amdgpu_buffer_rsrc_t rh = fp8_rsrc(a.h, (uint32_t)P * (uint32_t)a.F * 4u);
-    auto slot_end = [&](int u) { return u + 1 < slots ? s.first[u + 1] : P; };
 
     if (ticket < a.gateup_wgs) {
-        using S = GateUpShape<FMT>;
-        // passes (expert slot, columns) in contiguous ranges over the waves
-        const int per = (a.F + S::C - 1) / S::C, n = slots * per;
-        const int nw = a.gateup_wgs * kFewWaves, w = ticket * kFewWaves + wv;
-        const int q0 = (int)((int64_t)n * w / nw), q1 = (int)((int64_t)n * (w + 1) / nw);
-        for (int q = q0; q < q1; ++q) {
-            const int u = q / per, col = (q - u * per) * S::C;
-            const int r0 = s.first[u], rows = slot_end(u) - r0;
-            gateup_pass<FMT, S::L, S::U>(
-                a.gate, a.up, (size_t)s.idx[s.order[r0]], a.F, a.H, col, a.x, rows, &acc[wv][0][0],
-                [&](int i) { return s.order[r0 + i] / a.k; },
-                [&](int i, int c, bool mine, float g, float v) {
-                    const float h = silu(g) * v * s.gate[s.order[r0 + i]];
-                    if (mine)
-                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(h), rh,
-                                                              (int)(((uint32_t)(r0 + i) * (uint32_t)a.F + (uint32_t)c) * 4u), 0,
-                                                              kAgent);
-                });
+        // items (expert, 16 columns), the inputs split over the 8 waves and
+        // joined in their order through LDS
+        const __amdgpu_buffer_rsrc_t rx = fp8_rsrc(a.x, (uint32_t)a.T * (uint32_t)a.H * 2u);
+        const int per = a.F / 16, n = slots * per;
+        int buf = 0;
+        for (int q = ticket; q < n; q += a.gateup_wgs, buf ^= 1) {
+            const int u = q / per, o0 = (q - u * per) * 16;
+            const uint32_t p = s.pair[u][l16];
+            const int e = __builtin_amdgcn_readfirstlane((int)s.expert[u]);
+            f32x4_t acc[2] = {};
+            gateup_units<FMT>(acc, a.gate, a.up, e, a.F, a.H, o0, rx, p != 0xFFFFu ? (uint32_t)(l16 * a.H) * 2u : kOob, wv,
+                              kFewWaves);
+            part[buf][wv][0][lane] = acc[0];
+            part[buf][wv][1][lane] = acc[1];
+            lds_barrier();
+            if (wv == 0 && p != 0xFFFFu) {
+                f32x4_t g = acc[0], v = acc[1], h;
+#pragma unroll
+                for (int i = 1; i < kFewWaves; ++i) {
+                    g += part[buf][i][0][lane];
+                    v += part[buf][i][1][lane];
+                }
+                const float gate = s.gate[p];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[i] = silu(g[i]) * v[i] * gate;
+                store_h(rh, p, (uint32_t)P, a.F, o0 + g4, h, 1);
+            }
         }
         if (ticket == 0 && a.topk_idx)
             for (int p = threadIdx.x; p < P; p += kFewThreads) a.topk_idx[p] = s.idx[p];
@@ -398,15 +502,18 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_experts_kernel(const FewAr
         return;
     }
 
-    // ---- down: outputs o0 .. o0 + 7, experts dealt over the waves
-    using S = DownShape<FMT>;
-    constexpr int N = Piece<FMT>::N;
-    const int o0 = (ticket - a.gateup_wgs) * kFewCols;
-    for (int i = threadIdx.x; i < kFewWaves * kFewMaxT * kFewCols; i += kFewThreads) (&acc[0][0][0])[i] = 0.0f;
-    if (threadIdx.x == 0) s_ok = 1;
-    __syncthreads();
-    if (wv == 0) {
+    // ---- outputs o0 .. o0 + 15, experts dealt over the waves
+    const int o0 = (ticket - a.gateup_wgs) * 16;
+    f32x4_t acc = {};
+    if (a.Fs)
+        down_units<F_BF16, 3>(acc, a.sdown, 0, a.H, a.Fs, o0, fp8_rsrc(a.hs, (uint32_t)a.T * (uint32_t)a.Fs * 4u),
+                              l16 < a.T ? (uint32_t)(l16 * a.Fs) * 2u : kOob, (uint32_t)a.T * (uint32_t)a.Fs * 2u, wv,
+                              kFewWaves, [] {});
+    bool waited = false, ok = true;
+    auto ready = [&] {
         // all gate/up workgroups done?  Lanes 0..7 read the eight counts.
+        if (waited) return;
+        waited = true;
         const uint64_t begin = wall_clock64();
         for (;;) {
             uint32_t c = 0;
@@ -415,74 +522,28 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_experts_kernel(const FewAr
             for (int m = 4; m >= 1; m >>= 1) c += __shfl_xor(c, m, kWave);
             if ((uint32_t)__builtin_amdgcn_readfirstlane((int)c) >= (uint32_t)a.gateup_wgs) break;
             if (wall_clock64() - begin > 400000000ull) {  // 4 s of the 100 MHz counter
-                if (lane == 0) s_ok = 0;
+                ok = false;
                 break;
             }
-            __builtin_amdgcn_s_sleep(2);
+            __builtin_amdgcn_s_sleep(8);
         }
-    }
-    __syncthreads();
-    asm volatile("" ::: "memory");
-
-    const int gl = lane % S::L, gi = lane / S::L;
-    const int pieces = a.F / N;
+        asm volatile("" ::: "memory");
+    };
+    constexpr int U = FMT == F_AWQ ? 2 : 10;
     for (int u = wv; u < slots; u += kFewWaves) {
-        const int r0 = s.first[u], rows = slot_end(u) - r0;
-        const size_t e = (size_t)s.idx[s.order[r0]];
-        for (int cb = 0; cb < kFewCols; cb += S::C) {
-            const int o = min(o0 + cb + gi, a.H - 1);
-            for (int c0 = 0; c0 < pieces; c0 += S::U * S::L) {
-                Weights<FMT> w[S::U];
-#pragma unroll
-                for (int i = 0; i < S::U; ++i)
-                    load_piece<FMT>(w[i], a.down, e, a.H, a.F, o, min(c0 + i * S::L + gl, pieces - 1));
-                for (int r = 0; r < rows; ++r) {
-                    float v = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < S::U; ++i) {
-                        const int c = c0 + i * S::L + gl;
-                        f32x4_t h[N / 4];
-#pragma unroll
-                        for (int q = 0; q < N / 4; ++q)
-                            h[q] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                rh, (int)(((uint32_t)(r0 + r) * (uint32_t)a.F + (uint32_t)(min(c, pieces - 1) * N + 4 * q)) * 4u),
-                                0, kAgent));
-                        const float d = dot_h<FMT>(w[i], h);
-                        v += c < pieces ? d : 0.0f;
-                    }
-                    v = group_sum<S::L>(v);
-                    if (gl == 0) acc[wv][s.order[r0 + r] / a.k][cb + gi] += v;
-                }
-            }
-        }
+        const uint32_t p = s.pair[u][l16];
+        const int e = __builtin_amdgcn_readfirstlane((int)s.expert[u]);
+        down_units<FMT, U>(acc, a.down, e, a.H, a.F, o0, rh, p != 0xFFFFu ? p * (uint32_t)a.F * 2u : kOob,
+                           (uint32_t)P * (uint32_t)a.F * 2u, 0, 1, ready);
     }
-    if (a.Fs) {
-        // the shared expert: tokens dealt over the waves
-        using B = DownShape<F_BF16>;
-        const int sl = lane % B::L, si = lane / B::L, sp = a.Fs / 8;
-        for (int t = wv; t < a.T; t += kFewWaves)
-            for (int cb = 0; cb < kFewCols; cb += B::C) {
-                const int o = min(o0 + cb + si, a.H - 1);
-                float v = 0.0f;
-                for (int c = sl; c < sp; c += B::L) {
-                    Weights<F_BF16> w;
-                    load_piece<F_BF16>(w, a.sdown, 0, a.H, a.Fs, o, c);
-                    const f32x4_t* hp = reinterpret_cast<const f32x4_t*>(a.hs + (size_t)t * a.Fs + 8 * c);
-                    const f32x4_t h[2] = {hp[0], hp[1]};
-                    v += dot_h<F_BF16>(w, h);
-                }
-                v = group_sum<B::L>(v);
-                if (sl == 0) acc[wv][t][cb + si] += v;
-            }
-    }
+    if (!ok) acc = f32x4_t{1, 1, 1, 1} * __uint_as_float(0x7FC00000u);
+    part[0][wv][0][lane] = acc;
     __syncthreads();
-    for (int i = threadIdx.x; i < a.T * kFewCols; i += kFewThreads) {
-        const int t = i / kFewCols, c = i % kFewCols;
-        float v = 0.0f;
+    if (wv == 0 && l16 < a.T) {
 #pragma unroll
-        for (int q = 0; q < kFewWaves; ++q) v += acc[q][t][c];
-        if (!s_ok) v = __uint_as_float(0x7FC00000u);
-        if (o0 + c < a.H) a.y[(size_t)t * a.H + o0 + c] = (uint16_t)f32_to_bf16_bits(v);
+        for (int q = 1; q < kFewWaves; ++q) acc += part[0][q][0][lane];
+        *reinterpret_cast<uint2*>(a.y + (size_t)l16 * a.H + o0 + g4) =
+            make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
     }
 }
 
@@ -531,19 +592,20 @@ hipError_t launch_layer_few(const uint16_t* x, int T, const uint16_t* router, in
     w += up256(9 * 32 * 4);
     a.logits = reinterpret_cast<float*>(w);
     w += up256((size_t)T * a.E * 4);
-    a.hs = reinterpret_cast<float*>(w);
+    a.hs = reinterpret_cast<uint16_t*>(w);
     w += up256((size_t)T * a.Fs * 4);
-    a.h = reinterpret_cast<float*>(w);
+    a.h = reinterpret_cast<uint16_t*>(w);
     a.y = y;
     a.topk_idx = topk_idx;
-    a.gateup_wgs = 256;
-    const dim3 front((a.E + a.Fs + kFrontWaves - 1) / kFrontWaves), fb(kFrontThreads);
-    if (T == 1) hipLaunchKernelGGL(few_front_kernel<1>, front, fb, 0, s, a);
-    else if (T <= 4) hipLaunchKernelGGL(few_front_kernel<4>, front, fb, 0, s, a);
-    else hipLaunchKernelGGL(few_front_kernel<16>, front, fb, 0, s, a);
+    // at most two gate/up workgroups a compute unit, and no more than there can be items
+    const long items = (long)(T * k < a.E ? T * k : a.E) * (a.F / 16);
+    a.gateup_wgs = (int)(items < 512 ? items : 512);
+    const int groups = (T + kFrontTokens - 1) / kFrontTokens;
+    const dim3 front(a.Fs / 16 + (a.E * groups + kFewWaves - 1) / kFewWaves), block(kFewThreads);
+    hipLaunchKernelGGL(few_front_kernel, front, block, 0, s, a);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    const dim3 grid(a.gateup_wgs + (a.H + kFewCols - 1) / kFewCols), block(kFewThreads);
+    const dim3 grid(a.gateup_wgs + a.H / 16);
     if (ex->gate.fmt == MOE_W_BF16) hipLaunchKernelGGL(few_experts_kernel<F_BF16>, grid, block, 0, s, a);
     else if (ex->gate.fmt == MOE_W_FP8_BLOCK) hipLaunchKernelGGL(few_experts_kernel<F_FP8>, grid, block, 0, s, a);
     else hipLaunchKernelGGL(few_experts_kernel<F_AWQ>, grid, block, 0, s, a);
