@@ -10,17 +10,21 @@
 //    independent of them, gate/up of the shared expert; also clears the second
 //    kernel's counters.
 //  few_experts_kernel: every workgroup selects the top k of every token by
-//    itself from the logits (cheaper than a third launch or a wait), then takes
-//    a ticket.  The first tickets are gate/up workgroups: they write gate_tj h
-//    and count themselves done.  The others own 16 outputs each: they do their
-//    part of the shared expert, load their first down rows, wait for the
-//    count, and sum all experts in fp32, in a fixed order.
+//    itself from the logits (cheaper than a third launch or a wait).  All of
+//    them then take gate/up items (an expert's columns) until none is left and
+//    write gate_tj h; load their first down rows and do their part of the shared
+//    expert; wait until all items are done; and sum the experts for their share
+//    of the outputs in fp32, in a fixed order.  Up to three workgroups share the
+//    same 16 outputs; the last of them to finish adds the parts, again in a fixed
+//    order.
 //
-// The wait always ends: a workgroup that waits holds a ticket that was given
-// out after all gate/up tickets, so every gate/up workgroup is already running,
-// and those wait for nothing.  (No workgroup needs another to be resident that
-// is not, whatever else runs on the GPU.)  It is bounded all the same, for a
-// workspace that a second call clears meanwhile: then y is NaN.
+// The wait always ends: it begins when no gate/up item is left untaken, so each
+// of them is in the hands of a running workgroup, and those wait for nothing
+// before they have finished it.  (No workgroup needs another to be resident
+// that is not, whatever else runs on the GPU.)  It is bounded all the same, for
+// a workspace that a second call clears meanwhile: then y is NaN.
+// Items are counted in 16 ranges, a cache line each: one counter for all took
+// 20 ns an item, more than the item's work.
 // h passes between compute dies, whose L2s are not coherent within a kernel:
 // stores and loads of it go past them (agent scope, sc1), and a store has
 // completed before its workgroup counts itself done.
@@ -48,6 +52,12 @@ constexpr int kStream = 2;         // non-temporal
 
 enum { F_BF16 = 0, F_FP8 = 1, F_AWQ = 2 };
 
+// Counters, 128 bytes apart: items taken of each range, items done of each
+// range, ranges done; then, 4 bytes apart, finished workgroups of each 16 outputs.
+constexpr int kRanges = 16;
+constexpr int kFewSplits = 3;      // workgroups that can share 16 outputs
+enum FewCount { C_TAKEN = 0, C_DONE = 32 * kRanges, C_ROOT = 64 * kRanges, C_OUT = 64 * kRanges + 32 };
+
 struct FewProj {
     const void* w;          // bf16 [E][O][I], E4M3 codes [E][O][I], 4-bit codes [E][O][I/8]
     const float* bscales;   // E4M3: [E][O/128][I/128]
@@ -61,8 +71,9 @@ struct FewArgs {
     const float* shared_scale;
     FewProj gate, up, down, sgate, sup, sdown;
     int T, H, E, k, F, Fs;  // Fs = 0: no shared expert
-    int gateup_wgs;
-    uint32_t* counters;     // [0] tickets, [32 (1 + i)] done, i < 8
+    int down_wgs;           // workgroups that share the down pass
+    uint32_t* counters;     // see FewCount
+    float* parts;           // [kFewSplits][H / 16][16 x 16] sums of down workgroups
     float* logits;          // [T][E]
     uint16_t* hs;           // shared h: bf16 parts [2][T][Fs]
     uint16_t* h;            // gated h of every pair: bf16 parts [2][T k][F]
@@ -85,31 +96,28 @@ struct Unit {
     }
 };
 
-// 16 rows (outputs o0 ..) of one expert's projection.
+// The 16 rows of a fragment as one lane sees them: its row's bytes and its
+// scales.  Gate/up fragments hold 8 columns of the gate's rows and the same 8 of
+// the up's, so the addresses are per lane.
 template <int FMT>
 struct Rows {
-    __amdgpu_buffer_rsrc_t w, s, z;
-    uint32_t woff, soff, zoff;
+    const uint8_t* w;     // the lane's row, at its piece of unit 0
+    const float* s;       // E4M3: block scales of the expert and output block of rows 4 g
+    const uint16_t* gs;   // 4-bit: scales of rows 4 g .. + 3, one row of O per group of 32 inputs
+    const uint8_t* gz;    // and their zero words
     int O;
 
-    __device__ __forceinline__ void init(const FewProj& p, int e, int O_, int I, int o0, int lane) {
+    // row l % 16 of the fragment is output `o` of p (may differ by lane); rows
+    // 4 g .. + 3 are outputs `o4` .. of p4
+    __device__ __forceinline__ void init(const FewProj& p, int o, const FewProj& p4, int o4, int e, int O_, int I, int lane) {
         using Un = Unit<FMT>;
         O = O_;
         const uint32_t rowb = (uint32_t)(I / 8) * Un::ROW8;
-        const size_t row = (size_t)e * O + o0;
-        w = fp8_rsrc(static_cast<const uint8_t*>(p.w) + row * rowb, 16u * rowb);
-        woff = (uint32_t)(lane & 15) * rowb + 16u * (uint32_t)(lane >> 4);
-        if (FMT == F_FP8) {
-            const int KB = I / 128;
-            s = fp8_rsrc(p.bscales + ((size_t)e * (O / 128) + o0 / 128) * KB, (uint32_t)KB * 4u);
-            soff = 0;
-        }
+        w = static_cast<const uint8_t*>(p.w) + ((size_t)e * O + o) * rowb + 16 * (lane >> 4);
+        if (FMT == F_FP8) s = p4.bscales + ((size_t)e * (O / 128) + o4 / 128) * (I / 128);
         if (FMT == F_AWQ) {
-            // scales and zeros of outputs o0 + 4 g .. + 3, one row of them per group of 32 inputs
-            s = fp8_rsrc(p.scales + (size_t)e * (I / 32) * O, (uint32_t)(I / 32) * (uint32_t)O * 2u);
-            z = fp8_rsrc(p.qzeros + (size_t)e * (I / 32) * (O / 8), (uint32_t)(I / 32) * (uint32_t)O / 2u);
-            soff = (uint32_t)(o0 + 4 * (lane >> 4)) * 2u;
-            zoff = (uint32_t)((o0 + 4 * (lane >> 4)) >> 3) * 4u;
+            gs = p4.scales + (size_t)e * (I / 32) * O + o4;
+            gz = reinterpret_cast<const uint8_t*>(p4.qzeros + (size_t)e * (I / 32) * (O / 8) + o4 / 8);
         }
     }
 };
@@ -122,19 +130,16 @@ struct UnitData {
     uint32_t gz[4];               // and their zero words
 };
 
-// Unit u; past the end (u >= n) everything reads zero.
+// Unit u of the lane's row.
 template <int FMT>
-__device__ __forceinline__ void load_unit(UnitData<FMT>& d, const Rows<FMT>& r, int u, int n) {
-    const bool in = u < n;
-    d.w = __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r.w, in ? (int)(r.woff + 64u * u) : (int)kOob, 0, kStream));
-    if (FMT == F_FP8) d.s = buf_load_f32(r.s, in ? (uint32_t)(u / 2) * 4u : kOob, 0);
+__device__ __forceinline__ void load_unit(UnitData<FMT>& d, const Rows<FMT>& r, int u) {
+    d.w = __builtin_nontemporal_load(reinterpret_cast<const i32x4_t*>(r.w + 64 * (size_t)u));
+    if (FMT == F_FP8) d.s = r.s[u / 2];
     if (FMT == F_AWQ) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t so = r.soff + (uint32_t)(4 * u + j) * (uint32_t)r.O * 2u;
-            const uint32_t zo = r.zoff + (uint32_t)(4 * u + j) * (uint32_t)r.O / 2u;
-            d.gs[j] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r.s, in ? (int)so : (int)kOob, 0, 0));
-            d.gz[j] = __builtin_amdgcn_raw_buffer_load_b32(r.z, in ? (int)zo : (int)kOob, 0, 0);
+            d.gs[j] = *reinterpret_cast<const u32x2_t*>(r.gs + (size_t)(4 * u + j) * r.O);
+            d.gz[j] = *reinterpret_cast<const uint32_t*>(r.gz + (size_t)(4 * u + j) * (r.O / 2));
         }
     }
 }
@@ -191,7 +196,8 @@ __device__ __forceinline__ f32x4_t mfma32(bf16x8_t a, bf16x8_t b, f32x4_t c) {
 
 // acc += unit . inputs; b[NB][FRAGS]: the inputs are the sum of NB parts.
 template <int FMT, int NB>
-__device__ __forceinline__ void unit_product(f32x4_t& acc, const UnitData<FMT>& d, const bf16x8_t (&b)[NB][Unit<FMT>::FRAGS]) {
+__device__ __forceinline__ void unit_product(f32x4_t& acc, const UnitData<FMT>& d, const bf16x8_t (&b)[NB][Unit<FMT>::FRAGS],
+                                             int zshift) {
     constexpr int FR = Unit<FMT>::FRAGS;
     bf16x8_t a[FR];
     unit_frags<FMT>(d, a);
@@ -219,7 +225,7 @@ __device__ __forceinline__ void unit_product(f32x4_t& acc, const UnitData<FMT>& 
                 sum = mfma32(ones, b[p][j], sum);
             }
             // zeros of outputs 4 g + i: AWQ order of the word's nibbles
-            const uint32_t zw = d.gz[j] >> ((threadIdx.x & 16) ? 8 : 0);
+            const uint32_t zw = d.gz[j] >> zshift;  // 8 where rows 4 g .. are outputs 4 .. 7 of their word
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float z = (float)((zw >> ((i & 1) * 16 + (i >> 1) * 4)) & 15u) + 128.0f;
@@ -238,40 +244,69 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// Gate and up of 16 columns for the tokens whose byte offset of x is `xoff`
-// (kOob: none; one token a lane l), over the wave's share of the units.
+// Units of a batch: their weights are under way while the batch before is computed.
 template <int FMT>
-__device__ __forceinline__ void gateup_units(f32x4_t (&acc)[2], const FewProj& pg, const FewProj& pu, int e, int F, int H,
-                                             int o0, __amdgpu_buffer_rsrc_t rx, uint32_t xoff, int part, int parts) {
+constexpr int kBatch = FMT == F_AWQ ? 3 : 10;
+
+// Gate (rows 0..7) and up (rows 8..15) of 8 columns from o0 of expert e.
+template <int FMT>
+__device__ __forceinline__ Rows<FMT> gateup_rows(const FewProj& pg, const FewProj& pu, int e, int F, int H, int o0) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+    Rows<FMT> r;
+    r.init(l16 < 8 ? pg : pu, o0 + (l16 & 7), g < 2 ? pg : pu, o0 + 4 * (g & 1), e, F, H, lane);
+    return r;
+}
+
+template <int FMT>
+__device__ __forceinline__ void load_batch(UnitData<FMT> (&d)[kBatch<FMT>], const Rows<FMT>& r, int ub, int u1) {
+#pragma unroll
+    for (int i = 0; i < kBatch<FMT>; ++i)
+        if (ub + i < u1) load_unit<FMT>(d[i], r, ub + i);
+}
+
+// acc += units ub .. of a batch (those below u1) times x of the tokens whose
+// byte offset is xoff (kOob: none; token l).  `between` issues the next loads:
+// after those of x, which are the first to be waited for.
+template <int FMT, class Between>
+__device__ __forceinline__ void gateup_batch(f32x4_t& acc, const UnitData<FMT> (&d)[kBatch<FMT>], __amdgpu_buffer_rsrc_t rx,
+                                             uint32_t xoff, int ub, int u1, Between between) {
     using Un = Unit<FMT>;
-    constexpr int U = FMT == F_AWQ ? 2 : 5, FR = Un::FRAGS;  // units under way
-    const int lane = threadIdx.x & 63, g = lane >> 4;
-    Rows<FMT> rg, ru;
-    rg.init(pg, e, F, H, o0, lane);
-    ru.init(pu, e, F, H, o0, lane);
-    const int n = (H + Un::IN - 1) / Un::IN;
-    const int u0 = n * part / parts, u1 = n * (part + 1) / parts;
-    for (int ub = u0; ub < u1; ub += U) {
-        UnitData<FMT> dg[U], du[U];
+    constexpr int FR = Un::FRAGS;
+    const int g = (threadIdx.x & 63) >> 4;
+    u32x4_t x[kBatch<FMT>][FR];
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            load_unit<FMT>(dg[i], rg, ub + i, u1);
-            load_unit<FMT>(du[i], ru, ub + i, u1);
+    for (int i = 0; i < kBatch<FMT>; ++i)
+        if (ub + i < u1)
+#pragma unroll
+        for (int j = 0; j < FR; ++j) {
+            const uint32_t in = (uint32_t)((ub + i) * Un::IN + Un::input(g, j));
+            const bool ok = xoff != kOob;
+            x[i][j] = __builtin_bit_cast(
+                u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rx, ok ? (int)(xoff + 2u * in) : (int)kOob, 0, 0));
         }
+    __builtin_amdgcn_sched_barrier(0);
+    between();
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            bf16x8_t b[1][FR];
+    for (int i = 0; i < kBatch<FMT>; ++i) if (ub + i < u1) {
+        bf16x8_t b[1][FR];
 #pragma unroll
-            for (int j = 0; j < FR; ++j) {
-                const uint32_t in = (uint32_t)((ub + i) * Un::IN + Un::input(g, j));
-                const bool ok = ub + i < u1 && xoff != kOob;
-                b[0][j] = input_frag<FMT>(__builtin_bit_cast(
-                    u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rx, ok ? (int)(xoff + 2u * in) : (int)kOob, 0, 0)));
-            }
-            unit_product<FMT, 1>(acc[0], dg[i], b);
-            unit_product<FMT, 1>(acc[1], du[i], b);
-        }
+        for (int j = 0; j < FR; ++j) b[0][j] = input_frag<FMT>(x[i][j]);
+        unit_product<FMT, 1>(acc, d[i], b, 8 * (g & 1));
     }
+}
+
+// The join of n waves' parts of such a fragment: lanes g < 2 get silu(gate) *
+// up of columns o0 + 4 g .. of token l.
+__device__ __forceinline__ f32x4_t gateup_join(const f32x4_t (*part)[kWave], int n, int lane) {
+    f32x4_t v = part[0][lane], u = part[0][lane ^ 32], h;
+    for (int q = 1; q < n; ++q) {
+        v += part[q][lane];
+        u += part[q][lane ^ 32];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = silu(v[i]) * u[i];
+    return h;
 }
 
 // h of four neighbouring columns as two bf16 parts, [2][rows][F].
@@ -292,39 +327,58 @@ __device__ __forceinline__ void store_h(__amdgpu_buffer_rsrc_t r, uint32_t row, 
     }
 }
 
-// A part of 16 outputs of one expert: units part, ... of its F inputs for the
-// tokens whose byte offset of h is `hoff` (kOob: none); lo: bytes to the second
-// bf16 part.  D units are loaded before `ready` is called.
-template <int FMT, int U, class Ready>
-__device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int e, int H, int F, int o0,
-                                           __amdgpu_buffer_rsrc_t rh, uint32_t hoff, uint32_t lo, int part, int parts,
-                                           Ready ready) {
+// Units v0 .. v1 of the F inputs of a list of experts, one after another, into
+// 16 outputs from o0.  expert(slot), hoff(slot): the slot's expert and the byte
+// offset of the lane's token's h (kOob: not routed to it); lo: bytes to the
+// second bf16 part of h.  `ready` is called once the first U units are under way.
+template <int FMT, int U, class Expert, class Hoff, class Ready>
+__device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int H, int F, int o0, __amdgpu_buffer_rsrc_t rh,
+                                           uint32_t lo, int v0, int v1, Expert expert, Hoff hoff, Ready ready) {
     using Un = Unit<FMT>;
     constexpr int FR = Un::FRAGS;
-    const int lane = threadIdx.x & 63, g = lane >> 4;
-    Rows<FMT> rd;
-    rd.init(pd, e, H, F, o0, lane);
-    const int n = (F + Un::IN - 1) / Un::IN;
-    const int u0 = n * part / parts, u1 = n * (part + 1) / parts;
-    for (int ub = u0; ub < u1; ub += U) {
-        UnitData<FMT> d[U];
+    const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+    const int n = F / Un::IN;
+    UnitData<FMT> d[U], dn[U];
+    auto load = [&](int vb) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) load_unit<FMT>(d[i], rd, ub + i, u1);
-        ready();
+        for (int i = 0; i < U; ++i) if (vb + i < v1) {
+            const int v = vb + i, slot = v / n;
+            Rows<FMT> r;
+            r.init(pd, o0 + l16, pd, o0 + 4 * g, expert(slot), H, F, lane);
+            load_unit<FMT>(dn[i], r, v - slot * n);
+        }
+    };
+    load(v0);
+    ready();
+    for (int vb = v0; vb < v1; vb += U) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            bf16x8_t b[2][FR];
+        for (int i = 0; i < U; ++i) d[i] = dn[i];
+        u32x4_t h[U][2][FR];  // before the next weights: a wave's loads return in order
+#pragma unroll
+        for (int i = 0; i < U; ++i) if (vb + i < v1) {
+            const int v = vb + i, slot = v / n;
+            const uint32_t at = hoff(slot);
 #pragma unroll
             for (int j = 0; j < FR; ++j) {
-                const uint32_t in = (uint32_t)((ub + i) * Un::IN + Un::input(g, j));
-                const bool ok = ub + i < u1 && hoff != kOob;
+                const uint32_t in = (uint32_t)((v - slot * n) * Un::IN + Un::input(g, j));
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
-                    b[p][j] = input_frag<FMT>(__builtin_bit_cast(
-                        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rh, ok ? (int)(hoff + 2u * in + p * lo) : (int)kOob, 0,
-                                                                       kAgent)));
+                    h[i][p][j] = __builtin_bit_cast(
+                        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rh, at != kOob ? (int)(at + 2u * in + p * lo) : (int)kOob,
+                                                                       0, 0));
             }
-            unit_product<FMT, 2>(acc, d[i], b);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        load(vb + U);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < U; ++i) if (vb + i < v1) {
+            bf16x8_t b[2][FR];
+#pragma unroll
+            for (int j = 0; j < FR; ++j)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) b[p][j] = input_frag<FMT>(h[i][p][j]);
+            unit_product<FMT, 2>(acc, d[i], b, 8 * (g & 1));
         }
     }
 }
@@ -344,8 +398,7 @@ __device__ __forceinline__ void front_logits(const FewArgs& a, int e, int t0, in
         for (int t = 0; t < kFrontTokens; ++t)
             if (t == 0 || t0 + t < a.T) x[t] = *reinterpret_cast<const u32x4_t*>(a.x + (size_t)(t0 + t) * a.H + c);
 #pragma unroll
-        for (int t = 0; t < kFrontTokens; ++t) {
-            if (t > 0 && t0 + t >= a.T) break;
+        for (int t = 0; t < kFrontTokens; ++t) if (t == 0 || t0 + t < a.T) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 acc[t] = fma((double)__uint_as_float(r[i] << 16), (double)__uint_as_float(x[t][i] << 16), acc[t]);
@@ -354,40 +407,44 @@ __device__ __forceinline__ void front_logits(const FewArgs& a, int e, int t0, in
         }
     }
 #pragma unroll
-    for (int t = 0; t < kFrontTokens; ++t) {
-        if (t0 + t >= a.T) break;
+    for (int t = 0; t < kFrontTokens; ++t) if (t0 + t < a.T) {
         const double s = wave_sum_f64(acc[t]);
         if (lane == 0) a.logits[(size_t)(t0 + t) * a.E + e] = (float)s;
     }
 }
 
-// The first Fs / 16 workgroups: 16 columns each of the shared expert's gate and
+// The first Fs / 8 workgroups: 8 columns each of the shared expert's gate and
 // up, the inputs split over the waves; the others: logits, one wave per expert
 // and kFrontTokens tokens.
-__global__ __launch_bounds__(kFewThreads, 4) void few_front_kernel(const FewArgs a) {
-    __shared__ f32x4_t part[kFewWaves][2][kWave];
+__global__ __launch_bounds__(kFewThreads, 2) void few_front_kernel(const FewArgs a) {
+    __shared__ f32x4_t part[kFewWaves][kWave];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), l16 = lane & 15;
-    if (blockIdx.x == 0 && threadIdx.x < 9) a.counters[32 * threadIdx.x] = 0;
-    const int sh = a.Fs / 16;
+    if (blockIdx.x == 0) {
+        for (int c = threadIdx.x; c < C_OUT + a.H / 16; c += kFewThreads) a.counters[c] = 0;
+    }
+    const int sh = a.Fs / 8;
     if ((int)blockIdx.x < sh) {
-        const int o0 = blockIdx.x * 16;
+        const int o0 = blockIdx.x * 8;
         const __amdgpu_buffer_rsrc_t rx = fp8_rsrc(a.x, (uint32_t)a.T * (uint32_t)a.H * 2u);
-        f32x4_t acc[2] = {};
-        gateup_units<F_BF16>(acc, a.sgate, a.sup, 0, a.Fs, a.H, o0, rx, l16 < a.T ? (uint32_t)(l16 * a.H) * 2u : kOob, wv,
-                             kFewWaves);
-        part[wv][0][lane] = acc[0];
-        part[wv][1][lane] = acc[1];
-        __syncthreads();
-        if (wv == 0 && l16 < a.T) {
-            f32x4_t g = acc[0], u = acc[1], h;
+        f32x4_t acc = {};
+        const Rows<F_BF16> r = gateup_rows<F_BF16>(a.sgate, a.sup, 0, a.Fs, a.H, o0);
+        const int n = a.H / Unit<F_BF16>::IN, u0 = n * wv / kFewWaves, u1 = n * (wv + 1) / kFewWaves;
+        UnitData<F_BF16> d[kBatch<F_BF16>], dn[kBatch<F_BF16>];
+        load_batch<F_BF16>(dn, r, u0, u1);
+        for (int ub = u0; ub < u1; ub += kBatch<F_BF16>) {
 #pragma unroll
-            for (int q = 1; q < kFewWaves; ++q) {
-                g += part[q][0][lane];
-                u += part[q][1][lane];
-            }
+            for (int i = 0; i < kBatch<F_BF16>; ++i) d[i] = dn[i];
+            gateup_batch<F_BF16>(acc, d, rx, l16 < a.T ? (uint32_t)(l16 * a.H) * 2u : kOob, ub, u1, [&] {
+                if (ub + kBatch<F_BF16> < u1) load_batch<F_BF16>(dn, r, ub + kBatch<F_BF16>, u1);
+            });
+        }
+        part[wv][lane] = acc;
+        __syncthreads();
+        if (wv == 0 && lane < 32 && l16 < a.T) {
+            f32x4_t h = gateup_join(part, kFewWaves, lane);
             const float s = a.shared_scale ? a.shared_scale[l16] : 1.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = silu(g[i]) * u[i] * s;
+            for (int i = 0; i < 4; ++i) h[i] *= s;
             store_h(fp8_rsrc(a.hs, (uint32_t)a.T * (uint32_t)a.Fs * 4u), (uint32_t)l16, (uint32_t)a.T, a.Fs,
                     o0 + 4 * (lane >> 4), h, 0);
         }
@@ -405,8 +462,66 @@ struct FewLists {
     uint16_t expert[kFewMaxPairs];          // slot -> expert, ascending
     uint16_t pair[kFewMaxPairs][kFewMaxT];  // slot, token -> pair, or 0xFFFF
     int32_t wave_slots[kFewWaves];
-    int32_t ticket;
+    int32_t next[2], left;
+    int32_t mine[kRanges];                  // items of each range this workgroup has done
+    uint32_t lane_max[kFewWaves][kWave];    // the selection's, one of each per wave
+    uint2 cand[kFewWaves][kWave];
 };
+
+// Top k of token t's E <= 512 logits by one wave.  Lane i holds experts 8 i ..
+// 8 i + 7.  Fewer than k of the lanes' largest logits lie above some lane's
+// largest only if that is at least the k-th largest logit of all; the smallest
+// such bounds the top k from below, usually leaving little more than k
+// candidates, and each finds its rank by comparing itself with the others.
+// Against k rounds of a wave-wide maximum this has no long chain, and a third
+// of the instructions, which every workgroup of the launch executes.
+__device__ __forceinline__ void few_topk(const FewArgs& a, FewLists& s, int t, u32x4_t l0, u32x4_t l1, int wv, int lane) {
+    uint32_t key[8], m = 0;
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+        key[v] = 8 * lane + v < a.E ? expert_key(__uint_as_float(v < 4 ? l0[v & 3] : l1[v & 3])) : 0u;
+        m = max(m, key[v]);
+    }
+    s.lane_max[wv][lane] = m;
+    __builtin_amdgcn_wave_barrier();
+    int above = 0;
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+        const uint4 o = reinterpret_cast<const uint4*>(s.lane_max[wv])[i];
+        above += (o.x > m) + (o.y > m) + (o.z > m) + (o.w > m);
+    }
+    const uint32_t least = ~wave_max_u32(above < a.k ? ~m : 0u);
+    int n = 0;
+    const uint64_t below = (1ull << lane) - 1;
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+        const bool is = key[v] >= least && key[v] != 0;
+        const uint64_t b = __ballot(is);
+        const int at = n + __popcll(b & below);
+        if (is && at < kWave) s.cand[wv][at] = make_uint2(key[v], (uint32_t)(8 * lane + v));
+        n += __popcll(b);
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (n > kWave) {  // many equal logits, or k near E: the rounds
+        select_token<8>(a.logits, (size_t)t, a.E, a.k, a.k, lane, s.idx, nullptr, s.gate);
+        return;
+    }
+    const uint2 mine = lane < n ? s.cand[wv][lane] : make_uint2(0u, 0xFFFFFFFFu);
+    int rank = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const uint2 o = s.cand[wv][i];
+        rank += o.x > mine.x || (o.x == mine.x && o.y < mine.y);
+    }
+    const bool in = lane < n && rank < a.k;
+    const float top = float_from_order_key(wave_max_u32(m));
+    const float p = in ? expf(float_from_order_key(mine.x) - top) : 0.0f;
+    const float z = wave_sum_f32(p);
+    if (in) {
+        s.idx[t * a.k + rank] = (int32_t)mine.y;
+        s.gate[t * a.k + rank] = p / z;
+    }
+}
 
 // Selection and grouping, the same in every workgroup: the top k of every
 // token, then the touched experts in ascending order, and which pair of which
@@ -417,20 +532,36 @@ __device__ __forceinline__ int few_select(const FewArgs& a, FewLists& s) {
     const int slots_max = min(P, a.E);
     for (int i = threadIdx.x; i < slots_max * (kFewMaxT / 2); i += kFewThreads)
         reinterpret_cast<uint32_t*>(s.pair)[i] = 0xFFFFFFFFu;
-    for (int t = wv; t < a.T; t += kFewWaves) {
-        if (a.E <= 512) select_token<8>(a.logits, (size_t)t, a.E, a.k, a.k, lane, s.idx, nullptr, s.gate);
-        else select_token<16>(a.logits, (size_t)t, a.E, a.k, a.k, lane, s.idx, nullptr, s.gate);
+    static_assert(kFewMaxT == 2 * kFewWaves, "two tokens a wave");
+    if (a.E <= 512) {
+        u32x4_t l[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = min(wv + i * kFewWaves, a.T - 1);
+            const __amdgpu_buffer_rsrc_t rl = fp8_rsrc(a.logits + (size_t)t * a.E, (uint32_t)a.E * 4u);
+            l[i][0] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rl, lane * 32, 0, 0));
+            l[i][1] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rl, lane * 32 + 16, 0, 0));
+        }
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            if (wv + i * kFewWaves < a.T) few_topk(a, s, wv + i * kFewWaves, l[0][0], l[0][1], wv, lane);
+            l[0][0] = l[1][0];
+            l[0][1] = l[1][1];
+        }
+    } else {
+        for (int t = wv; t < a.T; t += kFewWaves)
+            select_token<16>(a.logits, (size_t)t, a.E, a.k, a.k, lane, s.idx, nullptr, s.gate);
     }
-    __syncthreads();
+    lds_barrier();
     for (int p = threadIdx.x; p < P; p += kFewThreads) s.slot_of[s.idx[p]] = 1;
-    __syncthreads();
+    lds_barrier();
     // thread i numbers experts 2 i and 2 i + 1
     const uint32_t two = reinterpret_cast<const uint32_t*>(s.slot_of)[threadIdx.x];
     const uint64_t m0 = __ballot(two & 1u), m1 = __ballot(two >> 16);
     const uint64_t below = (1ull << lane) - 1;
     int at = __popcll(m0 & below) + __popcll(m1 & below);
     if (lane == 0) s.wave_slots[wv] = __popcll(m0) + __popcll(m1);
-    __syncthreads();
+    lds_barrier();
     int slots = 0;
 #pragma unroll
     for (int q = 0; q < kFewWaves; ++q) {
@@ -445,105 +576,232 @@ __device__ __forceinline__ int few_select(const FewArgs& a, FewLists& s) {
         s.slot_of[2 * threadIdx.x + 1] = (uint16_t)at;
         s.expert[at] = (uint16_t)(2 * threadIdx.x + 1);
     }
-    __syncthreads();
+    lds_barrier();
     for (int p = threadIdx.x; p < P; p += kFewThreads) s.pair[s.slot_of[s.idx[p]]][p / a.k] = (uint16_t)p;
-    __syncthreads();
+    lds_barrier();
     return __builtin_amdgcn_readfirstlane(slots);
 }
 
+// Sizes of the ranges of n items: the first n % kRanges have one more.
+__device__ __forceinline__ int range_size(int n, int r) { return n / kRanges + (r < n % kRanges); }
+__device__ __forceinline__ int range_first(int n, int r) { return n / kRanges * r + min(r, n % kRanges); }
+
+// Takes items for a workgroup (one wave): take() asks for the next of range `r`,
+// take_result() is that item, or one of any range that has some left (r becomes
+// that one), or -1 when all are taken.  They are apart because a wave's loads
+// return in order: asked for before the next weights are, the answer does not
+// wait for those.
+__device__ __forceinline__ uint32_t take(const FewArgs& a, int r, int lane) {
+    uint32_t v = 0;
+    if (lane == 0)
+        v = __hip_atomic_fetch_add(a.counters + C_TAKEN + 32 * r, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return v;
+}
+
+__device__ __forceinline__ int take_result(const FewArgs& a, int n, int& r, uint32_t v, int lane) {
+    for (;;) {
+        const uint32_t got = (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+        if (got < (uint32_t)range_size(n, r)) return range_first(n, r) + (int)got;
+        uint32_t c = 0xFFFFFFFFu;
+        if (lane < kRanges)
+            c = __hip_atomic_load(a.counters + C_TAKEN + 32 * lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const uint64_t left = __ballot(lane < kRanges && c < (uint32_t)range_size(n, lane));
+        if (left == 0) return -1;
+        // the next range after r, so that the searchers spread
+        const uint64_t after = left & ~((2ull << r) - 1);
+        r = __ffsll((long long)(after ? after : left)) - 1;
+        v = take(a, r, lane);
+    }
+}
+
 template <int FMT>
-__global__ __launch_bounds__(kFewThreads, 4) void few_experts_kernel(const FewArgs a) {
+__global__ __launch_bounds__(kFewThreads, 2) void few_experts_kernel(const FewArgs a) {
     __shared__ FewLists s;
-    __shared__ f32x4_t part[2][kFewWaves][2][kWave];
+    __shared__ f32x4_t part[2][kFewWaves][kWave];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int l16 = lane & 15, g4 = 4 * (lane >> 4);
     const int P = a.T * a.k;
-    if (threadIdx.x == 0)
-        s.ticket = (int)__hip_atomic_fetch_add(a.counters, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (threadIdx.x < kRanges) s.mine[threadIdx.x] = 0;
+    int r = blockIdx.x % kRanges;
+    uint32_t taken = 0;
+    if (wv == 0) taken = take(a, r, lane);
     const int slots = few_select(a, s);
-    const int ticket = __builtin_amdgcn_readfirstlane(s.ticket);
     const __amdgpu_buffer_rsrc_t rh = fp8_rsrc(a.h, (uint32_t)P * (uint32_t)a.F * 4u);
 
-    if (ticket < a.gateup_wgs) {
-        // items (expert, 16 columns), the inputs split over the 8 waves and
-        // joined in their order through LDS
+    // ---- gate/up.  An item is 8 columns of an expert for each group of `ks`
+    // waves, which split the inputs and are joined in their order through LDS:
+    // few items are cut finely, many keep a wave on longer runs.
+    const int cols8 = slots * (a.F / 8);
+    const int ks = cols8 >= 4096 ? 2 : cols8 >= 1024 ? 4 : 8, cw = kFewWaves / ks;
+    const int per = (a.F / 8 + cw - 1) / cw, items = slots * per;
+    const int ranges = min(items, kRanges);
+    {
+        using Un = Unit<FMT>;
+        constexpr int U = kBatch<FMT>;
         const __amdgpu_buffer_rsrc_t rx = fp8_rsrc(a.x, (uint32_t)a.T * (uint32_t)a.H * 2u);
-        const int per = a.F / 16, n = slots * per;
-        int buf = 0;
-        for (int q = ticket; q < n; q += a.gateup_wgs, buf ^= 1) {
-            const int u = q / per, o0 = (q - u * per) * 16;
-            const uint32_t p = s.pair[u][l16];
-            const int e = __builtin_amdgcn_readfirstlane((int)s.expert[u]);
-            f32x4_t acc[2] = {};
-            gateup_units<FMT>(acc, a.gate, a.up, e, a.F, a.H, o0, rx, p != 0xFFFFu ? (uint32_t)(l16 * a.H) * 2u : kOob, wv,
-                              kFewWaves);
-            part[buf][wv][0][lane] = acc[0];
-            part[buf][wv][1][lane] = acc[1];
-            lds_barrier();
-            if (wv == 0 && p != 0xFFFFu) {
-                f32x4_t g = acc[0], v = acc[1], h;
+        const int n = a.H / Un::IN, part_of = wv % ks, group = wv / ks;
+        const int u0 = n * part_of / ks, u1 = n * (part_of + 1) / ks;
+        if (wv == 0) {
+            const int first = take_result(a, items, r, taken, lane);
+            const int second = first < 0 ? -1 : take_result(a, items, r, take(a, r, lane), lane);
+            if (lane == 0) {
+                s.next[0] = first;
+                s.next[1] = second;
+            }
+        }
+        lds_barrier();
+        int item = __builtin_amdgcn_readfirstlane(s.next[0]), next = __builtin_amdgcn_readfirstlane(s.next[1]);
+        lds_barrier();
+        // columns past F (F / 8 no multiple of the groups) repeat the last ones and are not stored
+        auto first_col = [&](int it) { return (it % per * cw + group) * 8; };
+        auto rows_of = [&](int it) {
+            const int e = __builtin_amdgcn_readfirstlane((int)s.expert[it / per]);
+            return gateup_rows<FMT>(a.gate, a.up, e, a.F, a.H, min(first_col(it), a.F - 8));
+        };
+        UnitData<FMT> d[U], dn[U];
+        Rows<FMT> rows;
+        if (item >= 0) {
+            rows = rows_of(item);
+            load_batch<FMT>(dn, rows, u0, u1);
+        }
+        for (int buf = 0; item >= 0; buf ^= 1) {
+            const uint32_t p = s.pair[item / per][l16];
+            const uint32_t xoff = p != 0xFFFFu ? (uint32_t)(l16 * a.H) * 2u : kOob;
+            f32x4_t acc = {};
+            if (wv == 0 && next >= 0) taken = take(a, r, lane);
+            Rows<FMT> rn = rows;
+            if (next >= 0) rn = rows_of(next);
+            for (int ub = u0; ub < u1; ub += U) {
 #pragma unroll
-                for (int i = 1; i < kFewWaves; ++i) {
-                    g += part[buf][i][0][lane];
-                    v += part[buf][i][1][lane];
+                for (int i = 0; i < U; ++i) d[i] = dn[i];
+                gateup_batch<FMT>(acc, d, rx, xoff, ub, u1, [&] {
+                    if (ub + U < u1) load_batch<FMT>(dn, rows, ub + U, u1);
+                    else if (next >= 0) load_batch<FMT>(dn, rn, u0, u1);
+                });
+            }
+            part[buf][wv][lane] = acc;
+            if (wv == 0) {
+                // (taken, so done before this workgroup waits)
+                const int then = next < 0 ? -1 : take_result(a, items, r, taken, lane);
+                if (lane == 0) {
+                    s.next[buf] = then;
+                    int q = 0;
+                    while (q + 1 < ranges && item >= range_first(items, q + 1)) ++q;
+                    ++s.mine[q];
                 }
+            }
+            lds_barrier();
+            const int then = __builtin_amdgcn_readfirstlane(s.next[buf]);
+            if (part_of == 0 && lane < 32 && p != 0xFFFFu && first_col(item) < a.F) {
+                f32x4_t h = gateup_join(&part[buf][wv], ks, lane);
                 const float gate = s.gate[p];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) h[i] = silu(g[i]) * v[i] * gate;
-                store_h(rh, p, (uint32_t)P, a.F, o0 + g4, h, 1);
+                for (int i = 0; i < 4; ++i) h[i] *= gate;
+                store_h(rh, p, (uint32_t)P, a.F, first_col(item) + g4, h, 1);
             }
+            item = next;
+            next = then;
+            rows = rn;
         }
-        if (ticket == 0 && a.topk_idx)
+        if (blockIdx.x == 0 && a.topk_idx)
             for (int p = threadIdx.x; p < P; p += kFewThreads) a.topk_idx[p] = s.idx[p];
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the stores have completed
-        __syncthreads();
-        if (threadIdx.x == 0)
-            __hip_atomic_fetch_add(a.counters + 32 * (1 + ticket % 8), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        return;
+        lds_barrier();
+        if (wv == 0 && lane < ranges && s.mine[lane] > 0) {
+            const uint32_t mine = (uint32_t)s.mine[lane];
+            const uint32_t before =
+                __hip_atomic_fetch_add(a.counters + C_DONE + 32 * lane, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (before + mine == (uint32_t)range_size(items, lane))
+                __hip_atomic_fetch_add(a.counters + C_ROOT, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
     }
 
-    // ---- outputs o0 .. o0 + 15, experts dealt over the waves
-    const int o0 = (ticket - a.gateup_wgs) * 16;
-    f32x4_t acc = {};
-    if (a.Fs)
-        down_units<F_BF16, 3>(acc, a.sdown, 0, a.H, a.Fs, o0, fp8_rsrc(a.hs, (uint32_t)a.T * (uint32_t)a.Fs * 4u),
-                              l16 < a.T ? (uint32_t)(l16 * a.Fs) * 2u : kOob, (uint32_t)a.T * (uint32_t)a.Fs * 2u, wv,
-                              kFewWaves, [] {});
-    bool waited = false, ok = true;
+    // ---- down.  The units of all experts for 16 outputs, and those of all
+    // groups of 16 outputs one after another, are one list, of which every
+    // workgroup takes an equal run (at least half a group's units, so at most
+    // kFewSplits share a group), and of its part of a group every wave.
+    if ((int)blockIdx.x >= a.down_wgs) return;
+    const int nc = a.H / 16, n = slots * (a.F / Unit<FMT>::IN);
+    const int64_t all = (int64_t)nc * n;
+    auto run_begin = [&](int b) { return all * b / a.down_wgs; };
+    const int64_t v0 = run_begin(blockIdx.x), v1 = run_begin(blockIdx.x + 1);
+    bool first = true, ok = true;
     auto ready = [&] {
-        // all gate/up workgroups done?  Lanes 0..7 read the eight counts.
-        if (waited) return;
-        waited = true;
-        const uint64_t begin = wall_clock64();
-        for (;;) {
-            uint32_t c = 0;
-            if (lane < 8) c = __hip_atomic_load(a.counters + 32 * (1 + lane), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-            for (int m = 4; m >= 1; m >>= 1) c += __shfl_xor(c, m, kWave);
-            if ((uint32_t)__builtin_amdgcn_readfirstlane((int)c) >= (uint32_t)a.gateup_wgs) break;
-            if (wall_clock64() - begin > 400000000ull) {  // 4 s of the 100 MHz counter
-                ok = false;
-                break;
+        if (!first) return;
+        first = false;
+        // all ranges of items done?
+        if (wv == 0) {
+            const uint64_t begin = wall_clock64();
+            for (;;) {
+                const uint32_t v = __hip_atomic_load(a.counters + C_ROOT, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                if ((uint32_t)__builtin_amdgcn_readfirstlane((int)v) >= (uint32_t)ranges) break;
+                if (wall_clock64() - begin > 400000000ull) {  // 4 s of the 100 MHz counter
+                    ok = false;
+                    break;
+                }
+                __builtin_amdgcn_s_sleep(4);
             }
-            __builtin_amdgcn_s_sleep(8);
+            // what this compute unit and its die have cached of h is older
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
         }
-        asm volatile("" ::: "memory");
+        lds_barrier();
     };
-    constexpr int U = FMT == F_AWQ ? 2 : 10;
-    for (int u = wv; u < slots; u += kFewWaves) {
-        const uint32_t p = s.pair[u][l16];
-        const int e = __builtin_amdgcn_readfirstlane((int)s.expert[u]);
-        down_units<FMT, U>(acc, a.down, e, a.H, a.F, o0, rh, p != 0xFFFFu ? p * (uint32_t)a.F * 2u : kOob,
-                           (uint32_t)P * (uint32_t)a.F * 2u, 0, 1, ready);
-    }
-    if (!ok) acc = f32x4_t{1, 1, 1, 1} * __uint_as_float(0x7FC00000u);
-    part[0][wv][0][lane] = acc;
-    __syncthreads();
-    if (wv == 0 && l16 < a.T) {
+    int buf = 0;
+    for (int64_t v = v0; v < v1; buf ^= 1) {
+        const int c = (int)(v / n), o0 = c * 16;
+        const int64_t cb = (int64_t)c * n, ce = v1 < cb + n ? v1 : cb + n;  // the run's units of this group: v .. ce
+        const int b0 = (int)(v - cb), len = (int)(ce - v);
+        f32x4_t acc = {};
+        down_units<FMT, (FMT == F_FP8 ? 7 : kBatch<FMT>)>(
+            acc, a.down, a.H, a.F, o0, rh, (uint32_t)P * (uint32_t)a.F * 2u, b0 + len * wv / kFewWaves,
+            b0 + len * (wv + 1) / kFewWaves, [&](int u) { return __builtin_amdgcn_readfirstlane((int)s.expert[u]); },
+            [&](int u) {
+                const uint32_t p = s.pair[u][l16];
+                return p != 0xFFFFu ? p * (uint32_t)a.F * 2u : kOob;
+            },
+            ready);
+        // the shared expert's part goes with the first unit of the group
+        if (a.Fs && b0 == 0) {
+            const int ns = a.Fs / Unit<F_BF16>::IN;
+            down_units<F_BF16, 3>(
+                acc, a.sdown, a.H, a.Fs, o0, fp8_rsrc(a.hs, (uint32_t)a.T * (uint32_t)a.Fs * 4u),
+                (uint32_t)a.T * (uint32_t)a.Fs * 2u, ns * wv / kFewWaves, ns * (wv + 1) / kFewWaves, [](int) { return 0; },
+                [&](int) { return l16 < a.T ? (uint32_t)(l16 * a.Fs) * 2u : kOob; }, [] {});
+        }
+        if (!ok) acc = f32x4_t{1, 1, 1, 1} * __uint_as_float(0x7FC00000u);
+        part[buf][wv][lane] = acc;
+        v = ce;
+        lds_barrier();
+        if (wv != 0) continue;
 #pragma unroll
-        for (int q = 1; q < kFewWaves; ++q) acc += part[0][q][0][lane];
-        *reinterpret_cast<uint2*>(a.y + (size_t)l16 * a.H + o0 + g4) =
-            make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+        for (int q = 1; q < kFewWaves; ++q) acc += part[buf][q][lane];
+        // workgroups with units of this group: those whose runs hold its first to its last unit
+        auto owner = [&](int64_t unit) {
+            int b = (int)(unit * a.down_wgs / all);
+            while (run_begin(b + 1) <= unit) ++b;
+            while (run_begin(b) > unit) --b;
+            return b;
+        };
+        const int wb = owner(cb), we = owner(cb + n - 1);
+        if (wb != we) {
+            // leave the sum, count; the last of the workgroups adds them all
+            const __amdgpu_buffer_rsrc_t rp = fp8_rsrc(a.parts, (uint32_t)kFewSplits * (uint32_t)nc * 1024u);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc), rp,
+                                                   (((int)blockIdx.x - wb) * nc + c) * 1024 + lane * 16, 0, kAgent);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            uint32_t before = 0;
+            if (lane == 0)
+                before = __hip_atomic_fetch_add(a.counters + C_OUT + c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (__builtin_amdgcn_readfirstlane((int)before) != we - wb) continue;
+            asm volatile("" ::: "memory");
+            acc = f32x4_t{};
+            for (int q = 0; q <= we - wb; ++q)
+                acc += __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rp, (q * nc + c) * 1024 + lane * 16, 0,
+                                                                                        kAgent));
+        }
+        if (l16 < a.T)
+            *reinterpret_cast<uint2*>(a.y + (size_t)l16 * a.H + o0 + g4) =
+                make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
     }
 }
 
@@ -565,8 +823,11 @@ bool few_supported(const moe_experts* ex, const moe_experts* sh) {
     return (f == MOE_W_BF16 || f == MOE_W_FP8_BLOCK || f == MOE_W_AWQ_G32_OM) && (!sh || sh->gate.fmt == MOE_W_BF16);
 }
 
+static size_t few_counter_bytes(int H) { return up256((C_OUT + (size_t)H / 16) * 4); }
+
 size_t few_ws_bytes(int T, int k, const moe_experts* ex, const moe_experts* sh) {
-    return up256(9 * 32 * 4) + up256((size_t)T * ex->num_experts * 4) + up256(sh ? (size_t)T * sh->inter * 4 : 0) +
+    return few_counter_bytes(ex->hidden) + up256((size_t)kFewSplits * (ex->hidden / 16) * 1024) +
+           up256((size_t)T * ex->num_experts * 4) + up256(sh ? (size_t)T * sh->inter * 4 : 0) +
            up256((size_t)T * k * ex->inter * 4);
 }
 
@@ -589,7 +850,9 @@ hipError_t launch_layer_few(const uint16_t* x, int T, const uint16_t* router, in
     }
     char* w = static_cast<char*>(ws);
     a.counters = reinterpret_cast<uint32_t*>(w);
-    w += up256(9 * 32 * 4);
+    w += few_counter_bytes(a.H);
+    a.parts = reinterpret_cast<float*>(w);
+    w += up256((size_t)kFewSplits * (a.H / 16) * 1024);
     a.logits = reinterpret_cast<float*>(w);
     w += up256((size_t)T * a.E * 4);
     a.hs = reinterpret_cast<uint16_t*>(w);
@@ -597,15 +860,18 @@ hipError_t launch_layer_few(const uint16_t* x, int T, const uint16_t* router, in
     a.h = reinterpret_cast<uint16_t*>(w);
     a.y = y;
     a.topk_idx = topk_idx;
-    // at most two gate/up workgroups a compute unit, and no more than there can be items
-    const long items = (long)(T * k < a.E ? T * k : a.E) * (a.F / 16);
-    a.gateup_wgs = (int)(items < 512 ? items : 512);
+    // one workgroup a compute unit, which the registers allow; fewer where there is less to do
+    const int nc = a.H / 16;
+    a.down_wgs = nc * (kFewSplits - 1) < 256 ? nc * (kFewSplits - 1) : 256;
+    const int most = T * k < a.E ? T * k : a.E;
+    const long items = (long)most * (a.F / 8);
+    const int wgs = items < 256 ? (int)items : 256;
     const int groups = (T + kFrontTokens - 1) / kFrontTokens;
-    const dim3 front(a.Fs / 16 + (a.E * groups + kFewWaves - 1) / kFewWaves), block(kFewThreads);
+    const dim3 front(a.Fs / 8 + (a.E * groups + kFewWaves - 1) / kFewWaves), block(kFewThreads);
     hipLaunchKernelGGL(few_front_kernel, front, block, 0, s, a);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    const dim3 grid(a.gateup_wgs + a.H / 16);
+    const dim3 grid(wgs > a.down_wgs ? wgs : a.down_wgs);
     if (ex->gate.fmt == MOE_W_BF16) hipLaunchKernelGGL(few_experts_kernel<F_BF16>, grid, block, 0, s, a);
     else if (ex->gate.fmt == MOE_W_FP8_BLOCK) hipLaunchKernelGGL(few_experts_kernel<F_FP8>, grid, block, 0, s, a);
     else hipLaunchKernelGGL(few_experts_kernel<F_AWQ>, grid, block, 0, s, a);
