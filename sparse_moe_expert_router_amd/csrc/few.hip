@@ -14,7 +14,7 @@
 //    them then take gate/up items (an expert's columns) until none is left and
 //    write gate_tj h; load their first down rows and do their part of the shared
 //    expert; wait until all items are done; and sum the experts for their share
-//    of the outputs in fp32, in a fixed order.  Up to three workgroups share the
+//    of the outputs in fp32, in a fixed order.  Up to five workgroups share the
 //    same 16 outputs; the last of them to finish adds the parts, again in a fixed
 //    order.
 //
@@ -48,14 +48,13 @@ namespace {
 constexpr int kFewThreads = 512, kFewWaves = kFewThreads / kWave;
 constexpr int kFewMaxPairs = kFewMaxT * 64;
 constexpr int kAgent = 16;         // cache policy of buffer accesses: sc1
-constexpr int kStream = 2;         // non-temporal
 
 enum { F_BF16 = 0, F_FP8 = 1, F_AWQ = 2 };
 
 // Counters, 128 bytes apart: items taken of each range, items done of each
 // range, ranges done; then, 4 bytes apart, finished workgroups of each 16 outputs.
 constexpr int kRanges = 16;
-constexpr int kFewSplits = 3;      // workgroups that can share 16 outputs
+constexpr int kFewSplits = 5;      // workgroups that can share 16 outputs
 enum FewCount { C_TAKEN = 0, C_DONE = 32 * kRanges, C_ROOT = 64 * kRanges, C_OUT = 64 * kRanges + 32 };
 
 struct FewProj {
@@ -133,7 +132,7 @@ struct UnitData {
 // Unit u of the lane's row.
 template <int FMT>
 __device__ __forceinline__ void load_unit(UnitData<FMT>& d, const Rows<FMT>& r, int u) {
-    d.w = __builtin_nontemporal_load(reinterpret_cast<const i32x4_t*>(r.w + 64 * (size_t)u));
+    d.w = *reinterpret_cast<const i32x4_t*>(r.w + 64 * (size_t)u);
     if (FMT == F_FP8) d.s = r.s[u / 2];
     if (FMT == F_AWQ) {
 #pragma unroll
@@ -244,9 +243,11 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// Units of a batch: their weights are under way while the batch before is computed.
+// Units of a batch, under way at once.  Six waves a SIMD hide one another's
+// loads; longer batches, or the next one's weights loaded ahead, cost registers
+// and so waves, and measured slower (16 tokens, FP8: 226 us with two waves).
 template <int FMT>
-constexpr int kBatch = FMT == F_AWQ ? 3 : 10;
+constexpr int kBatch = FMT == F_AWQ ? 2 : FMT == F_FP8 ? 5 : 10;
 
 // Gate (rows 0..7) and up (rows 8..15) of 8 columns from o0 of expert e.
 template <int FMT>
@@ -264,35 +265,35 @@ __device__ __forceinline__ void load_batch(UnitData<FMT> (&d)[kBatch<FMT>], cons
         if (ub + i < u1) load_unit<FMT>(d[i], r, ub + i);
 }
 
-// acc += units ub .. of a batch (those below u1) times x of the tokens whose
-// byte offset is xoff (kOob: none; token l).  `between` issues the next loads:
-// after those of x, which are the first to be waited for.
-template <int FMT, class Between>
-__device__ __forceinline__ void gateup_batch(f32x4_t& acc, const UnitData<FMT> (&d)[kBatch<FMT>], __amdgpu_buffer_rsrc_t rx,
-                                             uint32_t xoff, int ub, int u1, Between between) {
+// acc += units u0 .. u1 - 1 times x of the tokens whose byte offset is xoff
+// (kOob: none; token l).
+template <int FMT>
+__device__ __forceinline__ void gateup_units(f32x4_t& acc, const Rows<FMT>& r, __amdgpu_buffer_rsrc_t rx, uint32_t xoff, int u0,
+                                             int u1) {
     using Un = Unit<FMT>;
-    constexpr int FR = Un::FRAGS;
+    constexpr int FR = Un::FRAGS, U = kBatch<FMT>;
     const int g = (threadIdx.x & 63) >> 4;
-    u32x4_t x[kBatch<FMT>][FR];
+    for (int ub = u0; ub < u1; ub += U) {
+        UnitData<FMT> d[U];
+        u32x4_t x[U][FR];
+        load_batch<FMT>(d, r, ub, u1);
 #pragma unroll
-    for (int i = 0; i < kBatch<FMT>; ++i)
-        if (ub + i < u1)
+        for (int i = 0; i < U; ++i)
+            if (ub + i < u1)
 #pragma unroll
-        for (int j = 0; j < FR; ++j) {
-            const uint32_t in = (uint32_t)((ub + i) * Un::IN + Un::input(g, j));
-            const bool ok = xoff != kOob;
-            x[i][j] = __builtin_bit_cast(
-                u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rx, ok ? (int)(xoff + 2u * in) : (int)kOob, 0, 0));
-        }
-    __builtin_amdgcn_sched_barrier(0);
-    between();
-    __builtin_amdgcn_sched_barrier(0);
+                for (int j = 0; j < FR; ++j)
+                    x[i][j] = __builtin_bit_cast(
+                        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                     rx, xoff != kOob ? (int)(xoff + 2u * (uint32_t)((ub + i) * Un::IN + Un::input(g, j))) : (int)kOob,
+                                     0, 0));
 #pragma unroll
-    for (int i = 0; i < kBatch<FMT>; ++i) if (ub + i < u1) {
-        bf16x8_t b[1][FR];
+        for (int i = 0; i < U; ++i)
+            if (ub + i < u1) {
+                bf16x8_t b[1][FR];
 #pragma unroll
-        for (int j = 0; j < FR; ++j) b[0][j] = input_frag<FMT>(x[i][j]);
-        unit_product<FMT, 1>(acc, d[i], b, 8 * (g & 1));
+                for (int j = 0; j < FR; ++j) b[0][j] = input_frag<FMT>(x[i][j]);
+                unit_product<FMT, 1>(acc, d[i], b, 8 * (g & 1));
+            }
     }
 }
 
@@ -338,48 +339,43 @@ __device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int 
     constexpr int FR = Un::FRAGS;
     const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
     const int n = F / Un::IN;
-    UnitData<FMT> d[U], dn[U];
-    auto load = [&](int vb) {
+    UnitData<FMT> d[U];
+    for (int vb = v0; vb < v1 || vb == v0; vb += U) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) if (vb + i < v1) {
-            const int v = vb + i, slot = v / n;
-            Rows<FMT> r;
-            r.init(pd, o0 + l16, pd, o0 + 4 * g, expert(slot), H, F, lane);
-            load_unit<FMT>(dn[i], r, v - slot * n);
-        }
-    };
-    load(v0);
-    ready();
-    for (int vb = v0; vb < v1; vb += U) {
-#pragma unroll
-        for (int i = 0; i < U; ++i) d[i] = dn[i];
-        u32x4_t h[U][2][FR];  // before the next weights: a wave's loads return in order
-#pragma unroll
-        for (int i = 0; i < U; ++i) if (vb + i < v1) {
-            const int v = vb + i, slot = v / n;
-            const uint32_t at = hoff(slot);
-#pragma unroll
-            for (int j = 0; j < FR; ++j) {
-                const uint32_t in = (uint32_t)((v - slot * n) * Un::IN + Un::input(g, j));
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    h[i][p][j] = __builtin_bit_cast(
-                        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rh, at != kOob ? (int)(at + 2u * in + p * lo) : (int)kOob,
-                                                                       0, 0));
+        for (int i = 0; i < U; ++i)
+            if (vb + i < v1) {
+                const int v = vb + i, slot = v / n;
+                Rows<FMT> r;
+                r.init(pd, o0 + l16, pd, o0 + 4 * g, expert(slot), H, F, lane);
+                load_unit<FMT>(d[i], r, v - slot * n);
             }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        load(vb + U);
-        __builtin_amdgcn_sched_barrier(0);
+        if (vb == v0) ready();
+        u32x4_t h[U][2][FR];
 #pragma unroll
-        for (int i = 0; i < U; ++i) if (vb + i < v1) {
-            bf16x8_t b[2][FR];
+        for (int i = 0; i < U; ++i)
+            if (vb + i < v1) {
+                const int v = vb + i, slot = v / n;
+                const uint32_t at = hoff(slot);
 #pragma unroll
-            for (int j = 0; j < FR; ++j)
+                for (int j = 0; j < FR; ++j) {
+                    const uint32_t in = (uint32_t)((v - slot * n) * Un::IN + Un::input(g, j));
 #pragma unroll
-                for (int p = 0; p < 2; ++p) b[p][j] = input_frag<FMT>(h[i][p][j]);
-            unit_product<FMT, 2>(acc, d[i], b, 8 * (g & 1));
-        }
+                    for (int p = 0; p < 2; ++p)
+                        h[i][p][j] = __builtin_bit_cast(
+                            u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                         rh, at != kOob ? (int)(at + 2u * in + p * lo) : (int)kOob, 0, 0));
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (vb + i < v1) {
+                bf16x8_t b[2][FR];
+#pragma unroll
+                for (int j = 0; j < FR; ++j)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) b[p][j] = input_frag<FMT>(h[i][p][j]);
+                unit_product<FMT, 2>(acc, d[i], b, 8 * (g & 1));
+            }
     }
 }
 
@@ -416,7 +412,7 @@ __device__ __forceinline__ void front_logits(const FewArgs& a, int e, int t0, in
 // The first Fs / 8 workgroups: 8 columns each of the shared expert's gate and
 // up, the inputs split over the waves; the others: logits, one wave per expert
 // and kFrontTokens tokens.
-__global__ __launch_bounds__(kFewThreads, 2) void few_front_kernel(const FewArgs a) {
+__global__ __launch_bounds__(kFewThreads, 4) void few_front_kernel(const FewArgs a) {
     __shared__ f32x4_t part[kFewWaves][kWave];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), l16 = lane & 15;
     if (blockIdx.x == 0) {
@@ -429,15 +425,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_front_kernel(const FewArgs
         f32x4_t acc = {};
         const Rows<F_BF16> r = gateup_rows<F_BF16>(a.sgate, a.sup, 0, a.Fs, a.H, o0);
         const int n = a.H / Unit<F_BF16>::IN, u0 = n * wv / kFewWaves, u1 = n * (wv + 1) / kFewWaves;
-        UnitData<F_BF16> d[kBatch<F_BF16>], dn[kBatch<F_BF16>];
-        load_batch<F_BF16>(dn, r, u0, u1);
-        for (int ub = u0; ub < u1; ub += kBatch<F_BF16>) {
-#pragma unroll
-            for (int i = 0; i < kBatch<F_BF16>; ++i) d[i] = dn[i];
-            gateup_batch<F_BF16>(acc, d, rx, l16 < a.T ? (uint32_t)(l16 * a.H) * 2u : kOob, ub, u1, [&] {
-                if (ub + kBatch<F_BF16> < u1) load_batch<F_BF16>(dn, r, ub + kBatch<F_BF16>, u1);
-            });
-        }
+        gateup_units<F_BF16>(acc, r, rx, l16 < a.T ? (uint32_t)(l16 * a.H) * 2u : kOob, u0, u1);
         part[wv][lane] = acc;
         __syncthreads();
         if (wv == 0 && lane < 32 && l16 < a.T) {
@@ -455,17 +443,43 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_front_kernel(const FewArgs
     if (e < a.E) front_logits(a, e, (w - e * groups) * kFrontTokens, lane);
 }
 
+// Lists of a workgroup in LDS, sized for the call (the fewer bytes, the more
+// workgroups share a compute unit): P pairs, at most S touched experts.
 struct FewLists {
-    int32_t idx[kFewMaxPairs];              // expert of pair t k + j
-    float gate[kFewMaxPairs];
-    uint16_t slot_of[1024];                 // expert -> slot
-    uint16_t expert[kFewMaxPairs];          // slot -> expert, ascending
-    uint16_t pair[kFewMaxPairs][kFewMaxT];  // slot, token -> pair, or 0xFFFF
-    int32_t wave_slots[kFewWaves];
-    int32_t next[2], left;
-    int32_t mine[kRanges];                  // items of each range this workgroup has done
-    uint32_t lane_max[kFewWaves][kWave];    // the selection's, one of each per wave
-    uint2 cand[kFewWaves][kWave];
+    f32x4_t (*part)[kFewWaves][kWave];    // [2]
+    uint2 (*cand)[kWave];                 // [waves], the selection's
+    uint32_t (*lane_max)[kWave];          // [waves]
+    int32_t* idx;                         // [P] expert of pair t k + j
+    float* gate;                          // [P]
+    int32_t* wave_slots;                  // [waves]
+    int32_t* next;                        // [2]
+    int32_t* mine;                        // [kRanges] items of each range this workgroup has done
+    uint16_t (*pair)[kFewMaxT];           // [S] slot, token -> pair, or 0xFFFF
+    uint16_t* slot_of;                    // [1024] expert -> slot
+    uint16_t* expert;                     // [S] slot -> expert, ascending
+
+    __host__ __device__ static size_t bytes(int P, int S) {
+        return 2 * kFewWaves * kWave * 16 + kFewWaves * kWave * 12 + (size_t)P * 8 + (kFewWaves + 2 + kRanges) * 4 +
+               (size_t)S * kFewMaxT * 2 + 1024 * 2 + (size_t)S * 2;
+    }
+    __device__ __forceinline__ void place(uint8_t* m, int P, int S) {
+        auto take = [&](size_t n) {
+            uint8_t* at = m;
+            m += n;
+            return at;
+        };
+        part = reinterpret_cast<f32x4_t(*)[kFewWaves][kWave]>(take(2 * kFewWaves * kWave * 16));
+        cand = reinterpret_cast<uint2(*)[kWave]>(take(kFewWaves * kWave * 8));
+        lane_max = reinterpret_cast<uint32_t(*)[kWave]>(take(kFewWaves * kWave * 4));
+        idx = reinterpret_cast<int32_t*>(take((size_t)P * 4));
+        gate = reinterpret_cast<float*>(take((size_t)P * 4));
+        wave_slots = reinterpret_cast<int32_t*>(take(kFewWaves * 4));
+        next = reinterpret_cast<int32_t*>(take(2 * 4));
+        mine = reinterpret_cast<int32_t*>(take(kRanges * 4));
+        pair = reinterpret_cast<uint16_t(*)[kFewMaxT]>(take((size_t)S * kFewMaxT * 2));
+        slot_of = reinterpret_cast<uint16_t*>(take(1024 * 2));
+        expert = reinterpret_cast<uint16_t*>(take((size_t)S * 2));
+    }
 };
 
 // Top k of token t's E <= 512 logits by one wave.  Lane i holds experts 8 i ..
@@ -475,7 +489,7 @@ struct FewLists {
 // candidates, and each finds its rank by comparing itself with the others.
 // Against k rounds of a wave-wide maximum this has no long chain, and a third
 // of the instructions, which every workgroup of the launch executes.
-__device__ __forceinline__ void few_topk(const FewArgs& a, FewLists& s, int t, u32x4_t l0, u32x4_t l1, int wv, int lane) {
+__device__ __forceinline__ void few_topk(const FewArgs& a, const FewLists& s, int t, u32x4_t l0, u32x4_t l1, int wv, int lane) {
     uint32_t key[8], m = 0;
 #pragma unroll
     for (int v = 0; v < 8; ++v) {
@@ -526,7 +540,7 @@ __device__ __forceinline__ void few_topk(const FewArgs& a, FewLists& s, int t, u
 // Selection and grouping, the same in every workgroup: the top k of every
 // token, then the touched experts in ascending order, and which pair of which
 // token each of them has.  Returns the number of touched experts.
-__device__ __forceinline__ int few_select(const FewArgs& a, FewLists& s) {
+__device__ __forceinline__ int few_select(const FewArgs& a, const FewLists& s) {
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, P = a.T * a.k;
     for (int e = threadIdx.x; e < 1024; e += kFewThreads) s.slot_of[e] = 0;
     const int slots_max = min(P, a.E);
@@ -615,12 +629,14 @@ __device__ __forceinline__ int take_result(const FewArgs& a, int n, int& r, uint
 }
 
 template <int FMT>
-__global__ __launch_bounds__(kFewThreads, 2) void few_experts_kernel(const FewArgs a) {
-    __shared__ FewLists s;
-    __shared__ f32x4_t part[2][kFewWaves][kWave];
+__global__ __launch_bounds__(kFewThreads, 4) void few_experts_kernel(const FewArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t few_smem[];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int l16 = lane & 15, g4 = 4 * (lane >> 4);
     const int P = a.T * a.k;
+    FewLists s;
+    s.place(few_smem, P, min(P, a.E));
+    f32x4_t (*part)[kFewWaves][kWave] = s.part;
     if (threadIdx.x < kRanges) s.mine[threadIdx.x] = 0;
     int r = blockIdx.x % kRanges;
     uint32_t taken = 0;
@@ -637,7 +653,6 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_experts_kernel(const FewAr
     const int ranges = min(items, kRanges);
     {
         using Un = Unit<FMT>;
-        constexpr int U = kBatch<FMT>;
         const __amdgpu_buffer_rsrc_t rx = fp8_rsrc(a.x, (uint32_t)a.T * (uint32_t)a.H * 2u);
         const int n = a.H / Un::IN, part_of = wv % ks, group = wv / ks;
         const int u0 = n * part_of / ks, u1 = n * (part_of + 1) / ks;
@@ -658,27 +673,11 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_experts_kernel(const FewAr
             const int e = __builtin_amdgcn_readfirstlane((int)s.expert[it / per]);
             return gateup_rows<FMT>(a.gate, a.up, e, a.F, a.H, min(first_col(it), a.F - 8));
         };
-        UnitData<FMT> d[U], dn[U];
-        Rows<FMT> rows;
-        if (item >= 0) {
-            rows = rows_of(item);
-            load_batch<FMT>(dn, rows, u0, u1);
-        }
         for (int buf = 0; item >= 0; buf ^= 1) {
             const uint32_t p = s.pair[item / per][l16];
-            const uint32_t xoff = p != 0xFFFFu ? (uint32_t)(l16 * a.H) * 2u : kOob;
             f32x4_t acc = {};
             if (wv == 0 && next >= 0) taken = take(a, r, lane);
-            Rows<FMT> rn = rows;
-            if (next >= 0) rn = rows_of(next);
-            for (int ub = u0; ub < u1; ub += U) {
-#pragma unroll
-                for (int i = 0; i < U; ++i) d[i] = dn[i];
-                gateup_batch<FMT>(acc, d, rx, xoff, ub, u1, [&] {
-                    if (ub + U < u1) load_batch<FMT>(dn, rows, ub + U, u1);
-                    else if (next >= 0) load_batch<FMT>(dn, rn, u0, u1);
-                });
-            }
+            gateup_units<FMT>(acc, rows_of(item), rx, p != 0xFFFFu ? (uint32_t)(l16 * a.H) * 2u : kOob, u0, u1);
             part[buf][wv][lane] = acc;
             if (wv == 0) {
                 // (taken, so done before this workgroup waits)
@@ -701,7 +700,6 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_experts_kernel(const FewAr
             }
             item = next;
             next = then;
-            rows = rn;
         }
         if (blockIdx.x == 0 && a.topk_idx)
             for (int p = threadIdx.x; p < P; p += kFewThreads) a.topk_idx[p] = s.idx[p];
@@ -718,12 +716,13 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_experts_kernel(const FewAr
 
     // ---- down.  The units of all experts for 16 outputs, and those of all
     // groups of 16 outputs one after another, are one list, of which every
-    // workgroup takes an equal run (at least half a group's units, so at most
-    // kFewSplits share a group), and of its part of a group every wave.
-    if ((int)blockIdx.x >= a.down_wgs) return;
+    // workgroup takes an equal run (at least a quarter of a group's units, so at
+    // most kFewSplits share a group), and of its part of a group every wave.
     const int nc = a.H / 16, n = slots * (a.F / Unit<FMT>::IN);
+    const int wgs = min(a.down_wgs, nc * min(n, kFewSplits - 1));  // no run is empty
+    if ((int)blockIdx.x >= wgs) return;
     const int64_t all = (int64_t)nc * n;
-    auto run_begin = [&](int b) { return all * b / a.down_wgs; };
+    auto run_begin = [&](int b) { return all * b / wgs; };
     const int64_t v0 = run_begin(blockIdx.x), v1 = run_begin(blockIdx.x + 1);
     bool first = true, ok = true;
     auto ready = [&] {
@@ -752,7 +751,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_experts_kernel(const FewAr
         const int64_t cb = (int64_t)c * n, ce = v1 < cb + n ? v1 : cb + n;  // the run's units of this group: v .. ce
         const int b0 = (int)(v - cb), len = (int)(ce - v);
         f32x4_t acc = {};
-        down_units<FMT, (FMT == F_FP8 ? 7 : kBatch<FMT>)>(
+        down_units<FMT, (FMT == F_FP8 ? 4 : FMT == F_AWQ ? 1 : 5)>(
             acc, a.down, a.H, a.F, o0, rh, (uint32_t)P * (uint32_t)a.F * 2u, b0 + len * wv / kFewWaves,
             b0 + len * (wv + 1) / kFewWaves, [&](int u) { return __builtin_amdgcn_readfirstlane((int)s.expert[u]); },
             [&](int u) {
@@ -777,7 +776,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_experts_kernel(const FewAr
         for (int q = 1; q < kFewWaves; ++q) acc += part[buf][q][lane];
         // workgroups with units of this group: those whose runs hold its first to its last unit
         auto owner = [&](int64_t unit) {
-            int b = (int)(unit * a.down_wgs / all);
+            int b = (int)(unit * wgs / all);
             while (run_begin(b + 1) <= unit) ++b;
             while (run_begin(b) > unit) --b;
             return b;
@@ -860,21 +859,22 @@ hipError_t launch_layer_few(const uint16_t* x, int T, const uint16_t* router, in
     a.h = reinterpret_cast<uint16_t*>(w);
     a.y = y;
     a.topk_idx = topk_idx;
-    // one workgroup a compute unit, which the registers allow; fewer where there is less to do
+    // three workgroups a compute unit, which the registers allow; fewer where there is less to do
     const int nc = a.H / 16;
-    a.down_wgs = nc * (kFewSplits - 1) < 256 ? nc * (kFewSplits - 1) : 256;
+    a.down_wgs = nc * (kFewSplits - 1) < 512 ? nc * (kFewSplits - 1) : 512;
     const int most = T * k < a.E ? T * k : a.E;
     const long items = (long)most * (a.F / 8);
-    const int wgs = items < 256 ? (int)items : 256;
+    const int wgs = items < 512 ? (int)items : 512;
+    const size_t lds = FewLists::bytes(T * k, most);
     const int groups = (T + kFrontTokens - 1) / kFrontTokens;
     const dim3 front(a.Fs / 8 + (a.E * groups + kFewWaves - 1) / kFewWaves), block(kFewThreads);
     hipLaunchKernelGGL(few_front_kernel, front, block, 0, s, a);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     const dim3 grid(wgs > a.down_wgs ? wgs : a.down_wgs);
-    if (ex->gate.fmt == MOE_W_BF16) hipLaunchKernelGGL(few_experts_kernel<F_BF16>, grid, block, 0, s, a);
-    else if (ex->gate.fmt == MOE_W_FP8_BLOCK) hipLaunchKernelGGL(few_experts_kernel<F_FP8>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(few_experts_kernel<F_AWQ>, grid, block, 0, s, a);
+    if (ex->gate.fmt == MOE_W_BF16) hipLaunchKernelGGL(few_experts_kernel<F_BF16>, grid, block, lds, s, a);
+    else if (ex->gate.fmt == MOE_W_FP8_BLOCK) hipLaunchKernelGGL(few_experts_kernel<F_FP8>, grid, block, lds, s, a);
+    else hipLaunchKernelGGL(few_experts_kernel<F_AWQ>, grid, block, lds, s, a);
     return hipGetLastError();
 }
 
