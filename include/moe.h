@@ -281,8 +281,9 @@ size_t moe_layer_workspace_bytes(int32_t T, int32_t k, const moe_experts *expert
  *          + shared_scale[t] * shared(x[t])
  * for decode steps where launches and the waits between them cost as much as
  * the weights.  Routing is moe_route's, exactly (topk_idx, nullable [T][k],
- * receives it); everything after it stays in fp32 until y is rounded to bf16
- * (moe_layer rounds the SwiGLU products and the experts' rows to bf16 on the
+ * receives it).  The gated SwiGLU products are rounded to bf16, everything
+ * after them stays in fp32 until y is rounded to bf16 (moe_layer rounds the
+ * products before the gate, and the experts' rows to bf16 on the
  * way, so the two differ by those roundings).  experts: bf16, FP8 or
  * output-major AWQ; shared (nullable): one bf16 expert of the same hidden
  * size; other formats, T > 16 or k > 64 -> MOE_ERR_UNSUPPORTED.  Other

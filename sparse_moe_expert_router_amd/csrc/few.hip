@@ -33,8 +33,7 @@
 // possible tokens, a token that is not routed to the expert reading zeros
 // (without memory traffic).  Weights stream 16 bytes a lane: 8 bf16, 16 E4M3
 // or 32 4-bit inputs of one row, widened to bf16 exactly; their scales are
-// applied to the fp32 sums, so nothing is rounded but h, kept as the sum of
-// two bf16 (16 bits of mantissa), and y.  Against dot products on the vector
+// applied to the fp32 sums, so nothing is rounded but h and y, both to bf16.  Against dot products on the vector
 // units this is a fifth of the instructions, which counts twice at one token,
 // where every instruction runs once and is fetched from memory.
 #include "fp8.h"
@@ -74,8 +73,8 @@ struct FewArgs {
     uint32_t* counters;     // see FewCount
     float* parts;           // [kFewSplits][H / 16][16 x 16] sums of down workgroups
     float* logits;          // [T][E]
-    uint16_t* hs;           // shared h: bf16 parts [2][T][Fs]
-    uint16_t* h;            // gated h of every pair: bf16 parts [2][T k][F]
+    uint16_t* hs;           // shared h [T][Fs] bf16
+    uint16_t* h;            // gated h of every pair [T k][F] bf16
     uint16_t* y;            // [T][H]
     int32_t* topk_idx;      // [T][k] or nullptr
 };
@@ -101,22 +100,29 @@ struct Unit {
 template <int FMT>
 struct Rows {
     const uint8_t* w;     // the lane's row, at its piece of unit 0
-    const float* s;       // E4M3: block scales of the expert and output block of rows 4 g
+    const float* s[2];    // E4M3: block scales of rows 0 .. 7 and 8 .. 15 (uniform)
     const uint16_t* gs;   // 4-bit: scales of rows 4 g .. + 3, one row of O per group of 32 inputs
     const uint8_t* gz;    // and their zero words
     int O;
 
     // row l % 16 of the fragment is output `o` of p (may differ by lane); rows
-    // 4 g .. + 3 are outputs `o4` .. of p4
-    __device__ __forceinline__ void init(const FewProj& p, int o, const FewProj& p4, int o4, int e, int O_, int I, int lane) {
+    // 4 g .. + 3 are outputs `o4` .. of p4; rows 0 .. 7 are of pa, the others of
+    // pb, all outputs of one block of 128 with o0
+    __device__ __forceinline__ void init(const FewProj& p, int o, const FewProj& p4, int o4, const FewProj& pa, const FewProj& pb,
+                                         int o0, int e, int O_, int I, int lane) {
         using Un = Unit<FMT>;
         O = O_;
         const uint32_t rowb = (uint32_t)(I / 8) * Un::ROW8;
         w = static_cast<const uint8_t*>(p.w) + ((size_t)e * O + o) * rowb + 16 * (lane >> 4);
-        if (FMT == F_FP8) s = p4.bscales + ((size_t)e * (O / 128) + o4 / 128) * (I / 128);
+        if (FMT == F_FP8) {
+            const size_t at = ((size_t)e * (O / 128) + o0 / 128) * (I / 128);
+            s[0] = pa.bscales + at;
+            s[1] = pb.bscales + at;
+        }
         if (FMT == F_AWQ) {
-            gs = p4.scales + (size_t)e * (I / 32) * O + o4;
-            gz = reinterpret_cast<const uint8_t*>(p4.qzeros + (size_t)e * (I / 32) * (O / 8) + o4 / 8);
+            // lane l of 16 loads group l % 4 of a unit
+            gs = p4.scales + ((size_t)e * (I / 32) + (lane & 3)) * O + o4;
+            gz = reinterpret_cast<const uint8_t*>(p4.qzeros + ((size_t)e * (I / 32) + (lane & 3)) * (O / 8) + o4 / 8);
         }
     }
 };
@@ -124,22 +130,24 @@ struct Rows {
 template <int FMT>
 struct UnitData {
     i32x4_t w;
-    float s;                      // E4M3
-    u32x2_t gs[4];                // 4-bit: four fp16 scales per group
-    uint32_t gz[4];               // and their zero words
+    float s[2];                   // E4M3 (uniform)
+    u32x2_t gs;                   // 4-bit: four fp16 scales of a group
+    uint32_t gz;                  // and their zero word
 };
+
+typedef const __attribute__((address_space(4))) float const_float;
 
 // Unit u of the lane's row.
 template <int FMT>
 __device__ __forceinline__ void load_unit(UnitData<FMT>& d, const Rows<FMT>& r, int u) {
     d.w = *reinterpret_cast<const i32x4_t*>(r.w + 64 * (size_t)u);
-    if (FMT == F_FP8) d.s = r.s[u / 2];
+    if (FMT == F_FP8) {
+        d.s[0] = ((const_float*)r.s[0])[u / 2];
+        d.s[1] = ((const_float*)r.s[1])[u / 2];
+    }
     if (FMT == F_AWQ) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            d.gs[j] = *reinterpret_cast<const u32x2_t*>(r.gs + (size_t)(4 * u + j) * r.O);
-            d.gz[j] = *reinterpret_cast<const uint32_t*>(r.gz + (size_t)(4 * u + j) * (r.O / 2));
-        }
+        d.gs = *reinterpret_cast<const u32x2_t*>(r.gs + (size_t)(4 * u) * r.O);
+        d.gz = *reinterpret_cast<const uint32_t*>(r.gz + (size_t)(4 * u) * (r.O / 2));
     }
 }
 
@@ -193,45 +201,50 @@ __device__ __forceinline__ f32x4_t mfma32(bf16x8_t a, bf16x8_t b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// acc += unit . inputs; b[NB][FRAGS]: the inputs are the sum of NB parts.
-template <int FMT, int NB>
-__device__ __forceinline__ void unit_product(f32x4_t& acc, const UnitData<FMT>& d, const bf16x8_t (&b)[NB][Unit<FMT>::FRAGS],
+// The value of lane J of each 16 (row_newbcast).
+template <int J>
+__device__ __forceinline__ uint32_t row_lane(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x150 + J, 0xF, 0xF, false);
+}
+
+// One group of a 4-bit unit: acc += s (sum (128 + q) x - (128 + z) sum x).
+template <int J>
+__device__ __forceinline__ void awq_group(f32x4_t& acc, const UnitData<F_AWQ>& d, bf16x8_t a, bf16x8_t b, int zshift) {
+    const u32x4_t one4 = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    const f32x4_t zero = {};
+    const f32x4_t v = mfma32(a, b, zero), sum = mfma32(__builtin_bit_cast(bf16x8_t, one4), b, zero);
+    // zeros of rows 4 g + i: AWQ order of the word's nibbles
+    const uint32_t zw = row_lane<J>(d.gz) >> zshift;  // 8 where rows 4 g .. are outputs 4 .. 7 of their word
+    const uint32_t gs[2] = {row_lane<J>(d.gs[0]), row_lane<J>(d.gs[1])};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float z = (float)((zw >> ((i & 1) * 16 + (i >> 1) * 4)) & 15u) + 128.0f;
+        const float s = f16_to_f32((gs[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+        acc[i] = fmaf(s, fmaf(-z, sum[i], v[i]), acc[i]);
+    }
+}
+
+// acc += unit . inputs.
+template <int FMT>
+__device__ __forceinline__ void unit_product(f32x4_t& acc, const UnitData<FMT>& d, const bf16x8_t (&b)[Unit<FMT>::FRAGS],
                                              int zshift) {
     constexpr int FR = Unit<FMT>::FRAGS;
     bf16x8_t a[FR];
     unit_frags<FMT>(d, a);
     if constexpr (FMT == F_BF16) {
-#pragma unroll
-        for (int p = 0; p < NB; ++p) acc = mfma32(a[0], b[p][0], acc);
+        acc = mfma32(a[0], b[0], acc);
     } else if constexpr (FMT == F_FP8) {
         f32x4_t v = {};
 #pragma unroll
-        for (int j = 0; j < FR; ++j)
+        for (int j = 0; j < FR; ++j) v = mfma32(a[j], b[j], v);
+        const float s = threadIdx.x & 32 ? d.s[1] : d.s[0];  // rows 4 g ..: 8 and on from lane 32
 #pragma unroll
-            for (int p = 0; p < NB; ++p) v = mfma32(a[j], b[p][j], v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = fmaf(d.s, v[i], acc[i]);
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(s, v[i], acc[i]);
     } else {
-        // per group of 32: s (sum (128 + q) x - (128 + z) sum x), the second sum by ones
-        const u32x4_t one4 = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-        const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, one4);
-#pragma unroll
-        for (int j = 0; j < FR; ++j) {
-            f32x4_t v = {}, sum = {};
-#pragma unroll
-            for (int p = 0; p < NB; ++p) {
-                v = mfma32(a[j], b[p][j], v);
-                sum = mfma32(ones, b[p][j], sum);
-            }
-            // zeros of outputs 4 g + i: AWQ order of the word's nibbles
-            const uint32_t zw = d.gz[j] >> zshift;  // 8 where rows 4 g .. are outputs 4 .. 7 of their word
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float z = (float)((zw >> ((i & 1) * 16 + (i >> 1) * 4)) & 15u) + 128.0f;
-                const float s = f16_to_f32((d.gs[j][i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-                acc[i] = fmaf(s, fmaf(-z, sum[i], v[i]), acc[i]);
-            }
-        }
+        awq_group<0>(acc, d, a[0], b[0], zshift);
+        awq_group<1>(acc, d, a[1], b[1], zshift);
+        awq_group<2>(acc, d, a[2], b[2], zshift);
+        awq_group<3>(acc, d, a[3], b[3], zshift);
     }
 }
 
@@ -254,7 +267,7 @@ template <int FMT>
 __device__ __forceinline__ Rows<FMT> gateup_rows(const FewProj& pg, const FewProj& pu, int e, int F, int H, int o0) {
     const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
     Rows<FMT> r;
-    r.init(l16 < 8 ? pg : pu, o0 + (l16 & 7), g < 2 ? pg : pu, o0 + 4 * (g & 1), e, F, H, lane);
+    r.init(l16 < 8 ? pg : pu, o0 + (l16 & 7), g < 2 ? pg : pu, o0 + 4 * (g & 1), pg, pu, o0, e, F, H, lane);
     return r;
 }
 
@@ -289,10 +302,10 @@ __device__ __forceinline__ void gateup_units(f32x4_t& acc, const Rows<FMT>& r, _
 #pragma unroll
         for (int i = 0; i < U; ++i)
             if (ub + i < u1) {
-                bf16x8_t b[1][FR];
+                bf16x8_t b[FR];
 #pragma unroll
-                for (int j = 0; j < FR; ++j) b[0][j] = input_frag<FMT>(x[i][j]);
-                unit_product<FMT, 1>(acc, d[i], b, 8 * (g & 1));
+                for (int j = 0; j < FR; ++j) b[j] = input_frag<FMT>(x[i][j]);
+                unit_product<FMT>(acc, d[i], b, 8 * (g & 1));
             }
     }
 }
@@ -310,31 +323,22 @@ __device__ __forceinline__ f32x4_t gateup_join(const f32x4_t (*part)[kWave], int
     return h;
 }
 
-// h of four neighbouring columns as two bf16 parts, [2][rows][F].
-__device__ __forceinline__ void store_h(__amdgpu_buffer_rsrc_t r, uint32_t row, uint32_t rows, int F, int col, f32x4_t h,
-                                        int policy) {
-    float lo[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) lo[i] = h[i] - bf16_to_f32(f32_to_bf16_bits(h[i]));
+// h of four neighbouring columns, rounded to bf16 as the layer of separate
+// kernels does: kept in 16 bits more the down pass has twice the loads of it,
+// and their number bounds that pass (16 tokens, FP8: 72 us of 213).
+__device__ __forceinline__ void store_h(__amdgpu_buffer_rsrc_t r, uint32_t row, int F, int col, f32x4_t h, bool agent) {
     const u32x2_t a = {pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])};
-    const u32x2_t b = {pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3])};
     const uint32_t at = (row * (uint32_t)F + (uint32_t)col) * 2u;
-    if (policy) {
-        __builtin_amdgcn_raw_buffer_store_b64(a, r, (int)at, 0, kAgent);
-        __builtin_amdgcn_raw_buffer_store_b64(b, r, (int)(at + rows * (uint32_t)F * 2u), 0, kAgent);
-    } else {
-        __builtin_amdgcn_raw_buffer_store_b64(a, r, (int)at, 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b64(b, r, (int)(at + rows * (uint32_t)F * 2u), 0, 0);
-    }
+    if (agent) __builtin_amdgcn_raw_buffer_store_b64(a, r, (int)at, 0, kAgent);
+    else __builtin_amdgcn_raw_buffer_store_b64(a, r, (int)at, 0, 0);
 }
 
 // Units v0 .. v1 of the F inputs of a list of experts, one after another, into
 // 16 outputs from o0.  expert(slot), hoff(slot): the slot's expert and the byte
-// offset of the lane's token's h (kOob: not routed to it); lo: bytes to the
-// second bf16 part of h.  `ready` is called once the first U units are under way.
+// offset of the lane's token's h (kOob: not routed to it).  `ready` is called once the first U units are under way.
 template <int FMT, int U, class Expert, class Hoff, class Ready>
 __device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int H, int F, int o0, __amdgpu_buffer_rsrc_t rh,
-                                           uint32_t lo, int v0, int v1, Expert expert, Hoff hoff, Ready ready) {
+                                           int v0, int v1, Expert expert, Hoff hoff, Ready ready) {
     using Un = Unit<FMT>;
     constexpr int FR = Un::FRAGS;
     const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
@@ -346,11 +350,11 @@ __device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int 
             if (vb + i < v1) {
                 const int v = vb + i, slot = v / n;
                 Rows<FMT> r;
-                r.init(pd, o0 + l16, pd, o0 + 4 * g, expert(slot), H, F, lane);
+                r.init(pd, o0 + l16, pd, o0 + 4 * g, pd, pd, o0, expert(slot), H, F, lane);
                 load_unit<FMT>(d[i], r, v - slot * n);
             }
         if (vb == v0) ready();
-        u32x4_t h[U][2][FR];
+        u32x4_t h[U][FR];
 #pragma unroll
         for (int i = 0; i < U; ++i)
             if (vb + i < v1) {
@@ -359,22 +363,17 @@ __device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int 
 #pragma unroll
                 for (int j = 0; j < FR; ++j) {
                     const uint32_t in = (uint32_t)((v - slot * n) * Un::IN + Un::input(g, j));
-#pragma unroll
-                    for (int p = 0; p < 2; ++p)
-                        h[i][p][j] = __builtin_bit_cast(
-                            u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                         rh, at != kOob ? (int)(at + 2u * in + p * lo) : (int)kOob, 0, 0));
+                    h[i][j] = __builtin_bit_cast(
+                        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rh, at != kOob ? (int)(at + 2u * in) : (int)kOob, 0, 0));
                 }
             }
 #pragma unroll
         for (int i = 0; i < U; ++i)
             if (vb + i < v1) {
-                bf16x8_t b[2][FR];
+                bf16x8_t b[FR];
 #pragma unroll
-                for (int j = 0; j < FR; ++j)
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) b[p][j] = input_frag<FMT>(h[i][p][j]);
-                unit_product<FMT, 2>(acc, d[i], b, 8 * (g & 1));
+                for (int j = 0; j < FR; ++j) b[j] = input_frag<FMT>(h[i][j]);
+                unit_product<FMT>(acc, d[i], b, 8 * (g & 1));
             }
     }
 }
@@ -433,8 +432,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_front_kernel(const FewArgs
             const float s = a.shared_scale ? a.shared_scale[l16] : 1.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) h[i] *= s;
-            store_h(fp8_rsrc(a.hs, (uint32_t)a.T * (uint32_t)a.Fs * 4u), (uint32_t)l16, (uint32_t)a.T, a.Fs,
-                    o0 + 4 * (lane >> 4), h, 0);
+            store_h(fp8_rsrc(a.hs, (uint32_t)a.T * (uint32_t)a.Fs * 2u), (uint32_t)l16, a.Fs, o0 + 4 * (lane >> 4), h, false);
         }
         return;
     }
@@ -603,8 +601,8 @@ __device__ __forceinline__ int range_first(int n, int r) { return n / kRanges * 
 // Takes items for a workgroup (one wave): take() asks for the next of range `r`,
 // take_result() is that item, or one of any range that has some left (r becomes
 // that one), or -1 when all are taken.  They are apart because a wave's loads
-// return in order: asked for before the next weights are, the answer does not
-// wait for those.
+// return in order: asked for before the weights are, the answer is there when
+// they are.
 __device__ __forceinline__ uint32_t take(const FewArgs& a, int r, int lane) {
     uint32_t v = 0;
     if (lane == 0)
@@ -642,13 +640,13 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_experts_kernel(const FewAr
     uint32_t taken = 0;
     if (wv == 0) taken = take(a, r, lane);
     const int slots = few_select(a, s);
-    const __amdgpu_buffer_rsrc_t rh = fp8_rsrc(a.h, (uint32_t)P * (uint32_t)a.F * 4u);
+    const __amdgpu_buffer_rsrc_t rh = fp8_rsrc(a.h, (uint32_t)P * (uint32_t)a.F * 2u);
 
     // ---- gate/up.  An item is 8 columns of an expert for each group of `ks`
     // waves, which split the inputs and are joined in their order through LDS:
     // few items are cut finely, many keep a wave on longer runs.
     const int cols8 = slots * (a.F / 8);
-    const int ks = cols8 >= 4096 ? 2 : cols8 >= 1024 ? 4 : 8, cw = kFewWaves / ks;
+    const int ks = cols8 >= 1024 ? 4 : 8, cw = kFewWaves / ks;
     const int per = (a.F / 8 + cw - 1) / cw, items = slots * per;
     const int ranges = min(items, kRanges);
     {
@@ -658,15 +656,10 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_experts_kernel(const FewAr
         const int u0 = n * part_of / ks, u1 = n * (part_of + 1) / ks;
         if (wv == 0) {
             const int first = take_result(a, items, r, taken, lane);
-            const int second = first < 0 ? -1 : take_result(a, items, r, take(a, r, lane), lane);
-            if (lane == 0) {
-                s.next[0] = first;
-                s.next[1] = second;
-            }
+            if (lane == 0) s.next[1] = first;
         }
         lds_barrier();
-        int item = __builtin_amdgcn_readfirstlane(s.next[0]), next = __builtin_amdgcn_readfirstlane(s.next[1]);
-        lds_barrier();
+        int item = __builtin_amdgcn_readfirstlane(s.next[1]);
         // columns past F (F / 8 no multiple of the groups) repeat the last ones and are not stored
         auto first_col = [&](int it) { return (it % per * cw + group) * 8; };
         auto rows_of = [&](int it) {
@@ -676,30 +669,28 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_experts_kernel(const FewAr
         for (int buf = 0; item >= 0; buf ^= 1) {
             const uint32_t p = s.pair[item / per][l16];
             f32x4_t acc = {};
-            if (wv == 0 && next >= 0) taken = take(a, r, lane);
+            if (wv == 0) taken = take(a, r, lane);  // the next one, before the weights' loads
             gateup_units<FMT>(acc, rows_of(item), rx, p != 0xFFFFu ? (uint32_t)(l16 * a.H) * 2u : kOob, u0, u1);
             part[buf][wv][lane] = acc;
             if (wv == 0) {
-                // (taken, so done before this workgroup waits)
-                const int then = next < 0 ? -1 : take_result(a, items, r, taken, lane);
+                const int next = take_result(a, items, r, taken, lane);
                 if (lane == 0) {
-                    s.next[buf] = then;
+                    s.next[buf] = next;
                     int q = 0;
                     while (q + 1 < ranges && item >= range_first(items, q + 1)) ++q;
                     ++s.mine[q];
                 }
             }
             lds_barrier();
-            const int then = __builtin_amdgcn_readfirstlane(s.next[buf]);
+            const int next = __builtin_amdgcn_readfirstlane(s.next[buf]);
             if (part_of == 0 && lane < 32 && p != 0xFFFFu && first_col(item) < a.F) {
                 f32x4_t h = gateup_join(&part[buf][wv], ks, lane);
                 const float gate = s.gate[p];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) h[i] *= gate;
-                store_h(rh, p, (uint32_t)P, a.F, first_col(item) + g4, h, 1);
+                store_h(rh, p, a.F, first_col(item) + g4, h, true);
             }
             item = next;
-            next = then;
         }
         if (blockIdx.x == 0 && a.topk_idx)
             for (int p = threadIdx.x; p < P; p += kFewThreads) a.topk_idx[p] = s.idx[p];
@@ -751,8 +742,8 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_experts_kernel(const FewAr
         const int64_t cb = (int64_t)c * n, ce = v1 < cb + n ? v1 : cb + n;  // the run's units of this group: v .. ce
         const int b0 = (int)(v - cb), len = (int)(ce - v);
         f32x4_t acc = {};
-        down_units<FMT, (FMT == F_FP8 ? 4 : FMT == F_AWQ ? 1 : 5)>(
-            acc, a.down, a.H, a.F, o0, rh, (uint32_t)P * (uint32_t)a.F * 2u, b0 + len * wv / kFewWaves,
+        down_units<FMT, (FMT == F_FP8 ? 6 : FMT == F_AWQ ? 2 : 10)>(
+            acc, a.down, a.H, a.F, o0, rh, b0 + len * wv / kFewWaves,
             b0 + len * (wv + 1) / kFewWaves, [&](int u) { return __builtin_amdgcn_readfirstlane((int)s.expert[u]); },
             [&](int u) {
                 const uint32_t p = s.pair[u][l16];
@@ -763,8 +754,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_experts_kernel(const FewAr
         if (a.Fs && b0 == 0) {
             const int ns = a.Fs / Unit<F_BF16>::IN;
             down_units<F_BF16, 3>(
-                acc, a.sdown, a.H, a.Fs, o0, fp8_rsrc(a.hs, (uint32_t)a.T * (uint32_t)a.Fs * 4u),
-                (uint32_t)a.T * (uint32_t)a.Fs * 2u, ns * wv / kFewWaves, ns * (wv + 1) / kFewWaves, [](int) { return 0; },
+                acc, a.sdown, a.H, a.Fs, o0, fp8_rsrc(a.hs, (uint32_t)a.T * (uint32_t)a.Fs * 2u), ns * wv / kFewWaves, ns * (wv + 1) / kFewWaves, [](int) { return 0; },
                 [&](int) { return l16 < a.T ? (uint32_t)(l16 * a.Fs) * 2u : kOob; }, [] {});
         }
         if (!ok) acc = f32x4_t{1, 1, 1, 1} * __uint_as_float(0x7FC00000u);
@@ -826,8 +816,8 @@ static size_t few_counter_bytes(int H) { return up256((C_OUT + (size_t)H / 16) *
 
 size_t few_ws_bytes(int T, int k, const moe_experts* ex, const moe_experts* sh) {
     return few_counter_bytes(ex->hidden) + up256((size_t)kFewSplits * (ex->hidden / 16) * 1024) +
-           up256((size_t)T * ex->num_experts * 4) + up256(sh ? (size_t)T * sh->inter * 4 : 0) +
-           up256((size_t)T * k * ex->inter * 4);
+           up256((size_t)T * ex->num_experts * 4) + up256(sh ? (size_t)T * sh->inter * 2 : 0) +
+           up256((size_t)T * k * ex->inter * 2);
 }
 
 hipError_t launch_layer_few(const uint16_t* x, int T, const uint16_t* router, int k, const moe_experts* ex,
@@ -855,7 +845,7 @@ hipError_t launch_layer_few(const uint16_t* x, int T, const uint16_t* router, in
     a.logits = reinterpret_cast<float*>(w);
     w += up256((size_t)T * a.E * 4);
     a.hs = reinterpret_cast<uint16_t*>(w);
-    w += up256((size_t)T * a.Fs * 4);
+    w += up256((size_t)T * a.Fs * 2);
     a.h = reinterpret_cast<uint16_t*>(w);
     a.y = y;
     a.topk_idx = topk_idx;

@@ -4,7 +4,7 @@ Bound.  A sum of products in fp32, however split over lanes, meets fewer than 12
 (at most 90 additions in a lane, 6 levels of lanes, a scale), each off by at most 2^-23 of the magnitudes
 summed (2^-24 rounded to nearest, twice that truncated): error <= 128 2^-23 A, A the sum of the magnitudes of
 what is added.  For 4-bit codes that is s (128 + q) x and s (128 + z) x in the first two projections, s q h
-and s z h in the last.  Gates: an exponential (2 ulp), a sum and a division, 2^-20 relative.
+and s z h in the last.  h is rounded to bf16, half a step of 2^-8.  Gates: an exponential (2 ulp), a sum and a division, 2^-20 relative.
 """
 import torch
 
@@ -38,7 +38,8 @@ def expert(bank, e, x):
     (wg, mg, _), (wu, mu, _), (wd, _, md) = (matrices(bank, n, e) for n in ("gate", "up", "down"))
     g, u = wg @ x, wu @ x
     h, dh = R.swiglu(g, eps * (mg @ x.abs()), u, eps * (mu @ x.abs()))
-    return wd @ h, md @ dh + eps * (md @ (h.abs() + dh))
+    dh = dh + 2.0 ** -8 * (h.abs() + dh)      # rounded to bf16 (with the gate, a factor)
+    return wd @ h, wd.abs() @ dh + eps * (md @ (h.abs() + dh))
 
 
 def layer(x, router, k, bank, shared=None, scale=None):
