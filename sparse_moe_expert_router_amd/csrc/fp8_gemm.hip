@@ -33,7 +33,7 @@ namespace moe {
 
 enum { G_DENSE = 0, G_GATEUP = 1, G_DOWN = 2 };
 
-constexpr int kGThreads = 512, kGWaves = 8;
+constexpr int kGThreads = 512;
 constexpr int kGN = 256;       // outputs of a tile (gate/up: 128 of each)
 // LDS of a tile of BT rows, in bytes.
 template <int TF>
@@ -66,6 +66,16 @@ __device__ __forceinline__ int g_order(int r) {
 
 typedef __attribute__((address_space(3))) void lds_void;
 
+// A load of 16 (4) bytes a lane from memory to LDS: lane i's land at lds + 16 i (4 i).
+__device__ __forceinline__ void load16_lds(const void* base, uint32_t bytes, uint8_t* lds, uint32_t voff, int soff) {
+    const __amdgpu_buffer_rsrc_t r = fp8_rsrc(base, bytes);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, (int)voff, soff, 0, 0);
+}
+__device__ __forceinline__ void load4_lds(const void* base, uint32_t bytes, void* lds, uint32_t voff, int soff) {
+    const __amdgpu_buffer_rsrc_t r = fp8_rsrc(base, bytes);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 4, (int)voff, soff, 0, 0);
+}
+
 // Waits until at most n of the wave's memory loads are under way, and for its
 // LDS reads; then for the other waves.
 template <int n>
@@ -73,6 +83,29 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(n) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+}
+
+// Eight neighbouring outputs of a row, rounded once, in 16-byte stores.
+__device__ __forceinline__ void store8(void* row, int out_f32, int n, f32x4_t a, f32x4_t b) {
+    if (out_f32) {
+        f32x4_t* o = reinterpret_cast<f32x4_t*>(static_cast<float*>(row) + n);
+        o[0] = a;
+        o[1] = b;
+    } else {
+        const u32x4_t o = {pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
+        *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(row) + n) = o;
+    }
+}
+
+// The sums of the first n groups of rows are final here.  Without it the compiler
+// moves additions, with all their operands, past the branches that follow, which
+// costs 40 registers a lane.
+template <int TF>
+__device__ __forceinline__ void hold(f32x4_t (&acc)[4][TF], int n) {
+#pragma unroll
+    for (int t = 0; t < n; ++t)
+#pragma unroll
+        for (int f = 0; f < 4; ++f) asm volatile("" : "+v"(acc[f][t]));
 }
 
 template <int TF, int MODE, bool kExact>
@@ -269,6 +302,7 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
 #pragma unroll
         for (int t = 0; t < TF; ++t) {
             if (t == kMeet) {
+                hold(acc, kMeet);
                 wait_and_meet<(S - 2) * NL>();
                 if ((j & 7) == 0 && j + 8 < KB) load_s(j / 8 + 1);
             }
@@ -295,6 +329,7 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
         }
         add(4 * TF - 2);
         add(4 * TF - 1);
+        hold(acc, TF);
     }
     wait_and_meet<0>();  // no load still writes LDS, no wave still reads it
 
@@ -352,16 +387,7 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
                 const int n = n0 + 64 * wn + 16 * f + 8 * g;
                 if (n >= N) continue;
                 if (vec && n + 7 < N) {
-                    if (out_f32) {
-                        f32x4_t* o = reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(row) + n);
-                        o[0] = acc[f][t];
-                        o[1] = acc[f + 1][t];
-                    } else {
-                        const u32x4_t o = {pack_bf16x2(acc[f][t][0], acc[f][t][1]), pack_bf16x2(acc[f][t][2], acc[f][t][3]),
-                                           pack_bf16x2(acc[f + 1][t][0], acc[f + 1][t][1]),
-                                           pack_bf16x2(acc[f + 1][t][2], acc[f + 1][t][3])};
-                        *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(row) + n) = o;
-                    }
+                    store8(row, out_f32, n, acc[f][t], acc[f + 1][t]);
                 } else {
                     fp8_store4(row, out_f32, n, N, false, acc[f][t]);
                     fp8_store4(row, out_f32, n + 4, N, false, acc[f + 1][t]);
@@ -369,6 +395,329 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
             }
         }
     }
+}
+
+// ---------------------------------------------------------------------------
+// The grouped passes on a run of tiles per workgroup, one workgroup a compute
+// unit: the steps of its tiles are one sequence, u = tile * KB + j, and the
+// pipeline above runs across tile borders, so the first loads of a tile are
+// under way while the tile before is computed and stored.  (One workgroup per
+// tile left 10 us of its 20 to 47 us without an MFMA; no second one fits the
+// LDS.)  Needs KB >= kRunMinKB, so that what the next tile needs can be
+// prepared within the present one:
+//   step 0     gate/up: the next tile's (token, slot) pairs are loaded
+//   step 2     and turned into token rows, seen after the barrier of step 3
+//   last steps the first scales and, S steps before the end, rows and weights
+// Scales come in chunks of 4 to 8 steps, two LDS buffers.
+template <int TF>
+struct RunLds {
+    using G = GemmLds<TF>;
+    static constexpr int BT = G::BT, S = G::S, A = G::A, B = G::B, W = G::W, SA = G::SA, SW = G::SW;
+    static constexpr int TOK = G::ROW;                // gate/up: token rows [2][BT]
+    static constexpr int RAW = TOK + 2 * BT * 4;      // and the pairs they come from [BT]
+    static constexpr int AMAX = RAW + BT * 4;         // group maxima [4][BT]
+    static constexpr int TOTAL = AMAX + 4 * BT * 4;
+    static_assert(TOTAL <= 160 * 1024, "LDS of a compute unit");
+};
+
+constexpr int kRunMinKB = 8, kRunMinKBDown = 4;
+
+struct RunTile {
+    int e, m0, mr, n0;
+};
+
+typedef const __attribute__((address_space(4))) int32_t const_int;
+
+// A value that no kernel writes meanwhile, at a uniform address: a scalar load.
+__device__ __forceinline__ int const_load(const int32_t* p) { return *(const_int*)p; }
+
+template <int TF, int MODE>
+__global__ __launch_bounds__(kGThreads, 2) void fp8_run_kernel(const Fp8Ffn p) {
+    using L = RunLds<TF>;
+    constexpr int BT = L::BT, S = L::S, NA = BT / 64, NL = NA + 4;
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wv & 3, wt = wv >> 2, g = lane >> 4, l16 = lane & 15;
+
+    // ---- the run: XCD x takes a contiguous eighth of the tiles, its workgroups every (grid / 8)-th of it
+    const int K = MODE == G_GATEUP ? p.H : p.F, N = MODE == G_GATEUP ? p.F : p.H;
+    const int KB = K / 128, NB = N / 128;
+    const int nt = MODE == G_GATEUP ? p.F / 128 : (p.H + kGN - 1) / kGN;
+    const int total = const_load(p.tiles) * nt, q = (total + kXcd - 1) / kXcd, stride = (int)gridDim.x / kXcd;
+    const int l0 = (int)blockIdx.x % kXcd * q + (int)blockIdx.x / kXcd, lend = min(((int)blockIdx.x % kXcd + 1) * q, total);
+    if (l0 >= lend) return;
+    const int count = (lend - l0 + stride - 1) / stride;
+    auto tile_at = [&](int i) {  // tile i of the run
+        const int l = l0 + i * stride, t = l / nt;
+        RunTile r;
+        r.n0 = (l - t * nt) * (MODE == G_GATEUP ? 128 : kGN);
+        r.e = const_load(p.tiles + 1 + 3 * t);
+        r.m0 = const_load(p.tiles + 2 + 3 * t);
+        r.mr = min(const_load(p.tiles + 3 + 3 * t), p.P) - r.m0;
+        return r;
+    };
+    const int chunks = (KB + 7) / 8;
+    auto chunk_first = [&](int c) { return c * KB / chunks; };  // 4 to 8 steps each
+
+    // ---- loads, as in fp8_gemm_kernel
+    const int lr = 8 * wv + (lane >> 3), piece = (lane & 7) ^ g_swz(lr);
+    const uint32_t woff = (uint32_t)g_order(lr) * (uint32_t)K + 16u * (uint32_t)piece;
+    const uint32_t aoff = (uint32_t)lr * (uint32_t)K + 16u * (uint32_t)piece;  // down: rows of a tile are neighbours
+    uint32_t* tok = reinterpret_cast<uint32_t*>(smem + L::TOK);
+    const int32_t* raw = reinterpret_cast<const int32_t*>(smem + L::RAW);
+
+    // where loads stand: tile i of the run, step j, and where its weights and (down) rows begin
+    struct At {
+        uint64_t w, a;
+        uint32_t wb, ab;   // bytes of them
+        int i, j;
+    };
+    auto at_tile = [&](const RunTile& t, int i) {
+        At r;
+        r.w = ((uint64_t)t.e * N + t.n0) * K;
+        r.wb = (MODE == G_GATEUP ? 128u : (uint32_t)min(N - t.n0, kGN)) * (uint32_t)K;
+        r.a = (uint64_t)t.m0 * K;
+        r.ab = (uint32_t)t.mr * (uint32_t)K;
+        r.i = i;
+        r.j = 0;
+        return r;
+    };
+    auto load_w = [&](int n, const At& at, int st) {
+        const uint8_t* src = MODE == G_GATEUP ? (n >= 2 ? p.up : p.gate) : p.down;
+        const uint32_t off = woff + (uint32_t)(MODE == G_GATEUP ? n & 1 : n) * 64u * (uint32_t)K;
+        load16_lds(src + at.w, at.wb, smem + L::W + st * L::B + (8 * n + wv) * 1024, off, at.j * 128);
+    };
+    // load n of a group: weights and first halves of the rows at `a`, second
+    // halves at `b`, one step behind.  Rows past the tile's end: gate/up repeats
+    // some token, down reads zeros; their results are dropped.
+    auto load_group = [&](int n, const At& a, const At& b, int st) {
+        if (n < 4) {
+            load_w(n, a, st);
+            return;
+        }
+        n -= 4;
+        const bool second = ((64 * n + 8 * wv) / (8 * TF)) & 1;
+        const int stage = second ? (st == 0 ? S - 1 : st - 1) : st, i = second ? b.i : a.i, j = second ? b.j : a.j;
+        const uint8_t* src = MODE == G_GATEUP ? p.xq : p.hq + (second ? b.a : a.a);
+        const uint32_t bytes = MODE == G_GATEUP ? (uint32_t)p.T * (uint32_t)K : second ? b.ab : a.ab;
+        const uint32_t off = MODE == G_GATEUP ? tok[(i & 1) * BT + 64 * n + lr] * (uint32_t)K + 16u * (uint32_t)piece
+                                              : aoff + (uint32_t)n * 64u * (uint32_t)K;
+        load16_lds(src, bytes, smem + stage * L::A + (8 * n + wv) * 1024, off, j * 128);
+    };
+    // scales of steps c0 .. c0 + 7 of a tile into buffer `par`: wave v loads step c0 + v
+    auto load_s = [&](const RunTile& t, int i, int c0, int par) {
+        const int kb = min(c0 + wv, KB - 1);
+        const float* rs = MODE == G_GATEUP ? p.xs : p.hs + (size_t)t.m0 * KB;
+        const uint32_t bytes = (uint32_t)(MODE == G_GATEUP ? p.T : t.mr) * (uint32_t)KB * 4u;
+        float* sa = reinterpret_cast<float*>(smem + L::SA) + par * 8 * BT + wv * BT;
+#pragma unroll
+        for (int n = 0; n < NA; ++n) {
+            const uint32_t row = MODE == G_GATEUP ? tok[(i & 1) * BT + 64 * n + lane] : (uint32_t)(64 * n + lane);
+            load4_lds(rs, bytes, sa + 64 * n, row * (uint32_t)KB * 4u, kb * 4);
+        }
+        if (wv < 2 && lane < 8) {
+            // the gate's and the up's, or those of the tile's two blocks of 128 outputs
+            const size_t at = ((size_t)t.e * NB + min(t.n0 / 128 + (MODE == G_GATEUP ? 0 : wv), NB - 1)) * KB;
+            const float* src = MODE == G_GATEUP ? (wv ? p.sup : p.sgate) : p.sdown;
+            float* sw = reinterpret_cast<float*>(smem + L::SW) + par * 16 + wv * 8;
+            load4_lds(src + at, (uint32_t)KB * 4u, sw, (uint32_t)min(c0 + lane, KB - 1) * 4u, 0);
+        }
+    };
+    auto token_row = [&](int r, const RunTile& t, int pair) {
+        if (r >= t.mr) return 0u;
+        return (uint32_t)(p.sorted_pair ? min(max(pair / p.k, 0), p.T - 1) : t.m0 + r);
+    };
+
+    const RunTile first = tile_at(0);
+    RunTile cur = first, nx = count > 1 ? tile_at(1) : first;  // the tile computed, the one after it
+    if (MODE == G_GATEUP) {
+        for (int r = tid; r < BT; r += kGThreads)
+            tok[r] = token_row(r, first, p.sorted_pair && r < first.mr ? p.sorted_pair[first.m0 + r] : 0);
+        __syncthreads();
+    }
+    load_s(first, 0, 0, 0);
+    // (b before the first step: the first step's rows, where the loads of step S - 1 will overwrite them)
+    At a = at_tile(first, 0), b = a;
+    int st = 0;  // stage of `a`
+    auto advance = [&] {
+        b = a;
+        if (++a.j == KB) {
+            if (a.i + 1 < count) a = at_tile(nx, a.i + 1);  // (while the tile before is computed)
+            else a.j = KB - 1;  // past the run's end: the last step again
+        }
+        st = st + 1 == S ? 0 : st + 1;
+    };
+#pragma unroll
+    for (int u = 0; u < S; ++u) {
+#pragma unroll
+        for (int n = 0; n < NL; ++n) load_group(n, a, b, st);
+        advance();
+    }
+
+    const int x0 = 16 * (g ^ g_swz(l16)), x1 = 16 * ((g + 4) ^ g_swz(l16));
+    const int ar = (wt * 16 * TF + l16) * 128;
+    const int br = L::W + ((MODE == G_GATEUP ? 32 * wn : 64 * wn) + l16) * 128;
+    const int sr0 = L::SA + (wt * 16 * TF + l16) * 4;
+    const int sw0 = L::SW + (MODE != G_GATEUP && wn >= 2 ? 32 : 0);
+    auto read16 = [&](int at) {
+        return join8(*reinterpret_cast<const i32x4_t*>(smem + at + x0), *reinterpret_cast<const i32x4_t*>(smem + at + x1));
+    };
+    auto read_a = [&](int stage, int t) { return read16(stage * L::A + ar + t * 2048); };
+    auto read_w = [&](int stage, int f) {
+        return read16(stage * L::B + br + (MODE == G_GATEUP && f >= 2 ? 128 + 16 * (f - 2) : 16 * f) * 128);
+    };
+    auto read_sa = [&](int par, int pos, int t) {
+        return *reinterpret_cast<const float*>(smem + sr0 + (par * 8 + pos) * BT * 4 + t * 64);
+    };
+    auto read_sw = [&](int par, int pos, int half) {
+        return *reinterpret_cast<const float*>(smem + sw0 + par * 64 + pos * 4 + half * 32);
+    };
+    i32x8_t w[4], an;
+    float sn, swn0, swn1 = 0.0f;
+    auto read_first = [&](int stage, int par, int pos) {
+        an = read_a(stage, 0);
+        sn = read_sa(par, pos, 0);
+        swn0 = read_sw(par, pos, 0);
+        if (MODE == G_GATEUP) swn1 = read_sw(par, pos, 1);
+    };
+    wait_and_meet<(S - 1) * NL>();
+#pragma unroll
+    for (int f = 0; f < 4; ++f) w[f] = read_w(0, f);
+    read_first(0, 0, 0);
+
+    constexpr int kMeet = TF / 2 - 1;
+    // position: tile i, step j, step `pos` of a chunk of `len` in scale buffer `par`; `st` is also the
+    // stage of the present step (that of S steps later)
+    int par = 0;
+    for (int i = 0; i < count; ++i) {
+        f32x4_t acc[4][TF];
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int t = 0; t < TF; ++t) acc[f][t] = f32x4_t{};
+        int pos = 0, chunk = 0, len = chunk_first(1);
+#pragma unroll 1
+        for (int j = 0; j < KB; ++j) {
+            const int cs = st;                                 // this step's stage
+            const int ns = st + 1 == S ? 0 : st + 1;           // the next step's
+            const bool turn = pos + 1 == len;
+            const int npos = turn ? 0 : pos + 1, npar = turn ? par ^ 1 : par;
+            f32x4_t v[3];
+            float c0[2], c1[2];
+            const float s0 = swn0, s1 = swn1;
+            auto add = [&](int x) {
+                const int t = x / 4, f = x % 4;
+                const float c = MODE == G_GATEUP && f >= 2 ? c1[t & 1] : c0[t & 1];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) acc[f][t][y] = fmaf(c, v[x % 3][y], acc[f][t][y]);
+            };
+#pragma unroll
+            for (int t = 0; t < TF; ++t) {
+                if (t == kMeet) {
+                    hold(acc, kMeet);
+                    wait_and_meet<(S - 2) * NL>();
+                    if (MODE == G_GATEUP && i + 1 < count) {
+                        if (j == 0 && p.sorted_pair && wv < NA) {
+                            load4_lds(p.sorted_pair + nx.m0, (uint32_t)max(nx.mr, 0) * 4u, smem + L::RAW + wv * 256,
+                                      (uint32_t)(64 * wv + lane) * 4u, 0);
+                        }
+                        if (j == S && tid < BT) tok[((i + 1) & 1) * BT + tid] = token_row(tid, nx, raw[tid]);
+                    }
+                    if (pos == len - S - 1) {
+                        const int c = j - pos + len;  // the next chunk's first step
+                        if (c < KB) load_s(cur, i, c, par ^ 1);
+                        else if (i + 1 < count) load_s(nx, i + 1, 0, par ^ 1);
+                    }
+                }
+                const i32x8_t ac = an;
+                c0[t & 1] = sn * s0;
+                if (MODE == G_GATEUP) c1[t & 1] = sn * s1;
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const int x = 4 * t + f;
+                    v[x % 3] = mfma_fp8<false>(w[f], ac);
+                    if (t + 1 == TF) w[f] = read_w(ns, f);
+                    if (f == 0) {
+                        if (t + 1 < TF) {
+                            an = read_a(cs, t + 1);
+                            sn = read_sa(par, pos, t + 1);
+                        } else {
+                            read_first(ns, npar, npos);
+                        }
+                    }
+                    if (x >= 4 * kMeet && x - 4 * kMeet < NL) load_group(x - 4 * kMeet, a, b, cs);
+                    if (x >= 2) add(x - 2);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            add(4 * TF - 2);
+            add(4 * TF - 1);
+            hold(acc, TF);
+            advance();
+            if (turn) {
+                ++chunk;
+                len = chunk_first(chunk + 1) - chunk_first(chunk);
+            }
+            pos = npos;
+            par = npar;
+        }
+
+        // ---- the tile is done.  (Row and column come from a value the compiler
+        // cannot see through, or it would keep every row's address in registers
+        // across the loop.)
+        int le = lane;
+        asm volatile("" : "+v"(le));
+        const int re = wt * 16 * TF + (le & 15), ge = le >> 4;
+        if constexpr (MODE == G_GATEUP) {
+            uint32_t* amax = reinterpret_cast<uint32_t*>(smem + L::AMAX);
+#pragma unroll
+            for (int t = 0; t < TF; ++t) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const float h = silu(acc[f][t][y]) * acc[f + 2][t][y];
+                        acc[f][t][y] = h;
+                        m = max(m, abs_bits(h));
+                    }
+                m = max(m, (uint32_t)__shfl_xor((int)m, 16, kWave));
+                m = max(m, (uint32_t)__shfl_xor((int)m, 32, kWave));
+                if (ge == 0) amax[wn * BT + re + 16 * t] = m;
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int t = 0; t < TF; ++t) {
+                const int r = re + 16 * t;
+                const uint32_t m = max(max(amax[r], amax[BT + r]), max(amax[2 * BT + r], amax[3 * BT + r]));
+                const float s = fp8_scale(m);
+                if (r < cur.mr) {
+                    *reinterpret_cast<uint2*>(p.hq + (size_t)(cur.m0 + r) * p.F + cur.n0 + 32 * wn + 8 * ge) =
+                        make_uint2(fp8_pack4(acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3], s),
+                                   fp8_pack4(acc[1][t][0], acc[1][t][1], acc[1][t][2], acc[1][t][3], s));
+                    if (wn == 0 && ge == 0) p.hs[(size_t)(cur.m0 + r) * NB + cur.n0 / 128] = s;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < TF; ++t) {
+                const int r = re + 16 * t;
+                if (r < cur.mr) {
+                    char* row = static_cast<char*>(p.rows) + (int64_t)(cur.m0 + r) * p.H * (p.out_f32 ? 4 : 2);
+#pragma unroll
+                    for (int f = 0; f < 4; f += 2) {
+                        const int n = cur.n0 + 64 * wn + 16 * f + 8 * ge;
+                        if (n < N) store8(row, p.out_f32, n, acc[f][t], acc[f + 1][t]);
+                    }
+                }
+            }
+        }
+        cur = nx;
+        if (i + 2 < count) nx = tile_at(i + 2);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load still writes LDS when the workgroup ends
 }
 
 template <int TF, int MODE, bool kExact>
@@ -391,20 +740,36 @@ hipError_t launch_fp8_gemm(const Fp8Dense& d, int bt, hipStream_t s) {
     return launch_one<2, G_DENSE, false>(d, p, tiles(64), s);
 }
 
-hipError_t launch_fp8_gemm_gateup(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s) {
+template <int TF, int MODE>
+static hipError_t launch_run(const Fp8Ffn& p, long tiles, hipStream_t s) {
+    const long grid = tiles < 256 ? (tiles + kXcd - 1) / kXcd * kXcd : 256;
+    const void* fn = reinterpret_cast<const void*>(fp8_run_kernel<TF, MODE>);
+    const hipError_t err = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, RunLds<TF>::TOTAL);
+    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL((fp8_run_kernel<TF, MODE>), dim3((unsigned)grid), dim3(kGThreads), RunLds<TF>::TOTAL, s, p);
+    return hipGetLastError();
+}
+
+template <int TF, int MODE>
+static hipError_t launch_grouped(const Fp8Ffn& p, long tiles, hipStream_t s) {
+    const int KB = (MODE == G_GATEUP ? p.H : p.F) / 128;
+    if (KB >= (MODE == G_GATEUP ? kRunMinKB : kRunMinKBDown)) return launch_run<TF, MODE>(p, tiles, s);
     const Fp8Dense d{};
+    return launch_one<TF, MODE, false>(d, p, tiles, s);
+}
+
+hipError_t launch_fp8_gemm_gateup(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s) {
     const long tiles = max_tiles * (p.F / 128);
-    if (bt == 256) return launch_one<8, G_GATEUP, false>(d, p, tiles, s);
-    if (bt == 128) return launch_one<4, G_GATEUP, false>(d, p, tiles, s);
-    return launch_one<2, G_GATEUP, false>(d, p, tiles, s);
+    if (bt == 256) return launch_grouped<8, G_GATEUP>(p, tiles, s);
+    if (bt == 128) return launch_grouped<4, G_GATEUP>(p, tiles, s);
+    return launch_grouped<2, G_GATEUP>(p, tiles, s);
 }
 
 hipError_t launch_fp8_gemm_down(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s) {
-    const Fp8Dense d{};
     const long tiles = max_tiles * ((p.H + kGN - 1) / kGN);
-    if (bt == 256) return launch_one<8, G_DOWN, false>(d, p, tiles, s);
-    if (bt == 128) return launch_one<4, G_DOWN, false>(d, p, tiles, s);
-    return launch_one<2, G_DOWN, false>(d, p, tiles, s);
+    if (bt == 256) return launch_grouped<8, G_DOWN>(p, tiles, s);
+    if (bt == 128) return launch_grouped<4, G_DOWN>(p, tiles, s);
+    return launch_grouped<2, G_DOWN>(p, tiles, s);
 }
 
 }  // namespace moe

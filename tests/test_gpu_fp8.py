@@ -194,7 +194,10 @@ def _sorted(idx, E):
 
 
 FFN = [(1, 256, 128, 4, 2), (5, 128, 256, 16, 3), (16, 384, 128, 8, 2), (40, 256, 384, 3, 2), (70, 512, 128, 2, 1), (300, 256, 256, 4, 2),
-       (700, 384, 128, 3, 3), (1100, 128, 128, 2, 2)]
+       (700, 384, 128, 3, 3), (1100, 128, 128, 2, 2),
+       # deep enough for runs of tiles, with one tile a workgroup and with several; 64-, 128- and 256-row tiles
+       (70, 2560, 640, 2, 1), (300, 1024, 512, 4, 2), (700, 1152, 640, 3, 3), (260, 1280, 1024, 8, 2), (9000, 1024, 1152, 4, 2),
+       (5000, 1152, 512, 64, 2), (2000, 2176, 640, 32, 1)]
 
 
 @pytest.mark.parametrize("out", [moe.OUT_BF16, moe.OUT_F32])
