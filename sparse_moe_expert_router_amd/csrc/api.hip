@@ -473,6 +473,9 @@ moe_status moe_layer_few(const uint16_t* x, int32_t T, const uint16_t* w_router,
         return MOE_ERR_SHAPE;
     }
     if (T > moe::kFewMaxT || k > 64 || !moe::few_supported(experts, shared)) return MOE_ERR_UNSUPPORTED;
+    // rows are addressed with 32 bits
+    constexpr int kMost = 1 << 20;
+    if (H > kMost || experts->inter > kMost || (shared && shared->inter > kMost)) return MOE_ERR_UNSUPPORTED;
     if (T == 0) return MOE_OK;
     if (!x || !w_router || !y) return MOE_ERR_NULL;
     if (!aligned16(x) || !aligned16(w_router) || !aligned16(y) || (uintptr_t)shared_scale % 4 || (uintptr_t)topk_idx % 4)
@@ -480,6 +483,8 @@ moe_status moe_layer_few(const uint16_t* x, int32_t T, const uint16_t* w_router,
     if (ws_bytes < moe::few_ws_bytes(T, k, experts, shared)) return MOE_ERR_WORKSPACE;
     if (!ws) return MOE_ERR_NULL;
     if (!aligned16(ws)) return MOE_ERR_UNSUPPORTED;
+    // x is read until the last output is written
+    if (y < x + (size_t)T * H && x < y + (size_t)T * H) return MOE_ERR_SHAPE;
     return hip_status(moe::launch_layer_few(x, T, w_router, k, experts, shared, shared_scale, y, topk_idx, ws,
                                             static_cast<hipStream_t>(stream)));
 }

@@ -12,11 +12,10 @@
 //  few_experts_kernel: every workgroup selects the top k of every token by
 //    itself from the logits (cheaper than a third launch or a wait).  All of
 //    them then take gate/up items (an expert's columns) until none is left and
-//    write gate_tj h; load their first down rows and do their part of the shared
-//    expert; wait until all items are done; and sum the experts for their share
-//    of the outputs in fp32, in a fixed order.  Up to five workgroups share the
-//    same 16 outputs; the last of them to finish adds the parts, again in a fixed
-//    order.
+//    write gate_tj h; load their first down rows; wait until all items are done;
+//    and sum the experts, and the shared expert, for their share of the outputs
+//    in fp32, in a fixed order.  Up to five workgroups share the same 16 outputs;
+//    the last of them to finish adds the parts, again in a fixed order.
 //
 // The wait always ends: it begins when no gate/up item is left untaken, so each
 // of them is in the hands of a running workgroup, and those wait for nothing
@@ -33,9 +32,18 @@
 // possible tokens, a token that is not routed to the expert reading zeros
 // (without memory traffic).  Weights stream 16 bytes a lane: 8 bf16, 16 E4M3
 // or 32 4-bit inputs of one row, widened to bf16 exactly; their scales are
-// applied to the fp32 sums, so nothing is rounded but h and y, both to bf16.  Against dot products on the vector
-// units this is a fifth of the instructions, which counts twice at one token,
-// where every instruction runs once and is fetched from memory.
+// applied to the fp32 sums, so nothing is rounded but h and y, both to bf16.
+// Against dot products on the vector units this is a fifth of the instructions,
+// which counts twice at one token, where every instruction runs once and is
+// fetched from memory.
+//
+// Measured, hidden 2560, 10 of 512 experts of 640, a shared expert of 640: one
+// token in 39 (FP8), 40 (4-bit) and 50 us (bf16), of which the bytes need 13, 8
+// and 24; the layer of separate kernels takes 55 to 65, 63 to 69 and 59 to 67.
+// Four tokens take about the same either way (74 to 110 us).  16 take 206, 194
+// and 325 us here and 155, 137 and 251 there: of the 206 the front takes 12,
+// selection 9, gate/up 98 (4.6 TB/s), the items' ends and the wait 11, down 58
+// (3.9 TB/s).
 #include "fp8.h"
 #include "ffn_internal.h"
 #include "select.h"
@@ -151,6 +159,13 @@ __device__ __forceinline__ void load_unit(UnitData<FMT>& d, const Rows<FMT>& r, 
     }
 }
 
+// (v & mask) | c in one instruction: it takes one of the two constants from a
+// scalar register, so c is kept in a vector register.
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t c) {
+    asm("" : "+v"(c));
+    return (v & mask) | c;
+}
+
 // The MFMA operands of a unit's weights.
 template <int FMT>
 __device__ __forceinline__ void unit_frags(const UnitData<FMT>& d, bf16x8_t (&a)[Unit<FMT>::FRAGS]) {
@@ -180,7 +195,7 @@ __device__ __forceinline__ void unit_frags(const UnitData<FMT>& d, bf16x8_t (&a)
         for (int j = 0; j < 4; ++j) {
             u32x4_t v;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = ((q[j] >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+            for (int i = 0; i < 4; ++i) v[i] = and_or(q[j] >> (4 * i), 0x000F000Fu, 0x43004300u);
             a[j] = __builtin_bit_cast(bf16x8_t, v);
         }
     }
@@ -204,7 +219,7 @@ __device__ __forceinline__ f32x4_t mfma32(bf16x8_t a, bf16x8_t b, f32x4_t c) {
 // The value of lane J of each 16 (row_newbcast).
 template <int J>
 __device__ __forceinline__ uint32_t row_lane(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x150 + J, 0xF, 0xF, false);
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x150 + J, 0xF, 0xF, true);
 }
 
 // One group of a 4-bit unit: acc += s (sum (128 + q) x - (128 + z) sum x).
@@ -218,7 +233,9 @@ __device__ __forceinline__ void awq_group(f32x4_t& acc, const UnitData<F_AWQ>& d
     const uint32_t gs[2] = {row_lane<J>(d.gs[0]), row_lane<J>(d.gs[1])};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float z = (float)((zw >> ((i & 1) * 16 + (i >> 1) * 4)) & 15u) + 128.0f;
+        // 128 + z: its bits are 0x43000000 | z << 16
+        const uint32_t zn = i == 0 ? zw << 16 : i == 1 ? zw : i == 2 ? zw << 12 : zw >> 4;
+        const float z = __uint_as_float(and_or(zn, 0x000F0000u, 0x43000000u));
         const float s = f16_to_f32((gs[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
         acc[i] = fmaf(s, fmaf(-z, sum[i], v[i]), acc[i]);
     }
@@ -256,9 +273,10 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// Units of a batch, under way at once.  Six waves a SIMD hide one another's
-// loads; longer batches, or the next one's weights loaded ahead, cost registers
-// and so waves, and measured slower (16 tokens, FP8: 226 us with two waves).
+// Units of a batch, under way at once.  The four waves of a SIMD hide one
+// another's loads; longer batches, or the next one's weights loaded ahead, cost
+// registers and so waves, and measured slower (16 tokens, FP8: 226 us with two
+// waves).
 template <int FMT>
 constexpr int kBatch = FMT == F_AWQ ? 2 : FMT == F_FP8 ? 5 : 10;
 
@@ -325,7 +343,7 @@ __device__ __forceinline__ f32x4_t gateup_join(const f32x4_t (*part)[kWave], int
 
 // h of four neighbouring columns, rounded to bf16 as the layer of separate
 // kernels does: kept in 16 bits more the down pass has twice the loads of it,
-// and their number bounds that pass (16 tokens, FP8: 72 us of 213).
+// and their number bounds that pass (16 tokens, FP8: 72 us against 58).
 __device__ __forceinline__ void store_h(__amdgpu_buffer_rsrc_t r, uint32_t row, int F, int col, f32x4_t h, bool agent) {
     const u32x2_t a = {pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])};
     const uint32_t at = (row * (uint32_t)F + (uint32_t)col) * 2u;
@@ -335,7 +353,8 @@ __device__ __forceinline__ void store_h(__amdgpu_buffer_rsrc_t r, uint32_t row, 
 
 // Units v0 .. v1 of the F inputs of a list of experts, one after another, into
 // 16 outputs from o0.  expert(slot), hoff(slot): the slot's expert and the byte
-// offset of the lane's token's h (kOob: not routed to it).  `ready` is called once the first U units are under way.
+// offset of the lane's token's h (kOob: not routed to it).  `ready` is called
+// once the first U units are under way.
 template <int FMT, int U, class Expert, class Hoff, class Ready>
 __device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int H, int F, int o0, __amdgpu_buffer_rsrc_t rh,
                                            int v0, int v1, Expert expert, Hoff hoff, Ready ready) {
@@ -445,8 +464,8 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_front_kernel(const FewArgs
 // workgroups share a compute unit): P pairs, at most S touched experts.
 struct FewLists {
     f32x4_t (*part)[kFewWaves][kWave];    // [2]
-    uint2 (*cand)[kWave];                 // [waves], the selection's
-    uint32_t (*lane_max)[kWave];          // [waves]
+    uint2 (*cand)[kWave];                 // [waves], the selection's: in part, which is used after it
+    uint32_t (*lane_max)[kWave];          // [waves], likewise
     int32_t* idx;                         // [P] expert of pair t k + j
     float* gate;                          // [P]
     int32_t* wave_slots;                  // [waves]
@@ -456,8 +475,8 @@ struct FewLists {
     uint16_t* slot_of;                    // [1024] expert -> slot
     uint16_t* expert;                     // [S] slot -> expert, ascending
 
-    __host__ __device__ static size_t bytes(int P, int S) {
-        return 2 * kFewWaves * kWave * 16 + kFewWaves * kWave * 12 + (size_t)P * 8 + (kFewWaves + 2 + kRanges) * 4 +
+    __host__ __device__ static constexpr size_t bytes(int P, int S) {
+        return 2 * kFewWaves * kWave * 16 + (size_t)P * 8 + (kFewWaves + 2 + kRanges) * 4 +
                (size_t)S * kFewMaxT * 2 + 1024 * 2 + (size_t)S * 2;
     }
     __device__ __forceinline__ void place(uint8_t* m, int P, int S) {
@@ -467,8 +486,8 @@ struct FewLists {
             return at;
         };
         part = reinterpret_cast<f32x4_t(*)[kFewWaves][kWave]>(take(2 * kFewWaves * kWave * 16));
-        cand = reinterpret_cast<uint2(*)[kWave]>(take(kFewWaves * kWave * 8));
-        lane_max = reinterpret_cast<uint32_t(*)[kWave]>(take(kFewWaves * kWave * 4));
+        cand = reinterpret_cast<uint2(*)[kWave]>(part);
+        lane_max = reinterpret_cast<uint32_t(*)[kWave]>(cand + kFewWaves);
         idx = reinterpret_cast<int32_t*>(take((size_t)P * 4));
         gate = reinterpret_cast<float*>(take((size_t)P * 4));
         wave_slots = reinterpret_cast<int32_t*>(take(kFewWaves * 4));
@@ -479,6 +498,7 @@ struct FewLists {
         expert = reinterpret_cast<uint16_t*>(take((size_t)S * 2));
     }
 };
+static_assert(FewLists::bytes(kFewMaxPairs, 1024) <= 64 * 1024, "what a launch gets without asking");
 
 // Top k of token t's E <= 512 logits by one wave.  Lane i holds experts 8 i ..
 // 8 i + 7.  Fewer than k of the lanes' largest logits lie above some lane's
@@ -849,7 +869,7 @@ hipError_t launch_layer_few(const uint16_t* x, int T, const uint16_t* router, in
     a.h = reinterpret_cast<uint16_t*>(w);
     a.y = y;
     a.topk_idx = topk_idx;
-    // three workgroups a compute unit, which the registers allow; fewer where there is less to do
+    // two workgroups a compute unit, which the registers allow; fewer where there is less to do
     const int nc = a.H / 16;
     a.down_wgs = nc * (kFewSplits - 1) < 512 ? nc * (kFewSplits - 1) : 512;
     const int most = T * k < a.E ? T * k : a.E;

@@ -60,3 +60,34 @@ def test_the_binding_refuses():
             few(x)
     with pytest.raises(moe.MoeError, match="5 tokens"):
         few(torch.zeros((5, 256), dtype=torch.bfloat16))
+
+
+def test_refuses_overlap_and_sizes_past_32_bits():
+    L = moe.lib()
+    b = _bank()
+    n = L.moe_layer_few_workspace_bytes(8, 2, ctypes.byref(b), None)
+
+    def call(x, y, bank=b):
+        return L.moe_layer_few(ctypes.c_void_p(x), 8, FAKE, 2, ctypes.byref(bank), None, None, ctypes.c_void_p(y), None, FAKE,
+                               n, None)
+    end = 8 * 256 * 2
+    for x, y in ((4096, 4096), (4096, 4096 + end - 16), (4096 + end - 16, 4096)):
+        assert call(x, y) == SHAPE
+    for big in (_bank(H=(1 << 20) + 128), _bank(F=(1 << 20) + 128)):
+        assert call(4096, 1 << 30, big) == UNSUP
+
+
+def test_the_binding_refuses_other_devices():
+    mk = lambda dev: {"fmt": "bf16", "gate": torch.zeros((4, 128, 256), dtype=torch.bfloat16, device=dev),
+                      "up": torch.zeros((4, 128, 256), dtype=torch.bfloat16, device=dev),
+                      "down": torch.zeros((4, 256, 128), dtype=torch.bfloat16, device=dev)}
+    router = torch.zeros((4, 256), dtype=torch.bfloat16)
+    with pytest.raises(moe.MoeError, match="different devices"):
+        moe.FewTokenLayer(router, 2, mk("meta"))
+    few = moe.FewTokenLayer(router, 2, mk("cpu"), max_tokens=4,
+                            ws=type("W", (), {"get": lambda s, n: (torch.empty(n, dtype=torch.uint8), n)})())
+    x = torch.zeros((2, 256), dtype=torch.bfloat16)
+    for kw in ({"y": x.to("meta")}, {"topk_idx": torch.zeros((2, 2), dtype=torch.int32, device="meta")},
+               {"shared_scale": torch.zeros(2, device="meta")}):
+        with pytest.raises(moe.MoeError, match="different devices"):
+            few(x, **kw)

@@ -78,3 +78,21 @@ def test_the_binding_refuses_what_would_read_out_of_bounds():
         moe.fp8_quantize(torch.zeros((4, 128), dtype=torch.float16))
     with pytest.raises(moe.MoeError, match="fp8 bank"):
         moe.grouped_ffn_a8(torch.zeros((4, 128), dtype=torch.bfloat16), 1, {"fmt": "bf16"})
+
+
+def test_the_binding_refuses_other_devices():
+    mk = lambda dev: {"fmt": "fp8", "gate_codes": torch.zeros((2, 128, 256), dtype=torch.uint8, device=dev),
+                      "up_codes": torch.zeros((2, 128, 256), dtype=torch.uint8, device=dev),
+                      "down_codes": torch.zeros((2, 256, 128), dtype=torch.uint8, device=dev),
+                      "gate_bscales": torch.ones((2, 1, 2), device=dev), "up_bscales": torch.ones((2, 1, 2), device=dev),
+                      "down_bscales": torch.ones((2, 2, 1), device=dev)}
+    x = torch.zeros((4, 256), dtype=torch.bfloat16)
+    off, sp = torch.zeros(3, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
+    for args in ((mk("meta"), off, sp), (mk("cpu"), off.to("meta"), sp), (mk("cpu"), off, sp.to("meta"))):
+        with pytest.raises(moe.MoeError, match="different devices"):
+            moe.grouped_ffn_a8(x, 1, *args)
+    with pytest.raises(moe.MoeError, match="different devices"):
+        moe.fp8_quantize(x, codes=torch.zeros((4, 256), dtype=torch.uint8, device="meta"))
+    with pytest.raises(moe.MoeError, match="different devices"):
+        moe.fp8_matmul(torch.zeros((4, 128), dtype=torch.uint8), torch.ones((4, 1)),
+                       torch.zeros((8, 128), dtype=torch.uint8, device="meta"), torch.ones((1, 1)))

@@ -148,6 +148,33 @@ def test_two_streams_at_once():
             assert torch.equal(y, want) and torch.equal(idx, widx)
 
 
+def test_every_list_at_its_largest():
+    """16 tokens of 64 among 1024 experts: the most pairs, touched experts and LDS of a call."""
+    x, router, bank, shared = _make(16, 256, 1024, 64, 128, 32, "bf16")
+    y, idx = moe.layer_few(x, router, 64, bank, shared)
+    _check(y, idx, R.layer(x, router, 64, bank, shared))
+
+
+def test_calls_without_a_workspace_on_two_streams():
+    x, router, bank, shared = _make(16, 1024, 64, 6, 256, 64, "fp8")
+    want, widx = moe.layer_few(x, router, 6, bank, shared)
+    made_here = moe.FewTokenLayer(router, 6, bank, shared)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    out = []
+    for i in range(10):
+        for s in streams:
+            with torch.cuda.stream(s):
+                out.append(moe.layer_few(x, router, 6, bank, shared))
+    with torch.cuda.stream(streams[1]):
+        out.append(made_here(x))
+    del made_here
+    torch.cuda.synchronize()
+    for y, idx in out:
+        assert torch.equal(y, want) and torch.equal(idx, widx)
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "awq_om"])
 def test_agrees_with_the_layer_of_separate_kernels(fmt):
     """moe_layer rounds h and the experts' rows to bf16: three roundings of 2^-8 on the way, of terms that
