@@ -43,9 +43,10 @@ static size_t a8_tiles_bytes(long P, int E, int bt) { return up256((1 + 3 * a8_m
 
 // Tile table: tiles[0] = number of tiles, then (expert, first row, end row).
 // An expert with n rows gets ceil(n / bt) tiles of equal size, rounded up to
-// 16 rows (the last one shorter).
+// 16 rows (the last one shorter).  Offsets that do not ascend from 0 to P may
+// ask for more tiles than the table holds; those are left out.
 __global__ __launch_bounds__(1024) void a8_tile_table_kernel(const int32_t* __restrict__ offsets, int E, int P, int bt,
-                                                             int32_t* __restrict__ tiles) {
+                                                             int most, int32_t* __restrict__ tiles) {
     __shared__ int scan[1024];
     const int e = threadIdx.x;
     int cnt = 0, r0 = 0;
@@ -68,12 +69,12 @@ __global__ __launch_bounds__(1024) void a8_tile_table_kernel(const int32_t* __re
         __syncthreads();
     }
     const int start = scan[e] - nt;
-    for (int i = 0; i < nt; ++i) {
+    for (int i = 0; i < nt && start + i < most; ++i) {
         tiles[1 + 3 * (start + i)] = e;
         tiles[2 + 3 * (start + i)] = r0 + i * sz;
         tiles[3 + 3 * (start + i)] = min(r0 + (i + 1) * sz, r0 + cnt);
     }
-    if (e == 1023) tiles[0] = scan[1023];
+    if (e == 1023) tiles[0] = min(scan[1023], most);
 }
 
 // Grows with T: the tile table is sized for 16-row tiles throughout.
@@ -106,7 +107,7 @@ hipError_t launch_ffn_a8(const FfnArgs& f, void* ws, hipStream_t s) {
     w += up256((size_t)p.P * p.F);
     p.hs = reinterpret_cast<float*>(w);
     p.tiles = tiles; p.xq = xq; p.xs = xs;
-    hipLaunchKernelGGL(a8_tile_table_kernel, dim3(1), dim3(1024), 0, s, p.offsets, p.E, p.P, bt, tiles);
+    hipLaunchKernelGGL(a8_tile_table_kernel, dim3(1), dim3(1024), 0, s, p.offsets, p.E, p.P, bt, (int)mt, tiles);
     hipError_t err = launch_fp8_quantize(f.x, 0, p.T, p.H, p.H, xq, xs, s);
     if (err != hipSuccess) return err;
     if (bt == 16) return launch_fp8_skinny_ffn(p, (int)mt, s);

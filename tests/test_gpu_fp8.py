@@ -305,3 +305,103 @@ def test_on_a_side_stream():
     s.synchronize()
     assert torch.equal(got, want)
     assert torch.equal(c, moe.fp8_quantize(x)[0])
+
+
+# ------------------------------------------------------------------ many rows through runs of tiles, and long offsets
+
+@pytest.mark.parametrize("T", [150, 513, 1500])
+def test_experts_identity_deep(T):
+    x = torch.randn((T, 1024), generator=_gen(4)).bfloat16()
+    bank = _bank(1, 1024, 512, 5)
+    rows = moe.grouped_ffn_a8(x.to(DEV), 1, _gpu(bank))
+    _check_experts(rows, x, 1, bank, torch.tensor([0, T]), torch.arange(T).int())
+
+
+@pytest.mark.parametrize("T", [300, 1100])
+def test_experts_deep_with_empty_experts_and_nan_rows(T):
+    H, F, E, k = 1024, 512, 12, 2
+    x = torch.randn((T, H), generator=_gen(6)).bfloat16()
+    bank = _bank(E, H, F, 3)
+    idx = torch.full((T, k), 7)
+    idx[:, 1] = 10
+    idx[3], idx[-1] = torch.tensor([0, 11]), torch.tensor([7, 0])
+    off, sp = _sorted(idx, E)
+    args = (k, _gpu(bank), off.to(DEV), sp.to(DEV))
+    rows = moe.grouped_ffn_a8(x.to(DEV), *args)
+    _check_experts(rows, x, k, bank, off, sp)
+    x[3, 17], x[5, 0] = float("inf"), float("nan")
+    got = moe.grouped_ffn_a8(x.to(DEV), *args).cpu()
+    tok = sp.long() // k
+    bad = (tok == 3) | (tok == 5)
+    assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], rows.cpu()[~bad])
+
+
+def test_experts_deep_replays_and_surroundings():
+    T, H, F, E, k = 700, 1152, 512, 3, 2
+    bank = _gpu(_bank(E, H, F, 2))
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device=DEV)
+    off, sp = _sorted(torch.rand((T, E), generator=_gen(8)).topk(k, 1).indices, E)
+    off, sp = off.to(DEV), sp.to(DEV)
+    big = torch.full((T * k + 2, H), 7.0, dtype=torch.bfloat16, device=DEV)
+    rows = big[1:-1]
+    ws = moe.Workspace(x.device)
+    moe.grouped_ffn_a8(x, k, bank, off, sp, ws=ws, rows=rows)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.grouped_ffn_a8(x, k, bank, off, sp, ws=ws, rows=rows)
+    for i in range(4):
+        x.copy_(torch.randn((T, H), generator=_gen(i)).bfloat16())
+        graph.replay()
+        torch.cuda.synchronize()
+        got = rows.clone()
+        assert torch.equal(got, moe.grouped_ffn_a8(x, k, bank, off, sp))
+    assert (big[0] == 7).all() and (big[-1] == 7).all()
+
+
+@pytest.mark.parametrize("M", [60, 1100])
+def test_offsets_past_32_bits(M):
+    """Rows 4 MiB apart (the most a product takes), 1100 of them (w, and a and y too): 4.6 GB from the first to the
+    last."""
+    K, N, ld = 256, 1100, 1 << 22
+    g = _gen(M)
+    a, w = _codes((M, K), g), _codes((N, K), g)
+    sa, sw = torch.rand((M, 2), generator=g), torch.rand((-(-N // 128), 2), generator=g)
+    buf = [torch.empty(ld * rows, dtype=torch.uint8, device=DEV) for rows in (M, N, M)]
+    A, W = (b.as_strided((rows, K), (ld, 1)) for b, rows in ((buf[0], M), (buf[1], N)))
+    y = buf[2].view(torch.bfloat16).as_strided((M, N), (ld // 2, 1))
+    A.copy_(a), W.copy_(w)
+    moe.fp8_matmul(A, sa.to(DEV), W, sw.to(DEV), y=y)
+    _check_product(y.contiguous(), a, sa, w, sw)
+    x = torch.randn((M, K), generator=g).bfloat16()
+    y = buf[2].view(torch.bfloat16).as_strided((M, K), (ld // 2, 1))
+    y.copy_(x)
+    codes, s = moe.fp8_quantize(y)
+    rc, rs = R.quantize(x.double())
+    assert torch.equal(codes.cpu(), rc) and torch.equal(s.cpu().double(), rs)
+
+
+def test_experts_rows_past_32_bits():
+    """1.1 million rows of 1024 fp32 outputs, 4.6 GB: those of its first, last and some other tokens."""
+    T, H, F = 1_100_003, 1024, 512
+    x = torch.randn((T, H), dtype=torch.bfloat16, device=DEV)
+    bank = _bank(1, H, F, 5)
+    rows = moe.grouped_ffn_a8(x, 1, _gpu(bank), out_dtype=moe.OUT_F32)
+    pick = torch.cat([torch.arange(16), torch.arange(1, 33) * 33331, torch.arange(T - 16, T)]).to(DEV)
+    _check_experts(rows[pick], x[pick].cpu(), 1, bank, torch.tensor([0, 64]), torch.arange(64).int())
+
+
+@pytest.mark.parametrize("T,H,F", [(40, 256, 128), (900, 1024, 512)])
+def test_experts_offsets_that_overlap_stay_inside_the_workspace(T, H, F):
+    """Wrong offsets give wrong rows, but nothing behind the workspace or the rows is written."""
+    E = 64
+    bank = _gpu(_bank(E, H, F, 1))
+    x = torch.randn((T, H), dtype=torch.bfloat16, device=DEV)
+    off = torch.tensor([0, T] * 32 + [T], dtype=torch.int32, device=DEV)
+    sp = torch.arange(T, dtype=torch.int32, device=DEV)
+    n = moe.workspace_bytes(moe.OP_GROUPED_FFN_A8, T, 1, E, H, F)
+    buf = torch.full((n + (1 << 20),), 77, dtype=torch.uint8, device=DEV)
+    big = torch.full((T + 1, H), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = type("W", (), {"get": lambda s, m: (buf, n)})()
+    moe.grouped_ffn_a8(x, 1, bank, off, sp, ws=ws, rows=big[:T])
+    assert (buf[n:] == 77).all() and (big[T] == 7).all()
