@@ -6,22 +6,32 @@
 
 namespace moe {
 
-// Dense products up to this many rows stream the weights (fp8_skinny.hip).
-constexpr int kSkinnyRows = 128;
+// Whether a dense product streams the weights (fp8_skinny.hip): while all of its
+// workgroups, 16 outputs x 32 rows each, are resident at once (two a compute
+// unit); beyond that they read rows and weights too often.  With very few rows
+// there is nothing but the weights to read.  Measured, streaming / 64-row tiles,
+// us: 96 x 2560 x 2560 (480 workgroups) 11.7 / 15.6, 128 rows (640) 16.4 / 15.6;
+// 32 x 8192 x 8192 (512) 31 / 38, 64 rows (1024) 59 / 38; 512 x 512 x 2560 (512)
+// 11.8 / 15.6; 16384 x 8192 (1024), one row 26 / 38, 16 rows 40 / 38.
+static bool dense_streams(int M, int N) { return M <= 8 || fp8_skinny_workgroups(M, N) <= 512; }
 
-// Rows of a dense tile: the largest that still gives every compute unit one.
+// Rows of a dense tile.  256 tiles run at once, and such a round takes times as
+// 10 : 16 : 24 for tiles of 64, 128 and 256 rows (8192 x 8192: 512 rows 46 us,
+// 1024 77, 2048 117); the fewest of these units wins.  (4096 x 2560 x 2560: 3
+// rounds of 64 rows 48.6 us, 2 of 128 50.5, 1 of 256 41.4; 1024 x 2560 x 2560, one
+// round of any: 17.7, 24.5, 36.4.)
 static int dense_bt(int M, int N) {
     const long nt = (N + 255) / 256;
-    if ((M + 255) / 256 * nt >= 256) return 256;
-    if ((M + 127) / 128 * nt >= 128) return 128;
-    return 64;
+    auto cost = [&](long rows, long round) { return ((M + rows - 1) / rows * nt + 255) / 256 * round; };
+    const long c64 = cost(64, 10), c128 = cost(128, 16), c256 = cost(256, 24);
+    return c64 <= c128 && c64 <= c256 ? 64 : c128 <= c256 ? 128 : 256;
 }
 
 hipError_t launch_fp8_matmul(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, int M, int N, int K,
                              int64_t lda, int64_t ldw, int out_f32, void* y, int64_t ldy, hipStream_t s) {
     Fp8Dense p{a, sa, w, sw, M, N, K, lda, ldw, ldy, y, out_f32, 0};
     p.vec = (uintptr_t)y % 16 == 0 && ldy % (out_f32 ? 4 : 8) == 0;
-    if (M <= kSkinnyRows) return launch_fp8_skinny(p, s);
+    if (dense_streams(M, N)) return launch_fp8_skinny(p, s);
     return launch_fp8_gemm(p, dense_bt(M, N), s);
 }
 
@@ -32,11 +42,20 @@ static size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 // Row tiles of at most bt rows over E experts: at most one partial tile per expert.
 static size_t a8_max_tiles(long P, int E, int bt) { return (size_t)(P / bt + (P < E ? P : E)); }
 
-// Rows of a tile by the average rows of an expert that has any: 16 (the
-// streaming kernels) to 256.
-static int a8_bt(long P, int E) {
-    const long avg = P / (P < E ? P : E);
-    return avg >= 160 ? 256 : avg >= 80 ? 128 : avg >= 24 ? 64 : 16;
+// Rows of a tile.  64 while an expert with rows has fewer on average, and also
+// while all tiles run at once; 256 from 160 rows on average, where that still
+// makes four rounds of 256 tiles, so that the last one's unevenness counts little.
+// Measured with hidden 2560, inter 640, tiles of 64 / 128 / 256 rows, us.  Rows on
+// average over 64 experts: 8 79 / 91 / 128, 48 92 / 101 / 136, 80 112 / 109 / 142, 128
+// 140 / 119 / 150, 320 234 / 202 / 226; over 256: 64 330 / 295 / 380, 128 446 / 397 /
+// 412, 192 583 / 491 / 442, 640 1507 / 1251 / 1199, 1280 2863 / 2332 / 2160.  Hidden
+// 4096, inter 1152, 128 rows on average over 8 experts: 56 / 61 / 83.  (Down to one
+// row per expert a tile of 16 rows gains nothing: the weights' bytes bound the call.)
+static int a8_bt(long P, int E, int F) {
+    const long active = P < E ? P : E, avg = P / active, cols = F / 128;
+    auto tiles = [&](long rows) { return (P / rows + active / 2) * cols; };
+    if (avg < 64 || tiles(64) <= 256) return 64;
+    return avg >= 160 && tiles(256) >= 1024 ? 256 : 128;
 }
 
 static size_t a8_tiles_bytes(long P, int E, int bt) { return up256((1 + 3 * a8_max_tiles(P, E, bt)) * sizeof(int32_t)); }
@@ -77,10 +96,10 @@ __global__ __launch_bounds__(1024) void a8_tile_table_kernel(const int32_t* __re
     if (e == 1023) tiles[0] = min(scan[1023], most);
 }
 
-// Grows with T: the tile table is sized for 16-row tiles throughout.
+// Grows with T: the tile table is sized for 64-row tiles throughout.
 size_t ffn_a8_ws_bytes(int T, int k, int E, int H, int F) {
     const long P = (long)T * k;
-    return a8_tiles_bytes(P, E, 16) + up256((size_t)T * H) + up256((size_t)T * fp8_blocks(H) * 4) +
+    return a8_tiles_bytes(P, E, 64) + up256((size_t)T * H) + up256((size_t)T * fp8_blocks(H) * 4) +
            up256((size_t)P * F) + up256((size_t)P * fp8_blocks(F) * 4);
 }
 
@@ -94,7 +113,7 @@ hipError_t launch_ffn_a8(const FfnArgs& f, void* ws, hipStream_t s) {
     p.sgate = f.ex->gate.block_scales; p.sup = f.ex->up.block_scales; p.sdown = f.ex->down.block_scales;
     p.rows = f.rows;
     p.out_f32 = f.out_f32;
-    const int bt = a8_bt(p.P, p.E);
+    const int bt = a8_bt(p.P, p.E, p.F);
     const long mt = (long)a8_max_tiles(p.P, p.E, bt);
     char* w = static_cast<char*>(ws);
     int32_t* tiles = reinterpret_cast<int32_t*>(w);
@@ -110,7 +129,6 @@ hipError_t launch_ffn_a8(const FfnArgs& f, void* ws, hipStream_t s) {
     hipLaunchKernelGGL(a8_tile_table_kernel, dim3(1), dim3(1024), 0, s, p.offsets, p.E, p.P, bt, (int)mt, tiles);
     hipError_t err = launch_fp8_quantize(f.x, 0, p.T, p.H, p.H, xq, xs, s);
     if (err != hipSuccess) return err;
-    if (bt == 16) return launch_fp8_skinny_ffn(p, (int)mt, s);
     err = launch_fp8_gemm_gateup(p, bt, mt, s);
     if (err != hipSuccess) return err;
     return launch_fp8_gemm_down(p, bt, mt, s);

@@ -35,7 +35,7 @@ struct Fp8Ffn {
 };
 
 hipError_t launch_fp8_skinny(const Fp8Dense& p, hipStream_t s);
-hipError_t launch_fp8_skinny_ffn(const Fp8Ffn& p, int max_tiles, hipStream_t s);
+long fp8_skinny_workgroups(int M, int N);
 
 // Tiles of bt rows (256, 128 or 64) x 256 outputs.
 hipError_t launch_fp8_gemm(const Fp8Dense& d, int bt, hipStream_t s);
