@@ -454,9 +454,10 @@ moe_status moe_fp8_matmul(const uint8_t *a, const float *a_scales, const uint8_t
  * FP8 as well: x and the SwiGLU product h are quantised as moe_fp8_quantize
  * does (h per row and group of 128 inner columns, from its fp32 values), and
  * all three products run on the FP8 matrix cores as moe_fp8_matmul computes
- * them for bf16 outputs (for fp32 rows too).  Same arguments, layouts and errors as moe_grouped_ffn; any other
- * format -> MOE_ERR_UNSUPPORTED, as are T * hidden >= 2^32 values.  A row of
- * x that holds an infinity or a NaN gives NaN in its own rows only.
+ * them for bf16 outputs (for fp32 rows too).  Same arguments, layouts and
+ * errors as moe_grouped_ffn; any other format -> MOE_ERR_UNSUPPORTED, as are
+ * T * hidden >= 2^32 values and a hidden or inter size above 2^20.  A row of x
+ * that holds an infinity or a NaN gives NaN in its own rows only.
  * Workspace: moe_workspace_bytes(MOE_OP_GROUPED_FFN_A8, T, k, E, H, F).
  */
 moe_status moe_grouped_ffn_a8(const uint16_t *x, int32_t T, int32_t k, const moe_experts *ex,

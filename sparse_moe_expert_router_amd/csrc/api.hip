@@ -699,7 +699,8 @@ moe_status moe_grouped_ffn_a8(const uint16_t* x, int32_t T, int32_t k, const moe
     if (st != MOE_OK) return st;
     if (ex->gate.fmt != MOE_W_FP8_BLOCK) return MOE_ERR_UNSUPPORTED;
     // quantised rows are addressed with 32 bits
-    if ((uint64_t)T * ex->hidden >= (1ull << 32)) return MOE_ERR_UNSUPPORTED;
+    if ((uint64_t)T * ex->hidden >= (1ull << 32) || ex->hidden > (1 << 20) || ex->inter > (1 << 20))
+        return MOE_ERR_UNSUPPORTED;
     if (T == 0) return MOE_OK;
     need = moe::ffn_a8_ws_bytes(T, k, ex->num_experts, ex->hidden, ex->inter);
     if (ws_bytes < need) return MOE_ERR_WORKSPACE;

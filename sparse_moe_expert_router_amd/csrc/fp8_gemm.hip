@@ -25,6 +25,14 @@
 // half of step j - 1's.  After M_j the wave issues the loads that refill these,
 // of S steps later (S stages); they are waited for at M_{j + S - 1}, so every
 // load has S - 1 whole steps to land and nothing stops at the step's border.
+//
+// Measured: 8192 x 8192 x 8192 in 484 us, 2.27 PFLOP/s; 32768 tokens to 10 of 256
+// experts (hidden 2560, inter 640): gate/up 1270 us, 1.69 PFLOP/s, down 817 us, of
+// which its 1.7 GB of rows need 340.  The MFMA is busy 56, 45 and 36 % of the cycles
+// (1.93 GHz under this load): every 128 products of an output need an fp32
+// multiply-add outside it, and with the operands' loads the vector instructions
+// take as long again as the MFMA; gate/up adds SwiGLU and the division of the
+// quantisation (35 and 48 us), both the tail rows of each expert's last tile.
 #include "fp8.h"
 #include "ffn_internal.h"
 #include "fp8_internal.h"
@@ -466,6 +474,10 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_run_kernel(const Fp8Ffn p) {
     uint32_t* tok = reinterpret_cast<uint32_t*>(smem + L::TOK);
     const int32_t* raw = reinterpret_cast<const int32_t*>(smem + L::RAW);
 
+    // gate/up: where the rows of the wave's loads begin, kept for the length of a
+    // tile (read from LDS before each load, their waits cost a tenth of the pass)
+    uint32_t rowoff[NA] = {};
+
     // where loads stand: tile i of the run, step j, and where its weights and (down) rows begin
     struct At {
         uint64_t w, a;
@@ -487,6 +499,8 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_run_kernel(const Fp8Ffn p) {
         const uint32_t off = woff + (uint32_t)(MODE == G_GATEUP ? n & 1 : n) * 64u * (uint32_t)K;
         load16_lds(src + at.w, at.wb, smem + L::W + st * L::B + (8 * n + wv) * 1024, off, at.j * 128);
     };
+    // whether the wave's row load n belongs to the second half of the rows
+    auto second_half = [&](int n) { return (((64 * n + 8 * wv) / (8 * TF)) & 1) != 0; };
     // load n of a group: weights and first halves of the rows at `a`, second
     // halves at `b`, one step behind.  Rows past the tile's end: gate/up repeats
     // some token, down reads zeros; their results are dropped.
@@ -496,13 +510,18 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_run_kernel(const Fp8Ffn p) {
             return;
         }
         n -= 4;
-        const bool second = ((64 * n + 8 * wv) / (8 * TF)) & 1;
-        const int stage = second ? (st == 0 ? S - 1 : st - 1) : st, i = second ? b.i : a.i, j = second ? b.j : a.j;
+        const bool second = second_half(n);
+        const int stage = second ? (st == 0 ? S - 1 : st - 1) : st, j = second ? b.j : a.j;
         const uint8_t* src = MODE == G_GATEUP ? p.xq : p.hq + (second ? b.a : a.a);
         const uint32_t bytes = MODE == G_GATEUP ? (uint32_t)p.T * (uint32_t)K : second ? b.ab : a.ab;
-        const uint32_t off = MODE == G_GATEUP ? tok[(i & 1) * BT + 64 * n + lr] * (uint32_t)K + 16u * (uint32_t)piece
-                                              : aoff + (uint32_t)n * 64u * (uint32_t)K;
+        const uint32_t off = MODE == G_GATEUP ? rowoff[n] : aoff + (uint32_t)n * 64u * (uint32_t)K;
         load16_lds(src, bytes, smem + stage * L::A + (8 * n + wv) * 1024, off, j * 128);
+    };
+    auto row_offsets = [&](bool second, int i) {  // of tile i, of one half of the rows
+        if (MODE != G_GATEUP) return;
+#pragma unroll
+        for (int n = 0; n < NA; ++n)
+            if (second_half(n) == second) rowoff[n] = tok[(i & 1) * BT + 64 * n + lr] * (uint32_t)K + 16u * (uint32_t)piece;
     };
     // scales of steps c0 .. c0 + 7 of a tile into buffer `par`: wave v loads step c0 + v
     auto load_s = [&](const RunTile& t, int i, int c0, int par) {
@@ -539,11 +558,18 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_run_kernel(const Fp8Ffn p) {
     // (b before the first step: the first step's rows, where the loads of step S - 1 will overwrite them)
     At a = at_tile(first, 0), b = a;
     int st = 0;  // stage of `a`
+    row_offsets(false, 0);
+    row_offsets(true, 0);
     auto advance = [&] {
+        if (MODE == G_GATEUP && a.i != b.i) row_offsets(true, a.i);
         b = a;
         if (++a.j == KB) {
-            if (a.i + 1 < count) a = at_tile(nx, a.i + 1);  // (while the tile before is computed)
-            else a.j = KB - 1;  // past the run's end: the last step again
+            if (a.i + 1 < count) {
+                a = at_tile(nx, a.i + 1);  // (while the tile before is computed)
+                row_offsets(false, a.i);
+            } else {
+                a.j = KB - 1;  // past the run's end: the last step again
+            }
         }
         st = st + 1 == S ? 0 : st + 1;
     };
@@ -586,6 +612,10 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_run_kernel(const Fp8Ffn p) {
     read_first(0, 0, 0);
 
     constexpr int kMeet = TF / 2 - 1;
+    // Memory operations complete in order, and a tile's stores are the last before
+    // the next tile: the loads that its first S - 1 steps wait for are older, so
+    // those steps leave the stores under way.  Every wave issues at least this many.
+    constexpr int NST = 2 * TF;
     // position: tile i, step j, step `pos` of a chunk of `len` in scale buffer `par`; `st` is also the
     // stage of the present step (that of S steps later)
     int par = 0;
@@ -615,7 +645,8 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_run_kernel(const Fp8Ffn p) {
             for (int t = 0; t < TF; ++t) {
                 if (t == kMeet) {
                     hold(acc, kMeet);
-                    wait_and_meet<(S - 2) * NL>();
+                    if (i > 0 && j < S - 1) wait_and_meet<(S - 2) * NL + NST>();
+                    else wait_and_meet<(S - 2) * NL>();
                     if (MODE == G_GATEUP && i + 1 < count) {
                         if (j == 0 && p.sorted_pair && wv < NA) {
                             load4_lds(p.sorted_pair + nx.m0, (uint32_t)max(nx.mr, 0) * 4u, smem + L::RAW + wv * 256,
@@ -688,31 +719,40 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_run_kernel(const Fp8Ffn p) {
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
+            // (the stores of rows past the tile's end, and all but one lane's of a
+            // scale, fall outside their buffers: each is issued all the same)
+            const __amdgpu_buffer_rsrc_t rq = fp8_rsrc(p.hq + (size_t)cur.m0 * p.F, (uint32_t)cur.mr * (uint32_t)p.F);
+            const __amdgpu_buffer_rsrc_t rs = fp8_rsrc(p.hs + (size_t)cur.m0 * NB, (uint32_t)(cur.mr * NB) * 4u);
 #pragma unroll
             for (int t = 0; t < TF; ++t) {
                 const int r = re + 16 * t;
                 const uint32_t m = max(max(amax[r], amax[BT + r]), max(amax[2 * BT + r], amax[3 * BT + r]));
                 const float s = fp8_scale(m);
-                if (r < cur.mr) {
-                    *reinterpret_cast<uint2*>(p.hq + (size_t)(cur.m0 + r) * p.F + cur.n0 + 32 * wn + 8 * ge) =
-                        make_uint2(fp8_pack4(acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3], s),
-                                   fp8_pack4(acc[1][t][0], acc[1][t][1], acc[1][t][2], acc[1][t][3], s));
-                    if (wn == 0 && ge == 0) p.hs[(size_t)(cur.m0 + r) * NB + cur.n0 / 128] = s;
-                }
+                const u32x2_t q = {fp8_pack4(acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3], s),
+                                   fp8_pack4(acc[1][t][0], acc[1][t][1], acc[1][t][2], acc[1][t][3], s)};
+                __builtin_amdgcn_raw_buffer_store_b64(q, rq, r * p.F + cur.n0 + 32 * wn + 8 * ge, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), rs,
+                                                      wn == 0 && ge == 0 ? (r * NB + cur.n0 / 128) * 4 : (int)kOob, 0, 0);
             }
         } else {
+            const uint32_t rowb = (uint32_t)p.H * (p.out_f32 ? 4u : 2u);
+            const __amdgpu_buffer_rsrc_t rr = fp8_rsrc(static_cast<char*>(p.rows) + (size_t)cur.m0 * rowb, (uint32_t)cur.mr * rowb);
 #pragma unroll
-            for (int t = 0; t < TF; ++t) {
-                const int r = re + 16 * t;
-                if (r < cur.mr) {
-                    char* row = static_cast<char*>(p.rows) + (int64_t)(cur.m0 + r) * p.H * (p.out_f32 ? 4 : 2);
+            for (int t = 0; t < TF; ++t)
 #pragma unroll
-                    for (int f = 0; f < 4; f += 2) {
-                        const int n = cur.n0 + 64 * wn + 16 * f + 8 * ge;
-                        if (n < N) store8(row, p.out_f32, n, acc[f][t], acc[f + 1][t]);
+                for (int f = 0; f < 4; f += 2) {
+                    const int n = cur.n0 + 64 * wn + 16 * f + 8 * ge;
+                    const f32x4_t u = acc[f][t], v = acc[f + 1][t];
+                    const uint32_t at = n < N ? (uint32_t)(re + 16 * t) * rowb + (uint32_t)n * (p.out_f32 ? 4u : 2u) : kOob;
+                    if (p.out_f32) {
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, u), rr, (int)at, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rr, (int)(at + 16u), 0, 0);
+                    } else {
+                        const u32x4_t o = {pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(v[0], v[1]),
+                                           pack_bf16x2(v[2], v[3])};
+                        __builtin_amdgcn_raw_buffer_store_b128(o, rr, (int)at, 0, 0);
                     }
                 }
-            }
         }
         cur = nx;
         if (i + 2 < count) nx = tile_at(i + 2);

@@ -96,3 +96,11 @@ def test_the_binding_refuses_other_devices():
     with pytest.raises(moe.MoeError, match="different devices"):
         moe.fp8_matmul(torch.zeros((4, 128), dtype=torch.uint8), torch.ones((4, 1)),
                        torch.zeros((8, 128), dtype=torch.uint8, device="meta"), torch.ones((1, 1)))
+
+
+def test_experts_refuse_sizes_past_32_bits():
+    def ffn(T, H, F):
+        b = _bank(H=H, F=F)
+        return moe.lib().moe_grouped_ffn_a8(FAKE, T, 1, ctypes.byref(b), FAKE, FAKE, 0, FAKE, FAKE, 1 << 60, None)
+    assert ffn(8, (1 << 20) + 128, 128) == UNSUP and ffn(8, 128, (1 << 20) + 128) == UNSUP
+    assert ffn(1 << 22, 1024, 128) == UNSUP
