@@ -38,12 +38,11 @@
 // fetched from memory.
 //
 // Measured, hidden 2560, 10 of 512 experts of 640, a shared expert of 640: one
-// token in 39 (FP8), 40 (4-bit) and 50 us (bf16), of which the bytes need 13, 8
+// token in 38 (FP8), 39 (4-bit) and 47 us (bf16), of which the bytes need 13, 8
 // and 24; the layer of separate kernels takes 55 to 65, 63 to 69 and 59 to 67.
-// Four tokens take about the same either way (74 to 110 us).  16 take 206, 194
-// and 325 us here and 155, 137 and 251 there: of the 206 the front takes 12,
-// selection 9, gate/up 98 (4.6 TB/s), the items' ends and the wait 11, down 58
-// (3.9 TB/s).
+// Four tokens take the same either way (70 to 98 us).  16 take 188, 179 and 284
+// us here and 155, 137 and 251 there: of the 188 the front takes 12, selection
+// 9, gate/up 98 (4.6 TB/s), the items' ends and the wait 11.
 #include "fp8.h"
 #include "ffn_internal.h"
 #include "select.h"
@@ -273,10 +272,10 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// Units of a batch, under way at once.  The four waves of a SIMD hide one
-// another's loads; longer batches, or the next one's weights loaded ahead, cost
-// registers and so waves, and measured slower (16 tokens, FP8: 226 us with two
-// waves).
+// Units of a gate/up batch, under way at once.  The four waves of a SIMD hide
+// one another's loads; longer batches cost registers and so waves (16 tokens,
+// FP8: 226 us with two waves), and the next batch's weights loaded ahead gain
+// nothing here (4-bit 195 against 188 us, FP8 188 both).
 template <int FMT>
 constexpr int kBatch = FMT == F_AWQ ? 2 : FMT == F_FP8 ? 5 : 10;
 
@@ -354,7 +353,8 @@ __device__ __forceinline__ void store_h(__amdgpu_buffer_rsrc_t r, uint32_t row, 
 // Units v0 .. v1 of the F inputs of a list of experts, one after another, into
 // 16 outputs from o0.  expert(slot), hoff(slot): the slot's expert and the byte
 // offset of the lane's token's h (kOob: not routed to it).  `ready` is called
-// once the first U units are under way.
+// once the first U units are under way.  The next U units' weights are loaded
+// before the present ones are used (16 tokens, FP8: 205 -> 189 us, bf16 320 -> 285).
 template <int FMT, int U, class Expert, class Hoff, class Ready>
 __device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int H, int F, int o0, __amdgpu_buffer_rsrc_t rh,
                                            int v0, int v1, Expert expert, Hoff hoff, Ready ready) {
@@ -362,8 +362,7 @@ __device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int 
     constexpr int FR = Un::FRAGS;
     const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
     const int n = F / Un::IN;
-    UnitData<FMT> d[U];
-    for (int vb = v0; vb < v1 || vb == v0; vb += U) {
+    auto load_w = [&](UnitData<FMT> (&d)[U], int vb) {
 #pragma unroll
         for (int i = 0; i < U; ++i)
             if (vb + i < v1) {
@@ -372,7 +371,11 @@ __device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int 
                 r.init(pd, o0 + l16, pd, o0 + 4 * g, pd, pd, o0, expert(slot), H, F, lane);
                 load_unit<FMT>(d[i], r, v - slot * n);
             }
-        if (vb == v0) ready();
+    };
+    UnitData<FMT> d[U], next[U];
+    load_w(d, v0);
+    ready();
+    for (int vb = v0; vb < v1; vb += U) {
         u32x4_t h[U][FR];
 #pragma unroll
         for (int i = 0; i < U; ++i)
@@ -386,6 +389,7 @@ __device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int 
                         u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rh, at != kOob ? (int)(at + 2u * in) : (int)kOob, 0, 0));
                 }
             }
+        load_w(next, vb + U);
 #pragma unroll
         for (int i = 0; i < U; ++i)
             if (vb + i < v1) {
@@ -394,6 +398,8 @@ __device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int 
                 for (int j = 0; j < FR; ++j) b[j] = input_frag<FMT>(h[i][j]);
                 unit_product<FMT>(acc, d[i], b, 8 * (g & 1));
             }
+#pragma unroll
+        for (int i = 0; i < U; ++i) d[i] = next[i];
     }
 }
 
@@ -664,9 +670,13 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_experts_kernel(const FewAr
 
     // ---- gate/up.  An item is 8 columns of an expert for each group of `ks`
     // waves, which split the inputs and are joined in their order through LDS:
-    // few items are cut finely, many keep a wave on longer runs.
+    // few items are cut finely, many keep a wave on longer runs, and the 4-bit
+    // rows, half as long, take the coarser cut.  (Hidden 2560, 640 columns, cut in
+    // 8 / 4 / 2.  16 tokens, about 138 experts: FP8 195 / 188 / 189 us, 4-bit 203 /
+    // 187 / 179; 4 tokens: FP8 70 / 72 / -, 4-bit 74 / 71 / -.)
     const int cols8 = slots * (a.F / 8);
-    const int ks = cols8 >= 1024 ? 4 : 8, cw = kFewWaves / ks;
+    const int ks = cols8 < 1024 ? 8 : cols8 < 4096 ? (FMT == F_AWQ ? 4 : 8) : FMT == F_AWQ ? 2 : 4;
+    const int cw = kFewWaves / ks;
     const int per = (a.F / 8 + cw - 1) / cw, items = slots * per;
     const int ranges = min(items, kRanges);
     {
@@ -762,7 +772,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_experts_kernel(const FewAr
         const int64_t cb = (int64_t)c * n, ce = v1 < cb + n ? v1 : cb + n;  // the run's units of this group: v .. ce
         const int b0 = (int)(v - cb), len = (int)(ce - v);
         f32x4_t acc = {};
-        down_units<FMT, (FMT == F_FP8 ? 6 : FMT == F_AWQ ? 2 : 10)>(
+        down_units<FMT, (FMT == F_FP8 ? 5 : FMT == F_AWQ ? 2 : 6)>(
             acc, a.down, a.H, a.F, o0, rh, b0 + len * wv / kFewWaves,
             b0 + len * (wv + 1) / kFewWaves, [&](int u) { return __builtin_amdgcn_readfirstlane((int)s.expert[u]); },
             [&](int u) {
