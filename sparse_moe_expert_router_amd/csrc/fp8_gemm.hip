@@ -31,8 +31,8 @@
 // which its 1.7 GB of rows need 340.  The MFMA is busy 56, 45 and 36 % of the cycles
 // (1.93 GHz under this load): every 128 products of an output need an fp32
 // multiply-add outside it, and with the operands' loads the vector instructions
-// take as long again as the MFMA; gate/up adds SwiGLU and the division of the
-// quantisation (35 and 48 us), both the tail rows of each expert's last tile.
+// take as long again as the MFMA; gate/up adds SwiGLU and the quantisation (35 and
+// 48 us), both the tail rows of each expert's last tile.
 #include "fp8.h"
 #include "ffn_internal.h"
 #include "fp8_internal.h"
@@ -369,9 +369,10 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_gemm_kernel(const Fp8Dense d
             const int r = wt * 16 * TF + 16 * t + l16;
             const uint32_t m = max(max(amax[r], amax[BT + r]), max(amax[2 * BT + r], amax[3 * BT + r]));
             const float s = fp8_scale(m);
+            const Fp8Div by = fp8_div(s);
             *reinterpret_cast<uint2*>(smem + r * LD + 32 * wn + 8 * g) =
-                make_uint2(fp8_pack4(acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3], s),
-                           fp8_pack4(acc[1][t][0], acc[1][t][1], acc[1][t][2], acc[1][t][3], s));
+                make_uint2(fp8_pack4(acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3], by),
+                           fp8_pack4(acc[1][t][0], acc[1][t][1], acc[1][t][2], acc[1][t][3], by));
             if (wn == 0 && g == 0 && r < mr) p.hs[(size_t)(m0 + r) * NB + n0 / 128] = s;
         }
         __syncthreads();
@@ -728,8 +729,9 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_run_kernel(const Fp8Ffn p) {
                 const int r = re + 16 * t;
                 const uint32_t m = max(max(amax[r], amax[BT + r]), max(amax[2 * BT + r], amax[3 * BT + r]));
                 const float s = fp8_scale(m);
-                const u32x2_t q = {fp8_pack4(acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3], s),
-                                   fp8_pack4(acc[1][t][0], acc[1][t][1], acc[1][t][2], acc[1][t][3], s)};
+                const Fp8Div by = fp8_div(s);
+                const u32x2_t q = {fp8_pack4(acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3], by),
+                                   fp8_pack4(acc[1][t][0], acc[1][t][1], acc[1][t][2], acc[1][t][3], by)};
                 __builtin_amdgcn_raw_buffer_store_b64(q, rq, r * p.F + cur.n0 + 32 * wn + 8 * ge, 0, 0);
                 __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), rs,
                                                       wn == 0 && ge == 0 ? (r * NB + cur.n0 / 128) * 4 : (int)kOob, 0, 0);

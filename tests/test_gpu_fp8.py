@@ -70,6 +70,20 @@ def test_quantize_strided_rows_and_empty():
     assert c0.shape == (0, 128) and s0.shape == (0, 1)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantize_over_the_range_of_scales(dtype):
+    """Rows of every magnitude, down to denormal values and up to the type's largest; codes and scales bit for bit (the
+    reference's quotient is a 64-bit one rounded to fp32, which is the fp32 quotient: 53 >= 2 * 24 + 2 bits)."""
+    k = torch.arange(-145, 127).repeat_interleave(8)
+    x = torch.randn((k.numel(), 512), generator=_gen(9), dtype=torch.float64).clamp(-1.9, 1.9)
+    x[:, 128:256] = (torch.randint(-16, 17, (k.numel(), 128), generator=_gen(10)) / 16 * 1.75).double()   # many ties
+    x[:, 256:384] *= 2.0 ** -torch.randint(0, 24, (k.numel(), 128), generator=_gen(11)).double()
+    x = (x * torch.exp2(k.double())[:, None]).to(dtype)
+    codes, s = moe.fp8_quantize(x.to(DEV))
+    rc, rs = R.quantize(x.double())
+    assert torch.equal(s.cpu().double(), rs) and torch.equal(codes.cpu(), rc)
+
+
 # ------------------------------------------------------------------ product
 
 def _codes(shape, g):
