@@ -19,7 +19,7 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kFp8Block = 128;             // values per scale
-constexpr uint32_t kOob = 0x80000000u;     // a buffer offset past every buffer used here (they stay below 2 GiB)
+constexpr uint32_t kOob = 0x80000000u;     // past the end of every buffer it is used with (below 2 GiB)
 
 // Number of scales of a row of n values.
 __host__ __device__ __forceinline__ int fp8_blocks(int n) { return (n + kFp8Block - 1) / kFp8Block; }
