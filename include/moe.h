@@ -287,9 +287,8 @@ size_t moe_layer_workspace_bytes(int32_t T, int32_t k, const moe_experts *expert
  * products before the gate, and the experts' rows to bf16 on the
  * way, so the two differ by those roundings).  experts: bf16, FP8 or
  * output-major AWQ; shared (nullable): one bf16 expert of the same hidden
- * size; other formats, T > 16, k > 64, a hidden or inter size above 2^20
- * -> MOE_ERR_UNSUPPORTED; y overlapping x -> MOE_ERR_SHAPE.  Other
- * requirements and errors as moe_layer's.
+ * size; other formats, T > 16 or k > 64 -> MOE_ERR_UNSUPPORTED; y overlapping
+ * x -> MOE_ERR_SHAPE.  Other requirements and errors as moe_layer's.
  *   ws: moe_layer_few_workspace_bytes(T, k, experts, shared) bytes, 16-byte
  *   aligned, of any content.  Two calls that may run at the same time need
  *   two workspaces (one call clearing the other's counters can leave y NaN).
@@ -456,8 +455,8 @@ moe_status moe_fp8_matmul(const uint8_t *a, const float *a_scales, const uint8_t
  * all three products run on the FP8 matrix cores as moe_fp8_matmul computes
  * them for bf16 outputs (for fp32 rows too).  Same arguments, layouts and
  * errors as moe_grouped_ffn; any other format -> MOE_ERR_UNSUPPORTED, as are
- * T * hidden >= 2^32 values and a hidden or inter size above 2^20.  A row of x
- * that holds an infinity or a NaN gives NaN in its own rows only.
+ * T * hidden >= 2^32 values.  A row of x that holds an infinity or a NaN gives
+ * NaN in its own rows only.
  * Workspace: moe_workspace_bytes(MOE_OP_GROUPED_FFN_A8, T, k, E, H, F).
  */
 moe_status moe_grouped_ffn_a8(const uint16_t *x, int32_t T, int32_t k, const moe_experts *ex,

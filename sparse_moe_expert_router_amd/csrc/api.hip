@@ -473,9 +473,6 @@ moe_status moe_layer_few(const uint16_t* x, int32_t T, const uint16_t* w_router,
         return MOE_ERR_SHAPE;
     }
     if (T > moe::kFewMaxT || k > 64 || !moe::few_supported(experts, shared)) return MOE_ERR_UNSUPPORTED;
-    // rows are addressed with 32 bits
-    constexpr int kMost = 1 << 20;
-    if (H > kMost || experts->inter > kMost || (shared && shared->inter > kMost)) return MOE_ERR_UNSUPPORTED;
     if (T == 0) return MOE_OK;
     if (!x || !w_router || !y) return MOE_ERR_NULL;
     if (!aligned16(x) || !aligned16(w_router) || !aligned16(y) || (uintptr_t)shared_scale % 4 || (uintptr_t)topk_idx % 4)
@@ -699,8 +696,7 @@ moe_status moe_grouped_ffn_a8(const uint16_t* x, int32_t T, int32_t k, const moe
     if (st != MOE_OK) return st;
     if (ex->gate.fmt != MOE_W_FP8_BLOCK) return MOE_ERR_UNSUPPORTED;
     // quantised rows are addressed with 32 bits
-    if ((uint64_t)T * ex->hidden >= (1ull << 32) || ex->hidden > (1 << 20) || ex->inter > (1 << 20))
-        return MOE_ERR_UNSUPPORTED;
+    if ((uint64_t)T * ex->hidden >= (1ull << 32)) return MOE_ERR_UNSUPPORTED;
     if (T == 0) return MOE_OK;
     need = moe::ffn_a8_ws_bytes(T, k, ex->num_experts, ex->hidden, ex->inter);
     if (ws_bytes < need) return MOE_ERR_WORKSPACE;

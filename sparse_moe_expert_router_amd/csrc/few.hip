@@ -25,8 +25,8 @@
 // Items are counted in 16 ranges, a cache line each: one counter for all took
 // 20 ns an item, more than the item's work.
 // h passes between compute dies, whose L2s are not coherent within a kernel:
-// stores and loads of it go past them (agent scope, sc1), and a store has
-// completed before its workgroup counts itself done.
+// stores of it go past them (agent scope, sc1) and have completed before their
+// workgroup counts itself done; loads of it follow an acquire fence after the wait.
 //
 // The products run on the bf16 16 x 16 x 32 MFMA: 16 weight rows x the 16
 // possible tokens, a token that is not routed to the expert reading zeros

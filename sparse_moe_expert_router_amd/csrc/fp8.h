@@ -72,6 +72,61 @@ __device__ __forceinline__ uint32_t fp8_pack4(float v0, float v1, float v2, floa
 // Bit pattern of |v|.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
+// Maximum over the 8 lanes of an aligned group, in every lane of it.
+__device__ __forceinline__ uint32_t max8_u32(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));   // quad_perm 1,0,3,2
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));   // quad_perm 2,3,0,1
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));  // row_half_mirror
+    return v;
+}
+
+// Piece p of the flat list [T][8 nb] is 16 values: row p / (8 nb), values
+// 16 (p % (8 nb)) .. +15 of it; pieces past the row's end (n % 128 != 0) only
+// take part in the maximum.
+template <bool kF32>
+__device__ __forceinline__ void fp8_quantize_piece(uint32_t p, const void* __restrict__ x, uint32_t pieces, int n, int nb,
+                                                   int64_t stride, uint8_t* __restrict__ codes, float* __restrict__ scales) {
+    const uint32_t row = p / (uint32_t)(8 * nb), c = p - row * (uint32_t)(8 * nb);
+    const bool in = p < pieces && (int)(16 * c) < n;
+    float v[16];
+    if (in) {
+        if (kF32) {
+            const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(x) + row * stride + 16 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 q = s[i];
+                v[4 * i] = __uint_as_float(q.x);
+                v[4 * i + 1] = __uint_as_float(q.y);
+                v[4 * i + 2] = __uint_as_float(q.z);
+                v[4 * i + 3] = __uint_as_float(q.w);
+            }
+        } else {
+            const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + row * stride + 16 * c);
+            const uint4 a = s[0], b = s[1];
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, abs_bits(v[i]));
+    const float s = fp8_scale(max8_u32(m));
+    if (!in) return;
+    const Fp8Div d = fp8_div(s);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = fp8_pack4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], d);
+    *reinterpret_cast<uint4*>(codes + (size_t)row * n + 16 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+    if (c % 8 == 0) scales[(size_t)row * nb + c / 8] = s;
+}
+
 // 16 x 16 x 128 E4M3 product of one block, no accumulator: lane l of `rows`
 // holds 32 values of row l % 16, lane l of `cols` the same 32 inputs of column
 // l % 16; result i of lane l is row 4 (l / 16) + i, column l % 16.  Which 32

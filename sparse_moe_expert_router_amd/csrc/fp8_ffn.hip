@@ -60,13 +60,15 @@ static int a8_bt(long P, int E, int F) {
 
 static size_t a8_tiles_bytes(long P, int E, int bt) { return up256((1 + 3 * a8_max_tiles(P, E, bt)) * sizeof(int32_t)); }
 
+constexpr int kPrepThreads = 1024;  // at least the most experts
+
 // Tile table: tiles[0] = number of tiles, then (expert, first row, end row).
 // An expert with n rows gets ceil(n / bt) tiles of equal size, rounded up to
 // 16 rows (the last one shorter).  Offsets that do not ascend from 0 to P may
 // ask for more tiles than the table holds; those are left out.
-__global__ __launch_bounds__(1024) void a8_tile_table_kernel(const int32_t* __restrict__ offsets, int E, int P, int bt,
-                                                             int most, int32_t* __restrict__ tiles) {
-    __shared__ int scan[1024];
+__device__ __forceinline__ void a8_tile_table(const int32_t* __restrict__ offsets, int E, int P, int bt, int most,
+                                              int32_t* __restrict__ tiles) {
+    __shared__ int scan[kPrepThreads];
     const int e = threadIdx.x;
     int cnt = 0, r0 = 0;
     if (offsets) {
@@ -81,7 +83,7 @@ __global__ __launch_bounds__(1024) void a8_tile_table_kernel(const int32_t* __re
     const int sz = nt ? ((cnt + nt - 1) / nt + 15) / 16 * 16 : 0;
     scan[e] = nt;
     __syncthreads();
-    for (int off = 1; off < 1024; off <<= 1) {
+    for (int off = 1; off < kPrepThreads; off <<= 1) {
         const int v = e >= off ? scan[e - off] : 0;
         __syncthreads();
         scan[e] += v;
@@ -93,7 +95,22 @@ __global__ __launch_bounds__(1024) void a8_tile_table_kernel(const int32_t* __re
         tiles[2 + 3 * (start + i)] = r0 + i * sz;
         tiles[3 + 3 * (start + i)] = min(r0 + (i + 1) * sz, r0 + cnt);
     }
-    if (e == 1023) tiles[0] = min(scan[1023], most);
+    if (e == kPrepThreads - 1) tiles[0] = min(scan[kPrepThreads - 1], most);
+}
+
+// What the products need first, in one launch: workgroup 0 writes the tile table,
+// the others quantise x.  (Against two launches, 16 tokens of 512 experts: 139.5
+// -> 136.5 us.)
+__global__ __launch_bounds__(kPrepThreads) void a8_prepare_kernel(const Fp8Ffn p, const uint16_t* __restrict__ x, int bt, int most,
+                                                                  int32_t* __restrict__ tiles, uint8_t* __restrict__ xq,
+                                                                  float* __restrict__ xs) {
+    if (blockIdx.x == 0) {
+        a8_tile_table(p.offsets, p.E, p.P, bt, most, tiles);
+    } else {
+        const int nb = p.H / 128;
+        fp8_quantize_piece<false>((blockIdx.x - 1) * (uint32_t)kPrepThreads + threadIdx.x, x, (uint32_t)p.T * 8u * (uint32_t)nb, p.H,
+                                  nb, p.H, xq, xs);
+    }
 }
 
 // Grows with T: the tile table is sized for 64-row tiles throughout.
@@ -126,8 +143,10 @@ hipError_t launch_ffn_a8(const FfnArgs& f, void* ws, hipStream_t s) {
     w += up256((size_t)p.P * p.F);
     p.hs = reinterpret_cast<float*>(w);
     p.tiles = tiles; p.xq = xq; p.xs = xs;
-    hipLaunchKernelGGL(a8_tile_table_kernel, dim3(1), dim3(1024), 0, s, p.offsets, p.E, p.P, bt, (int)mt, tiles);
-    hipError_t err = launch_fp8_quantize(f.x, 0, p.T, p.H, p.H, xq, xs, s);
+    const uint32_t pieces = (uint32_t)p.T * (uint32_t)(p.H / 16);
+    hipLaunchKernelGGL(a8_prepare_kernel, dim3(1 + (pieces + kPrepThreads - 1) / kPrepThreads), dim3(kPrepThreads), 0, s, p, f.x,
+                       bt, (int)mt, tiles, xq, xs);
+    hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     err = launch_fp8_gemm_gateup(p, bt, mt, s);
     if (err != hipSuccess) return err;
