@@ -419,3 +419,18 @@ def test_experts_offsets_that_overlap_stay_inside_the_workspace(T, H, F):
     ws = type("W", (), {"get": lambda s, m: (buf, n)})()
     moe.grouped_ffn_a8(x, 1, bank, off, sp, ws=ws, rows=big[:T])
     assert (buf[n:] == 77).all() and (big[T] == 7).all()
+
+
+@pytest.mark.parametrize("T", [1, 77, 700])
+def test_quantiser_and_products_make_the_expert(T):
+    """One expert from the separate calls: quantise, gate and up with fp32 outputs, SwiGLU in torch's fp32 (within the
+    bound of the kernel's), quantise, down; against the same 64-bit expert as the grouped call."""
+    H, F = 384, 256
+    x = torch.randn((T, H), generator=_gen(12)).bfloat16()
+    bank = _bank(1, H, F, 13)
+    g = _gpu(bank)
+    a, sa = moe.fp8_quantize(x.to(DEV))
+    gate, up = (moe.fp8_matmul(a, sa, g[n + "_codes"][0], g[n + "_bscales"][0], out_dtype=moe.OUT_F32) for n in ("gate", "up"))
+    h, sh = moe.fp8_quantize(torch.nn.functional.silu(gate) * up)
+    rows = moe.fp8_matmul(h, sh, g["down_codes"][0], g["down_bscales"][0])
+    _check_experts(rows, x, 1, bank, torch.tensor([0, T]), torch.arange(T).int())
