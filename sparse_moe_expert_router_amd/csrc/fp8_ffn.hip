@@ -1,5 +1,7 @@
 // Dispatch of the W8A8 products: dense (moe_fp8_matmul) and grouped experts
 // (moe_grouped_ffn_a8).
+#include <limits.h>
+
 #include "ffn_internal.h"
 #include "fp8.h"
 #include "fp8_internal.h"
@@ -12,18 +14,23 @@ namespace moe {
 // there is nothing but the weights to read.  Measured, streaming / 64-row tiles,
 // us: 96 x 2560 x 2560 (480 workgroups) 11.7 / 15.6, 128 rows (640) 16.4 / 15.6;
 // 32 x 8192 x 8192 (512) 31 / 38, 64 rows (1024) 59 / 38; 512 x 512 x 2560 (512)
-// 11.8 / 15.6; 16384 x 8192 (1024), one row 26 / 38, 16 rows 40 / 38.
-static bool dense_streams(int M, int N) { return M <= 8 || fp8_skinny_workgroups(M, N) <= 512; }
+// 11.8 / 15.6; 16384 x 8192 (1024), one row 26 / 38, 16 rows 40 / 38.  With fp32
+// outputs the tiles take nearly twice as long, streaming the same: 64 x 8192 x
+// 8192 (1024) 61 / 71, 96 rows (1536) 89 / 72; 256 x 2560 x 2560 (1280) 26.7 / 27.0.
+static bool dense_streams(int M, int N, int out_f32) {
+    return M <= 8 || fp8_skinny_workgroups(M, N) <= (out_f32 ? 1024 : 512);
+}
 
 // Rows of a dense tile.  256 tiles run at once, and such a round takes times as
 // 10 : 16 : 24 for tiles of 64, 128 and 256 rows (8192 x 8192: 512 rows 46 us,
 // 1024 77, 2048 117); the fewest of these units wins.  (4096 x 2560 x 2560: 3
 // rounds of 64 rows 48.6 us, 2 of 128 50.5, 1 of 256 41.4; 1024 x 2560 x 2560, one
-// round of any: 17.7, 24.5, 36.4.)
-static int dense_bt(int M, int N) {
+// round of any: 17.7, 24.5, 36.4.)  fp32 outputs have the first two: 1024 x 8192 x
+// 8192 in 2 rounds of 64 rows 156 us, one of 128 124; 512 rows 83, 113.
+static int dense_bt(int M, int N, int out_f32) {
     const long nt = (N + 255) / 256;
     auto cost = [&](long rows, long round) { return ((M + rows - 1) / rows * nt + 255) / 256 * round; };
-    const long c64 = cost(64, 10), c128 = cost(128, 16), c256 = cost(256, 24);
+    const long c64 = cost(64, 10), c128 = cost(128, 16), c256 = out_f32 ? LONG_MAX : cost(256, 24);
     return c64 <= c128 && c64 <= c256 ? 64 : c128 <= c256 ? 128 : 256;
 }
 
@@ -31,8 +38,8 @@ hipError_t launch_fp8_matmul(const uint8_t* a, const float* sa, const uint8_t* w
                              int64_t lda, int64_t ldw, int out_f32, void* y, int64_t ldy, hipStream_t s) {
     Fp8Dense p{a, sa, w, sw, M, N, K, lda, ldw, ldy, y, out_f32, 0};
     p.vec = (uintptr_t)y % 16 == 0 && ldy % (out_f32 ? 4 : 8) == 0;
-    if (dense_streams(M, N)) return launch_fp8_skinny(p, s);
-    return launch_fp8_gemm(p, dense_bt(M, N), s);
+    if (dense_streams(M, N, out_f32)) return launch_fp8_skinny(p, s);
+    return launch_fp8_gemm(p, dense_bt(M, N, out_f32), s);
 }
 
 // Workspace of a grouped call, in order: tile table, quantised rows and

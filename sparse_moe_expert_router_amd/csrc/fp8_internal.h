@@ -37,7 +37,7 @@ struct Fp8Ffn {
 hipError_t launch_fp8_skinny(const Fp8Dense& p, hipStream_t s);
 long fp8_skinny_workgroups(int M, int N);
 
-// Tiles of bt rows (256, 128 or 64) x 256 outputs.
+// Tiles of bt rows (256, 128 or 64; fp32 outputs 128 or 64) x 256 outputs.
 hipError_t launch_fp8_gemm(const Fp8Dense& d, int bt, hipStream_t s);
 hipError_t launch_fp8_gemm_gateup(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s);
 hipError_t launch_fp8_gemm_down(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s);

@@ -107,7 +107,7 @@ def _check_product(y, a, sa, w, sw):
 
 SHAPES = [(1, 16, 16), (1, 1, 128), (1, 2560, 2560), (5, 33, 144), (16, 128, 640), (17, 130, 1296), (31, 257, 128), (33, 1000, 272),
           (77, 1000, 1296), (128, 256, 256), (129, 300, 384), (200, 640, 2560), (256, 256, 128), (257, 513, 1040), (300, 1280, 512),
-          (513, 129, 2064), (1000, 384, 640), (2048, 264, 1152), (4100, 4099, 144), (4097, 4200, 128), (2300, 8200, 1280)]
+          (513, 129, 2064), (1000, 384, 640), (2048, 264, 1152), (4100, 4099, 144), (4097, 4200, 128), (2300, 8200, 1280), (12, 9000, 400), (40, 18000, 272), (1500, 700, 656)]
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
@@ -139,7 +139,7 @@ def test_matmul_strided_and_untouched_surroundings(M, N, K):
     assert (big[0] == 7).all() and (big[-1] == 7).all() and (big[:, :3] == 7).all() and (big[:, 3 + N:] == 7).all()
 
 
-@pytest.mark.parametrize("M", [2, 40, 600])
+@pytest.mark.parametrize("M", [2, 40, 600, 1500, 9000])
 def test_matmul_nan_stays_in_its_row_and_column(M):
     N, K = 400, 384
     g = _gen(5)
