@@ -104,3 +104,11 @@ def test_experts_refuse_sizes_past_32_bits():
         return moe.lib().moe_grouped_ffn_a8(FAKE, T, 1, ctypes.byref(b), FAKE, FAKE, 0, FAKE, FAKE, 1 << 60, None)
     assert ffn(8, (1 << 20) + 128, 128) == UNSUP and ffn(8, 128, (1 << 20) + 128) == UNSUP
     assert ffn(1 << 22, 1024, 128) == UNSUP
+
+
+def test_rows_that_share_memory_are_refused():
+    """Broadcast rows (stride 0) would be written, or read, as one."""
+    q = lambda stride: moe.lib().moe_fp8_quantize(FAKE, 0, 4, 128, stride, FAKE, FAKE, None)
+    assert q(0) == SHAPE and q(120) == SHAPE
+    mm = lambda lda, ldw, ldy: moe.lib().moe_fp8_matmul(FAKE, FAKE, FAKE, FAKE, 4, 8, 128, lda, ldw, 0, FAKE, ldy, None)
+    assert mm(0, 128, 8) == SHAPE and mm(128, 0, 8) == SHAPE and mm(128, 128, 0) == SHAPE

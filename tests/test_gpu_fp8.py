@@ -434,3 +434,55 @@ def test_quantiser_and_products_make_the_expert(T):
     h, sh = moe.fp8_quantize(torch.nn.functional.silu(gate) * up)
     rows = moe.fp8_matmul(h, sh, g["down_codes"][0], g["down_bscales"][0])
     _check_experts(rows, x, 1, bank, torch.tensor([0, T]), torch.arange(T).int())
+
+
+def test_experts_without_a_workspace_on_two_streams_and_captured():
+    T, H, F, E, k = 300, 1024, 512, 8, 2
+    bank = _gpu(_bank(E, H, F, 2))
+    x = torch.randn((T, H), generator=_gen(14)).bfloat16().to(DEV)
+    off, sp = _sorted(torch.rand((T, E), generator=_gen(15)).topk(k, 1).indices, E)
+    off, sp = off.to(DEV), sp.to(DEV)
+    want = moe.grouped_ffn_a8(x, k, bank, off, sp)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    out = []
+    for _ in range(5):
+        for s in streams:
+            with torch.cuda.stream(s):
+                out.append(moe.grouped_ffn_a8(x, k, bank, off, sp))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in out)
+    graphs, rows = [], [torch.empty_like(want) for _ in range(2)]
+    for r in rows:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            moe.grouped_ffn_a8(x, k, bank, off, sp, rows=r)
+        graphs.append(g)
+    for i in range(3):
+        x.copy_(torch.randn((T, H), generator=_gen(20 + i)).bfloat16())
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        want = moe.grouped_ffn_a8(x, k, bank, off, sp)
+        assert torch.equal(rows[0], want) and torch.equal(rows[1], want)
+
+
+def test_quantiser_and_product_captured():
+    M, N, K = 40, 260, 400
+    g = _gen(16)
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device=DEV)
+    w, sw = _codes((N, K), g).to(DEV), torch.rand((3, 4), generator=g).to(DEV)
+    codes, s = moe.fp8_quantize(x)
+    y = moe.fp8_matmul(codes, s, w, sw)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.fp8_quantize(x, codes=codes, scales=s)
+        moe.fp8_matmul(codes, s, w, sw, y=y)
+    for i in range(4):
+        x.copy_(torch.randn((M, K), generator=_gen(30 + i)).bfloat16())
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        assert torch.equal(got, moe.fp8_matmul(*moe.fp8_quantize(x), w, sw))
