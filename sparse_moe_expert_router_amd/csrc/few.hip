@@ -352,8 +352,9 @@ __device__ __forceinline__ void store_h(__amdgpu_buffer_rsrc_t r, uint32_t row, 
 
 // Units v0 .. v1 of the F inputs of a list of experts, one after another, into
 // 16 outputs from o0.  expert(slot), hoff(slot): the slot's expert and the byte
-// offset of the lane's token's h (kOob: not routed to it).  `ready` is called
-// once the first U units are under way.  The next U units' weights are loaded
+// offset of the lane's token's h (kOob: not routed to it; the token's sum is
+// then left alone, as zeros times the expert's weights are no zeros where those
+// hold an infinity or a NaN).  `ready` is called once the first U units are under way.  The next U units' weights are loaded
 // before the present ones are used (16 tokens, FP8: 205 -> 189 us, bf16 320 -> 285).
 template <int FMT, int U, class Expert, class Hoff, class Ready>
 __device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int H, int F, int o0, __amdgpu_buffer_rsrc_t rh,
@@ -377,11 +378,13 @@ __device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int 
     ready();
     for (int vb = v0; vb < v1; vb += U) {
         u32x4_t h[U][FR];
+        bool routed[U];
 #pragma unroll
         for (int i = 0; i < U; ++i)
             if (vb + i < v1) {
                 const int v = vb + i, slot = v / n;
                 const uint32_t at = hoff(slot);
+                routed[i] = at != kOob;
 #pragma unroll
                 for (int j = 0; j < FR; ++j) {
                     const uint32_t in = (uint32_t)((v - slot * n) * Un::IN + Un::input(g, j));
@@ -396,7 +399,10 @@ __device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int 
                 bf16x8_t b[FR];
 #pragma unroll
                 for (int j = 0; j < FR; ++j) b[j] = input_frag<FMT>(h[i][j]);
-                unit_product<FMT>(acc, d[i], b, 8 * (g & 1));
+                f32x4_t sum = acc;
+                unit_product<FMT>(sum, d[i], b, 8 * (g & 1));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[q] = routed[i] ? sum[q] : acc[q];
             }
 #pragma unroll
         for (int i = 0; i < U; ++i) d[i] = next[i];

@@ -187,3 +187,28 @@ def test_agrees_with_the_layer_of_separate_kernels(fmt):
     assert torch.equal(idx, idx0)
     a, b = y.double(), y0.double()
     assert (a - b).norm() <= 3 * 2.0 ** -8 * a.norm()
+
+
+@pytest.mark.parametrize("name", ["gate", "up", "down"])
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+@pytest.mark.parametrize("T,fmt", [(4, "bf16"), (4, "fp8"), (4, "awq_om"), (16, "bf16"), (16, "fp8"), (16, "awq_om")])
+def test_weights_that_are_no_numbers_reach_only_their_tokens(T, fmt, bad, name):
+    """A NaN or an infinity in one expert's weights or scales shows in the tokens routed to it; the others keep their
+    bits (the expert's share of them is no part of their sums, not zero times its weights)."""
+    x, router, bank, shared = _make(T, 512, 32, 2, 256, 64, fmt, seed=T)
+    clean, idx = moe.layer_few(x, router, 2, bank, shared)
+    e = int(idx[0, 0])
+    hit = (idx == e).any(1)
+    assert hit.any() and not hit.all()
+    if fmt == "bf16":
+        bank[name][e, 3, 5] = float(bad)
+    elif fmt == "fp8" and bad == "nan":
+        bank[name + "_codes"][e, 3, 5] = 0x7F
+    elif fmt == "fp8":
+        bank[name + "_bscales"][e, 0, 0] = float(bad)
+    else:
+        bank[name + "_scales"][e, 0, 3] = float(bad)
+    y, idx2 = moe.layer_few(x, router, 2, bank, shared)
+    assert torch.equal(idx, idx2)
+    assert (~torch.isfinite(y[hit])).any(1).all()
+    assert torch.equal(y[~hit], clean[~hit])
