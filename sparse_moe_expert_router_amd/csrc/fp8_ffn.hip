@@ -56,13 +56,14 @@ static size_t a8_max_tiles(long P, int E, int bt) { return (size_t)(P / bt + (P 
 // average over 64 experts: 8 79 / 91 / 128, 48 92 / 101 / 136, 80 112 / 109 / 142, 128
 // 140 / 119 / 150, 320 234 / 202 / 226; over 256: 64 330 / 295 / 380, 128 446 / 397 /
 // 412, 192 583 / 491 / 442, 640 1507 / 1251 / 1199, 1280 2863 / 2332 / 2160.  Hidden
-// 4096, inter 1152, 128 rows on average over 8 experts: 56 / 61 / 83.  (Down to one
-// row per expert a tile of 16 rows gains nothing: the weights' bytes bound the call.)
-static int a8_bt(long P, int E, int F) {
+// 4096, inter 1152, 128 rows on average over 8 experts: 56 / 61 / 83.  fp32 rows
+// (exact products) have the first two, us: over 512 experts 5 rows on average 496 /
+// 688, 80 932 / 790; over 256 128 605 / 582, 1280 4497 / 3757.
+static int a8_bt(long P, int E, int F, int out_f32) {
     const long active = P < E ? P : E, avg = P / active, cols = F / 128;
     auto tiles = [&](long rows) { return (P / rows + active / 2) * cols; };
     if (avg < 64 || tiles(64) <= 256) return 64;
-    return avg >= 160 && tiles(256) >= 1024 ? 256 : 128;
+    return !out_f32 && avg >= 160 && tiles(256) >= 1024 ? 256 : 128;
 }
 
 static size_t a8_tiles_bytes(long P, int E, int bt) { return up256((1 + 3 * a8_max_tiles(P, E, bt)) * sizeof(int32_t)); }
@@ -137,7 +138,7 @@ hipError_t launch_ffn_a8(const FfnArgs& f, void* ws, hipStream_t s) {
     p.sgate = f.ex->gate.block_scales; p.sup = f.ex->up.block_scales; p.sdown = f.ex->down.block_scales;
     p.rows = f.rows;
     p.out_f32 = f.out_f32;
-    const int bt = a8_bt(p.P, p.E, p.F);
+    const int bt = a8_bt(p.P, p.E, p.F, p.out_f32);
     const long mt = (long)a8_max_tiles(p.P, p.E, bt);
     char* w = static_cast<char*>(ws);
     int32_t* tiles = reinterpret_cast<int32_t*>(w);

@@ -440,7 +440,7 @@ typedef const __attribute__((address_space(4))) int32_t const_int;
 // A value that no kernel writes meanwhile, at a uniform address: a scalar load.
 __device__ __forceinline__ int const_load(const int32_t* p) { return *(const_int*)p; }
 
-template <int TF, int MODE>
+template <int TF, int MODE, bool kExact>
 __global__ __launch_bounds__(kGThreads, 2) void fp8_run_kernel(const Fp8Ffn p) {
     using L = RunLds<TF>;
     constexpr int BT = L::BT, S = L::S, NA = BT / 64, NL = NA + 4;
@@ -667,7 +667,7 @@ __global__ __launch_bounds__(kGThreads, 2) void fp8_run_kernel(const Fp8Ffn p) {
 #pragma unroll
                 for (int f = 0; f < 4; ++f) {
                     const int x = 4 * t + f;
-                    v[x % 3] = mfma_fp8<false>(w[f], ac);
+                    v[x % 3] = mfma_fp8<kExact>(w[f], ac);
                     if (t + 1 == TF) w[f] = read_w(ns, f);
                     if (f == 0) {
                         if (t + 1 < TF) {
@@ -783,36 +783,38 @@ hipError_t launch_fp8_gemm(const Fp8Dense& d, int bt, hipStream_t s) {
     return launch_one<2, G_DENSE, false>(d, p, tiles(64), s);
 }
 
-template <int TF, int MODE>
+template <int TF, int MODE, bool kExact>
 static hipError_t launch_run(const Fp8Ffn& p, long tiles, hipStream_t s) {
     const long grid = tiles < 256 ? (tiles + kXcd - 1) / kXcd * kXcd : 256;
-    const void* fn = reinterpret_cast<const void*>(fp8_run_kernel<TF, MODE>);
+    const void* fn = reinterpret_cast<const void*>(fp8_run_kernel<TF, MODE, kExact>);
     const hipError_t err = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, RunLds<TF>::TOTAL);
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL((fp8_run_kernel<TF, MODE>), dim3((unsigned)grid), dim3(kGThreads), RunLds<TF>::TOTAL, s, p);
+    hipLaunchKernelGGL((fp8_run_kernel<TF, MODE, kExact>), dim3((unsigned)grid), dim3(kGThreads), RunLds<TF>::TOTAL, s, p);
     return hipGetLastError();
 }
 
-template <int TF, int MODE>
+template <int TF, int MODE, bool kExact>
 static hipError_t launch_grouped(const Fp8Ffn& p, long tiles, hipStream_t s) {
     const int KB = (MODE == G_GATEUP ? p.H : p.F) / 128;
-    if (KB >= (MODE == G_GATEUP ? kRunMinKB : kRunMinKBDown)) return launch_run<TF, MODE>(p, tiles, s);
+    if (KB >= (MODE == G_GATEUP ? kRunMinKB : kRunMinKBDown)) return launch_run<TF, MODE, kExact>(p, tiles, s);
     const Fp8Dense d{};
-    return launch_one<TF, MODE, false>(d, p, tiles, s);
+    return launch_one<TF, MODE, kExact>(d, p, tiles, s);
+}
+
+template <int MODE>
+static hipError_t launch_pass(const Fp8Ffn& p, int bt, long tiles, hipStream_t s) {
+    if (p.out_f32) return bt == 64 ? launch_grouped<2, MODE, true>(p, tiles, s) : launch_grouped<4, MODE, true>(p, tiles, s);
+    if (bt == 256) return launch_grouped<8, MODE, false>(p, tiles, s);
+    if (bt == 128) return launch_grouped<4, MODE, false>(p, tiles, s);
+    return launch_grouped<2, MODE, false>(p, tiles, s);
 }
 
 hipError_t launch_fp8_gemm_gateup(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s) {
-    const long tiles = max_tiles * (p.F / 128);
-    if (bt == 256) return launch_grouped<8, G_GATEUP>(p, tiles, s);
-    if (bt == 128) return launch_grouped<4, G_GATEUP>(p, tiles, s);
-    return launch_grouped<2, G_GATEUP>(p, tiles, s);
+    return launch_pass<G_GATEUP>(p, bt, max_tiles * (p.F / 128), s);
 }
 
 hipError_t launch_fp8_gemm_down(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s) {
-    const long tiles = max_tiles * ((p.H + kGN - 1) / kGN);
-    if (bt == 256) return launch_grouped<8, G_DOWN>(p, tiles, s);
-    if (bt == 128) return launch_grouped<4, G_DOWN>(p, tiles, s);
-    return launch_grouped<2, G_DOWN>(p, tiles, s);
+    return launch_pass<G_DOWN>(p, bt, max_tiles * ((p.H + kGN - 1) / kGN), s);
 }
 
 }  // namespace moe

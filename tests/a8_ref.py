@@ -98,11 +98,18 @@ def swiglu(g, dg, u, du):
     return h, 1.1 * dg * u.abs() + s.abs() * du + 1.1 * dg * du + (8 + g.abs()) * 2.0 ** -23 * h.abs()
 
 
-def expert_a8(xq, gate, up, down):
-    """Rows of one W8A8 expert on dequantised rows xq (float64): (rows, bound before the final rounding)."""
-    H, F = gate.shape[1], gate.shape[0]
-    g, dg = product(xq, gate, H, False)
-    u, du = product(xq, up, H, False)
+def expert_a8(xq, gate, up, down, exact=False):
+    """Rows of one W8A8 expert on dequantised rows xq (float64): (rows, bound before the final rounding); exact:
+    products with the fp32 sums' bound."""
+    H = gate.shape[1]
+    g, dg = product(xq, gate, H, exact)
+    u, du = product(xq, up, H, exact)
+    return rows_a8(g, dg, u, du, down, exact)
+
+
+def rows_a8(g, dg, u, du, down, exact=False):
+    """The rows from the sums of gate and up and the bounds dg, du of their errors."""
+    F = g.shape[1]
     h, dh = swiglu(g, dg, u, du)
     codes, s = quantize(h)
     sx = spread(s, F)
@@ -117,5 +124,5 @@ def expert_a8(xq, gate, up, down):
     near = (q.abs()[..., None] - MID.to(q.device)).abs().amin(-1) <= dq
     step = torch.exp2(torch.floor(torch.log2(q.abs().clamp(min=2.0 ** -6))) - 3) * 1.0
     dhq = (near * 2 * step + v.abs() * ds) * sx * (1 + ds)
-    y, dy = product(v * sx, down, F, False)
+    y, dy = product(v * sx, down, F, exact)
     return y, dy * 1.2 + dhq @ down.abs().t()

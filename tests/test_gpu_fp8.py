@@ -486,3 +486,90 @@ def test_quantiser_and_product_captured():
         torch.cuda.synchronize()
         got = y.clone()
         assert torch.equal(got, moe.fp8_matmul(*moe.fp8_quantize(x), w, sw))
+
+
+# ------------------------------------------------------------------ large products that cancel
+
+def _code(v):
+    """Codes of a tensor of values that E4M3 holds."""
+    return R.encode(v.double())
+
+
+def _cancelling(rows, n, g):
+    """[rows, n] with 448 and -448 in the first two places of every 8, small whole numbers in the others."""
+    w = torch.randint(-2, 3, (rows, n), generator=g).float()
+    w[:, ::8], w[:, 1::8] = 448.0, -448.0
+    return w
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 256), (7, 300, 400), (40, 512, 1024), (300, 260, 640), (1500, 700, 656), (2300, 1000, 384)])
+def test_matmul_large_products_that_cancel(M, N, K):
+    """448 * 448 and -448 * 448 beside products of at most 4.  Every partial sum of a block of 128 is a whole number
+    below 2^24 (16 * 448 * 448 and some), exact in fp32 in any order, and the scales are powers of two: fp32 outputs
+    are exact.  bf16 outputs have the FP8 matrix cores' bound, which the largest products set."""
+    g = _gen(M + K)
+    a, w = torch.randint(-2, 3, (M, K), generator=g).float(), _cancelling(N, K, g)
+    a[:, ::8], a[:, 1::8] = 448.0, 448.0
+    kb = -(-K // 128)
+    sa = torch.exp2(torch.randint(-3, 4, (M, kb), generator=g).float())
+    sw = torch.exp2(torch.randint(-3, 4, (-(-N // 128), kb), generator=g).float())
+    args = [t.to(DEV) for t in (_code(a), sa, _code(w), sw)]
+    av, wv = R.decode(args[0]) * R.spread(args[1].double(), K), R.weights(args[2], args[3])
+    ref, bound = R.product(av, wv, K, False)
+    y = moe.fp8_matmul(*args, out_dtype=moe.OUT_F32)
+    assert ref.abs().max() > 10 and torch.equal(y.double(), ref)
+    y = moe.fp8_matmul(*args).double()
+    assert ((y - ref).abs() <= bound + 2.0 ** -8 * (ref.abs() + bound)).all()
+
+
+CANCEL = [(5, 256, 128), (40, 1024, 512), (300, 256, 256), (700, 1024, 512), (5000, 1024, 512), (4200, 896, 512)]
+
+
+@pytest.mark.parametrize("T,H,F", CANCEL)
+def test_experts_fp32_rows_when_gate_and_up_cancel(T, H, F):
+    """As in the test of the product: the sums of gate and up are exact in fp32, so the rows have the bound of exact
+    sums (their terms of down do not cancel)."""
+    g = _gen(T)
+    x = torch.randint(-2, 3, (T, H), generator=g).float()
+    x[:, ::8], x[:, 1::8] = 448.0, 448.0
+    bank = {"fmt": "fp8"}
+    for n in ("gate", "up"):
+        bank[n + "_codes"] = _code(_cancelling(F, H, g))[None]
+        bank[n + "_bscales"] = torch.full((1, F // 128, H // 128), 2.0 ** -6)
+    bank["down_codes"] = _codes((1, H, F), g)
+    bank["down_bscales"] = torch.full((1, H // 128, F // 128), 2.0 ** -8)
+    rows = moe.grouped_ffn_a8(x.bfloat16().to(DEV), 1, _gpu(bank), out_dtype=moe.OUT_F32).double()
+    gate, up, down = (R.weights(bank[n + "_codes"][0].to(DEV), bank[n + "_bscales"][0].to(DEV)) for n in ("gate", "up", "down"))
+    xq = x.double().to(DEV)                       # 448 is the largest of every group: its scale is 1, every value a code
+    zero = torch.zeros((T, F), dtype=torch.float64, device=DEV)
+    ref, bound = R.rows_a8(xq @ gate.t(), zero, xq @ up.t(), zero, down, exact=True)
+    err = (rows - ref).abs()
+    assert ref.abs().mean() > 1e-3 and (err <= bound + 2.0 ** -24 * (ref.abs() + bound)).all()
+    # h is off by about 12 units of 2^-23, so a share of 2 * 12 * 2^-23 / 2^-4 = 2^-14.4 of its codes is a step off:
+    # 2^-7.2 * 2^-3.5 of the rows.  One such code alone, of the smallest case's five rows of 128: 2^-4 of a term,
+    # 2^-4 / sqrt(5 * 128) = 2^-8.7 of the rows.
+    assert err.norm() <= 2.0 ** -7 * ref.norm()
+
+
+@pytest.mark.parametrize("T,H,F", CANCEL)
+def test_experts_fp32_rows_when_down_cancels(T, H, F):
+    """h is 448 m in two places of every 8 and m or 2 m in the others, up to a sign: codes 448, 1 and 2.  The sum of down
+    is a whole number below 2^24 in fp32; what is left are h's scale (swiglu's 8 + |g| units of 2^-23 and a division),
+    its product with the weights' scale, and the rounding of each block's share: 8 + |g| + 3 + blocks units."""
+    g = _gen(T)
+    x = torch.zeros((T, H))
+    x[:, 0] = torch.randint(1, 4, (T,), generator=g).float()
+    gate, up = torch.zeros((F, H)), torch.zeros((F, H))
+    gate[:, 0] = 1.0
+    up[:, 0] = torch.randint(-2, 3, (F,), generator=g).float()
+    up[::8, 0], up[1::8, 0] = 448.0, 448.0
+    bank = {"fmt": "fp8", "gate_codes": _code(gate)[None], "up_codes": _code(up)[None], "down_codes": _code(_cancelling(H, F, g))[None],
+            "gate_bscales": torch.ones((1, F // 128, H // 128)), "up_bscales": torch.ones((1, F // 128, H // 128)),
+            "down_bscales": torch.ones((1, H // 128, F // 128))}
+    rows = moe.grouped_ffn_a8(x.bfloat16().to(DEV), 1, _gpu(bank), out_dtype=moe.OUT_F32).double().cpu()
+    v = x[:, :1].double()
+    h = torch.sigmoid(v) * v * v * up[:, 0].double()
+    ref = h @ R.decode(bank["down_codes"][0]).t()
+    size = h.abs() @ R.decode(bank["down_codes"][0]).abs().t()
+    size -= 2 * 448 * 448 * (F // 8) * (torch.sigmoid(v) * v * v)      # what does not cancel
+    assert ref.abs().mean() > 1 and ((rows - ref).abs() <= (8 + 3 + 3 + F // 128) * 2.0 ** -23 * size).all()
