@@ -526,7 +526,8 @@ class LayerCall:
                  side_stream=None, ws=None, topk_idx=None):
         T, H = x.shape
         self.x, self.w_router, self.k = x, w_router, k
-        self.bank, self.shared, self.shared_scale = bank, shared, shared_scale
+        # copies of the dicts: the tensors that st and sh point to live as long as they
+        self.bank, self.shared, self.shared_scale = dict(bank), shared and dict(shared), shared_scale
         self.st = experts_struct(bank)
         self.sh = experts_struct(shared) if shared is not None else None
         need = int(lib().moe_layer_workspace_bytes(T, k, ctypes.byref(self.st),
@@ -586,7 +587,8 @@ class FewTokenLayer:
         _require(w_router.shape == (E, H) and w_router.dtype == torch.bfloat16 and w_router.is_contiguous(), name,
                  "w_router must be contiguous bf16 [E, H]")
         _same_device(name, w_router.device, bank, shared)
-        self.w_router, self.k, self.bank, self.shared, self.H = w_router, k, bank, shared, H
+        # copies of the dicts: the tensors that st and sh point to live as long as they
+        self.w_router, self.k, self.bank, self.shared, self.H = w_router, k, dict(bank), shared and dict(shared), H
         self.max_tokens = max_tokens
         self.st = experts_struct(bank)
         self.sh = experts_struct(shared) if shared is not None else None
