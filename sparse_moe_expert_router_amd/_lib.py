@@ -129,6 +129,18 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+def _current_stream(device):
+    return torch.cuda.current_stream(device) if device.type == "cuda" else None
+
+
+def _capturing(device):
+    """Whether the device's current stream records a graph."""
+    if device.type != "cuda":
+        return False
+    with torch.cuda.device(device):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class _Device:
     """Runs the library's calls on a tensor's device: its index and its current
     stream, with that device current while the call is made."""
@@ -575,7 +587,10 @@ class FewTokenLayer:
     returns (y [T, H] bf16, topk_idx [T, k] int32).
 
     bank: "bf16", "fp8" or "awq_om"; shared: a "bf16" bank of one expert, or
-    None.  One object serves one stream at a time (its workspace is one).
+    None.  The object has one workspace, so its calls run one after another: one
+    on another stream than the call before waits for that stream.  Calls recorded
+    into a graph are the caller's to order (their replays with each other and
+    with other calls), and the object has to live as long as the graph.
 
     For one or two tokens, where it takes 0.6 to 0.8 of LayerCall's time; from
     four on LayerCall is as fast or faster."""
@@ -600,7 +615,8 @@ class FewTokenLayer:
         self.ws_buf, self._ws = buf, buf.data_ptr()
         self._router = w_router.data_ptr()
         self.device = w_router.device
-        self._stream = _Device(w_router).stream if self.device.type == "cuda" else None  # the workspace's
+        self._on = _current_stream(self.device)  # where the workspace was made, then where it was last used
+        self._on_ptr = self._on.cuda_stream if self._on else None
 
     def __call__(self, x, shared_scale=None, y=None, topk_idx=None):
         name = "moe_layer_few"
@@ -625,8 +641,12 @@ class FewTokenLayer:
             scale = shared_scale.data_ptr()
         _same_device(name, self.device, y, topk_idx, shared_scale)
         d = _Device(x)
-        if d.stream != self._stream:  # the workspace is not given to another before this call has ended
-            self.ws_buf.record_stream(torch.cuda.current_stream(self.device))
+        if d.stream != self._on_ptr:
+            on = _current_stream(self.device)
+            if not _capturing(self.device):  # (a capture may not wait for work outside it)
+                on.wait_stream(self._on)  # work there may still use the workspace's memory
+                self._on, self._on_ptr = on, d.stream
+            self.ws_buf.record_stream(on)  # nor is it given to another before this call has ended
         d.call(name, x.data_ptr(), T, self._router, self.k, self._st, self._sh, scale, y.data_ptr(),
                topk_idx.data_ptr(), self._ws, self.ws_n, d.stream)
         return y, topk_idx

@@ -33,3 +33,50 @@ def test_a_prepared_call_keeps_the_weights_it_points_to(make):
             d[name] = torch.zeros_like(d[name])
             gc.collect()
             assert old() is not None and old().data_ptr() == at == getattr(st, name).w
+
+
+class _Stream:
+    """Stands for a stream: writes down what it is made to wait for."""
+
+    def __init__(self, ptr):
+        self.cuda_stream, self.waits = ptr, []
+
+    def wait_stream(self, other):
+        self.waits.append(other)
+
+
+def test_a_few_token_layer_on_another_stream_waits_for_the_one_before(monkeypatch):
+    """The workspace was made on, or last used on, another stream, whose work may still use its memory."""
+    a, b, capture = _Stream(1), _Stream(2), _Stream(3)
+    now = [a]
+    calls = []
+
+    class Device:
+        def __init__(self, t):
+            self.stream = now[0].cuda_stream
+
+        def call(self, name, *args):
+            calls.append((now[0], [len(s.waits) for s in (a, b, capture)], args[-1]))
+
+    monkeypatch.setattr(moe._lib, "_Device", Device)
+    monkeypatch.setattr(moe._lib, "_current_stream", lambda device: now[0])
+    monkeypatch.setattr(moe._lib, "_capturing", lambda device: now[0] is capture)
+    few = _few(_bank(), None)
+    few.ws_buf = type("Buffer", (), {"record_stream": lambda self, s: None})()
+    x = torch.zeros((2, 256), dtype=torch.bfloat16)
+    few(x)
+    assert a.waits == []
+    now[0] = b
+    few(x), few(x)
+    assert b.waits == [a]
+    now[0] = a
+    few(x)
+    assert a.waits == [b] and b.waits == [a]
+    now[0] = capture            # a stream under capture must not wait for one that is not
+    few(x)
+    assert capture.waits == []
+    now[0] = a                  # and nothing outside waits for a capture
+    few(x)
+    assert a.waits == [b]
+    assert [s.cuda_stream for s, _, _ in calls] == [p for _, _, p in calls] == [1, 2, 2, 1, 3, 1]
+    assert calls[1][1] == [0, 1, 0]     # the wait comes before the call

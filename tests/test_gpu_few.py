@@ -212,3 +212,42 @@ def test_weights_that_are_no_numbers_reach_only_their_tokens(T, fmt, bad, name):
     assert torch.equal(idx, idx2)
     assert (~torch.isfinite(y[hit])).any(1).all()
     assert torch.equal(y[~hit], clean[~hit])
+
+
+def test_the_workspace_of_a_layer_made_behind_pending_work():
+    """The workspace takes memory that work on the current stream still reads; the first call, on another stream,
+    leaves that work its values."""
+    x, router, bank, shared = _make(16, 512, 32, 4, 128, 64, "fp8")
+    want, _ = moe.layer_few(x, router, 4, bank, shared)
+    n = moe.FewTokenLayer(router, 4, bank, shared).ws_buf.numel()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    m = torch.randn((4096, 4096), device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(a):
+            old = torch.full((n,), 5, dtype=torch.uint8, device=DEV)
+            for _ in range(20):
+                m = (m @ m).clamp(-1, 1)           # some ms of work
+            kept = old.clone()
+            del old
+            few = moe.FewTokenLayer(router, 4, bank, shared)
+        with torch.cuda.stream(b):
+            y, _ = few(x)
+        torch.cuda.synchronize()
+        assert (kept == 5).all() and torch.equal(y, want)
+
+
+def test_one_layer_on_two_streams_in_turn():
+    x, router, bank, shared = _make(16, 1024, 64, 6, 256, 64, "fp8")
+    xs = [x, x.flip(0).contiguous()]
+    few = moe.FewTokenLayer(router, 6, bank, shared)
+    want = [moe.layer_few(v, router, 6, bank, shared) for v in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    out = []
+    for i in range(20):
+        with torch.cuda.stream(streams[i % 2]):
+            out.append(few(xs[i % 2]))
+    torch.cuda.synchronize()
+    for i, (y, idx) in enumerate(out):
+        assert torch.equal(y, want[i % 2][0]) and torch.equal(idx, want[i % 2][1])
