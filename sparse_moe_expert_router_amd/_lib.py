@@ -133,12 +133,12 @@ def _current_stream(device):
     return torch.cuda.current_stream(device) if device.type == "cuda" else None
 
 
+_stream_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None)  # without the Python wrapper's cost
+
+
 def _capturing(device):
-    """Whether the device's current stream records a graph."""
-    if device.type != "cuda":
-        return False
-    with torch.cuda.device(device):
-        return torch.cuda.is_current_stream_capturing()
+    """Whether the current stream records a graph (a capture runs on the current device)."""
+    return device.type == "cuda" and _stream_capturing()
 
 
 class _Device:
@@ -177,17 +177,23 @@ def workspace_bytes(op, T, k, E, H, F=0) -> int:
 
 
 class Workspace:
-    """A grow-only device scratch buffer for the calls that need one."""
+    """A grow-only device scratch buffer for the calls that need one.  A buffer
+    that a call was captured with is kept when the workspace grows past it, as
+    the graph goes on using it; the workspace has to live as long as the graph."""
 
     def __init__(self, device=None):
         self.device = device
         self.buf = None
+        self._gpu = torch.device(device or "cuda").type == "cuda"
+        self._in_graphs = {}
 
     def get(self, nbytes: int):
         if nbytes == 0:
             return None, 0
         if self.buf is None or self.buf.numel() < nbytes:
             self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device or "cuda")
+        if self._gpu and _stream_capturing():
+            self._in_graphs[self.buf.data_ptr()] = self.buf
         return self.buf, self.buf.numel()
 
 

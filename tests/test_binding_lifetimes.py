@@ -80,3 +80,21 @@ def test_a_few_token_layer_on_another_stream_waits_for_the_one_before(monkeypatc
     assert a.waits == [b]
     assert [s.cuda_stream for s, _, _ in calls] == [p for _, _, p in calls] == [1, 2, 2, 1, 3, 1]
     assert calls[1][1] == [0, 1, 0]     # the wait comes before the call
+
+
+def test_a_workspace_that_grows_keeps_the_buffer_of_a_captured_call(monkeypatch):
+    """A graph goes on using the buffer that its calls were recorded with."""
+    capturing = [False]
+    monkeypatch.setattr(moe._lib, "_stream_capturing", lambda: capturing[0])
+    ws = moe.Workspace(torch.device("cpu"))
+    ws._gpu = True                          # asks whether the stream records a graph
+    eager = weakref.ref(ws.get(100)[0])
+    ws.get(200)
+    gc.collect()
+    assert eager() is None                  # nothing but the workspace used it
+    capturing[0] = True
+    in_graph = [weakref.ref(ws.get(n)[0]) for n in (150, 300)]
+    capturing[0] = False
+    buf, n = ws.get(1000)
+    gc.collect()
+    assert n == 1000 and all(r() is not None and r() is not buf for r in in_graph)

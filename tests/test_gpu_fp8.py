@@ -573,3 +573,26 @@ def test_experts_fp32_rows_when_down_cancels(T, H, F):
     size = h.abs() @ R.decode(bank["down_codes"][0]).abs().t()
     size -= 2 * 448 * 448 * (F // 8) * (torch.sigmoid(v) * v * v)      # what does not cancel
     assert ref.abs().mean() > 1 and ((rows - ref).abs() <= (8 + 3 + 3 + F // 128) * 2.0 ** -23 * size).all()
+
+
+def test_a_captured_call_after_its_workspace_has_grown():
+    H, F, E, k = 1024, 512, 8, 2
+    bank = _gpu(_bank(E, H, F, 2))
+    mk = lambda T, seed: (torch.randn((T, H), generator=_gen(seed)).bfloat16().to(DEV),
+                          *(t.to(DEV) for t in _sorted(torch.rand((T, E), generator=_gen(seed)).topk(k, 1).indices, E)))
+    x, off, sp = mk(40, 1)
+    big = mk(4000, 2)
+    ws = moe.Workspace(x.device)
+    rows = torch.empty((40 * k, H), dtype=torch.bfloat16, device=DEV)
+    moe.grouped_ffn_a8(x, k, bank, off, sp, ws=ws, rows=rows)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.grouped_ffn_a8(x, k, bank, off, sp, ws=ws, rows=rows)
+    moe.grouped_ffn_a8(big[0], k, bank, *big[1:], ws=ws)          # grows
+    others = [torch.full((1 << 20,), 7, dtype=torch.uint8, device=DEV) for _ in range(64)]
+    for i in range(3):
+        x.copy_(torch.randn(x.shape, generator=_gen(10 + i)).bfloat16())
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(rows, moe.grouped_ffn_a8(x, k, bank, off, sp)) and all((o == 7).all() for o in others)
