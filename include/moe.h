@@ -438,7 +438,9 @@ moe_status moe_fp8_quantize(const void *x, int32_t x_dtype, int32_t T, int32_t n
  * (one row per output, as in the FP8 banks) have row strides lda, ldw >= K in
  * bytes; a_scales [M][ceil(K/128)] and w_scales [ceil(N/128)][ceil(K/128)] are
  * contiguous fp32; y has row stride ldy >= N in elements; it may not overlap
- * the inputs, and nothing past column N of a row is written.  Any M and N;
+ * the inputs, and nothing past column N of a row is written.  Any M and N
+ * of which 2^23 - 8 tiles hold the outputs (a tile is 256 outputs of 64 to 256
+ * rows, so any N up to 2^31 - 2048 for few rows);
  * K, lda and ldw multiples of 16 and the strides at most 4 MiB; a and w
  * 16-byte aligned, the rest aligned to its element (MOE_ERR_UNSUPPORTED
  * otherwise).  A row of a that holds a NaN (or whose scale is one) gives NaN

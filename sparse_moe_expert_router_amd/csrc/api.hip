@@ -676,7 +676,7 @@ moe_status moe_fp8_matmul(const uint8_t* a, const float* a_scales, const uint8_t
     if (out_dtype != MOE_OUT_BF16 && out_dtype != MOE_OUT_F32) return MOE_ERR_UNSUPPORTED;
     // rows are read in 16-byte pieces; a tile's rows are addressed with 31 bits
     if (K % 16 || lda % 16 || ldw % 16 || lda > (1 << 22) || ldw > (1 << 22)) return MOE_ERR_UNSUPPORTED;
-    if (((int64_t)M + 15) / 16 * (((int64_t)N + 15) / 16) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (!moe::fp8_matmul_fits(M, N, out_dtype == MOE_OUT_F32)) return MOE_ERR_UNSUPPORTED;
     if (M == 0) return MOE_OK;
     if (!a || !a_scales || !w || !w_scales || !y) return MOE_ERR_NULL;
     const int f32 = out_dtype == MOE_OUT_F32;

@@ -8,6 +8,10 @@
 
 namespace moe {
 
+// Workgroups of 512 threads that a launch holds: fewer than 2^32 threads, and
+// tiles come in whole eighths (one an XCD).
+constexpr long kMaxWorkgroups = (1l << 23) - 8;
+
 // Whether a dense product streams the weights (fp8_skinny.hip): while all of its
 // workgroups, 16 outputs x 32 rows each, are resident at once (two a compute
 // unit); beyond that they read rows and weights too often.  With very few rows
@@ -18,7 +22,8 @@ namespace moe {
 // outputs the tiles take nearly twice as long, streaming the same: 64 x 8192 x
 // 8192 (1024) 61 / 71, 96 rows (1536) 89 / 72; 256 x 2560 x 2560 (1280) 26.7 / 27.0.
 static bool dense_streams(int M, int N, int out_f32) {
-    return M <= 8 || fp8_skinny_workgroups(M, N) <= (out_f32 ? 1024 : 512);
+    const long wgs = fp8_skinny_workgroups(M, N);
+    return (M <= 8 && wgs <= kMaxWorkgroups) || wgs <= (out_f32 ? 1024 : 512);
 }
 
 // Rows of a dense tile.  256 tiles run at once, and such a round takes times as
@@ -28,10 +33,16 @@ static bool dense_streams(int M, int N, int out_f32) {
 // round of any: 17.7, 24.5, 36.4.)  fp32 outputs have the first two: 1024 x 8192 x
 // 8192 in 2 rounds of 64 rows 156 us, one of 128 124; 512 rows 83, 113.
 static int dense_bt(int M, int N, int out_f32) {
-    const long nt = (N + 255) / 256;
+    const long nt = ((long)N + 255) / 256;
     auto cost = [&](long rows, long round) { return ((M + rows - 1) / rows * nt + 255) / 256 * round; };
     const long c64 = cost(64, 10), c128 = cost(128, 16), c256 = out_f32 ? LONG_MAX : cost(256, 24);
     return c64 <= c128 && c64 <= c256 ? 64 : c128 <= c256 ? 128 : 256;
+}
+
+bool fp8_matmul_fits(int M, int N, int out_f32) {
+    if (dense_streams(M, N, out_f32)) return true;
+    const long bt = dense_bt(M, N, out_f32);
+    return ((long)M + bt - 1) / bt * (((long)N + 255) / 256) <= kMaxWorkgroups;
 }
 
 hipError_t launch_fp8_matmul(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, int M, int N, int K,

@@ -775,7 +775,7 @@ static hipError_t launch_one(const Fp8Dense& d, const Fp8Ffn& p, long tiles, hip
 
 hipError_t launch_fp8_gemm(const Fp8Dense& d, int bt, hipStream_t s) {
     const Fp8Ffn p{};
-    auto tiles = [&](int rows) { return (long)((d.M + rows - 1) / rows) * ((d.N + kGN - 1) / kGN); };
+    auto tiles = [&](int rows) { return ((long)d.M + rows - 1) / rows * (((long)d.N + kGN - 1) / kGN); };
     if (d.out_f32)
         return bt == 64 ? launch_one<2, G_DENSE, true>(d, p, tiles(64), s) : launch_one<4, G_DENSE, true>(d, p, tiles(128), s);
     if (bt == 256) return launch_one<8, G_DENSE, false>(d, p, tiles(256), s);

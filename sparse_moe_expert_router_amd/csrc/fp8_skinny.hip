@@ -103,7 +103,7 @@ __global__ __launch_bounds__(kSkThreads) void fp8_skinny_kernel(const Fp8Dense p
     }
 }
 
-long fp8_skinny_workgroups(int M, int N) { return (long)((N + 15) / 16) * (M <= 16 ? 1 : (M + 31) / 32); }
+long fp8_skinny_workgroups(int M, int N) { return ((long)N + 15) / 16 * (M <= 16 ? 1 : ((long)M + 31) / 32); }
 
 hipError_t launch_fp8_skinny(const Fp8Dense& p, hipStream_t s) {
     const dim3 grid((unsigned)fp8_skinny_workgroups(p.M, p.N)), block(kSkThreads);

@@ -112,3 +112,13 @@ def test_rows_that_share_memory_are_refused():
     assert q(0) == SHAPE and q(120) == SHAPE
     mm = lambda lda, ldw, ldy: moe.lib().moe_fp8_matmul(FAKE, FAKE, FAKE, FAKE, 4, 8, 128, lda, ldw, 0, FAKE, ldy, None)
     assert mm(0, 128, 8) == SHAPE and mm(128, 0, 8) == SHAPE and mm(128, 128, 0) == SHAPE
+
+
+def test_matmul_refuses_more_tiles_than_a_launch_holds():
+    """A launch has fewer than 2^32 threads: 2^23 - 8 tiles of 512 (in whole eighths)."""
+    mm = lambda M, N: moe.lib().moe_fp8_matmul(FAKE, FAKE, FAKE, FAKE, M, N, 16, 16, 16, 0, FAKE, N, None)
+    most = (1 << 31) - 1
+    assert mm(1, most) == UNSUP and mm(8, most) == UNSUP and mm(9, most) == UNSUP and mm(64, most) == UNSUP
+    assert mm(most, most) == UNSUP and mm(1 << 23, 1 << 20) == UNSUP
+    # above 64 rows the largest tiles count: 2^23 - 8 of 256 x 256
+    assert mm(256, most) == UNSUP

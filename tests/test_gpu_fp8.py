@@ -596,3 +596,19 @@ def test_a_captured_call_after_its_workspace_has_grown():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(rows, moe.grouped_ffn_a8(x, k, bank, off, sp)) and all((o == 7).all() for o in others)
+
+
+@pytest.mark.parametrize("M", [1, 9])
+def test_matmul_over_more_outputs_than_streaming_workgroups(M):
+    """2^27 + 300 outputs of 16 inputs: more groups of 16 than a launch holds workgroups."""
+    N, K = (1 << 27) + 300, 16
+    w = torch.randint(0, 120, (N, K), dtype=torch.uint8, device=DEV)
+    sw = torch.rand((-(-N // 128), 1), device=DEV) + 0.5
+    a, sa = torch.randint(0, 120, (M, K), generator=_gen(1)).to(torch.uint8), torch.rand((M, 1), generator=_gen(2)) + 0.5
+    y = moe.fp8_matmul(a.to(DEV), sa.to(DEV), w, sw)
+    for lo in (0, (1 << 20) - 128, (1 << 26) + 128 * 77, (1 << 27) - 128 * 16, (1 << 27) + 128):
+        n = min(4096, N - lo)
+        got = y[:, lo:lo + n].contiguous()
+        av = R.decode(a.to(DEV)) * sa.to(DEV).double()
+        ref, bound = R.product(av, R.weights(w[lo:lo + n], sw[lo // 128:lo // 128 + -(-n // 128)]), K, False)
+        assert ((got.double() - ref).abs() <= bound + 2.0 ** -8 * (ref.abs() + bound)).all()
