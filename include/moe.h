@@ -458,7 +458,8 @@ moe_status moe_fp8_matmul(const uint8_t *a, const float *a_scales, const uint8_t
  * of out_dtype: on the FP8 matrix cores for bf16 rows, in full fp32 precision
  * for fp32 rows (1.1 to 1.8 times the time).  Same arguments, layouts and
  * errors as moe_grouped_ffn; any other format -> MOE_ERR_UNSUPPORTED, as are
- * T * hidden >= 2^32 values.  A row of x that holds an infinity or a NaN gives
+ * T * hidden >= 2^32 values and, with hidden < 1024 or inter < 512, more than
+ * 2^23 - 8 tiles (of 64 to 256 rows x 128 inner or 256 output columns).  A row of x that holds an infinity or a NaN gives
  * NaN in its own rows only.
  * Workspace: moe_workspace_bytes(MOE_OP_GROUPED_FFN_A8, T, k, E, H, F).
  */

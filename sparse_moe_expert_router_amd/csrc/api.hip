@@ -698,6 +698,7 @@ moe_status moe_grouped_ffn_a8(const uint16_t* x, int32_t T, int32_t k, const moe
     // quantised rows are addressed with 32 bits
     if ((uint64_t)T * ex->hidden >= (1ull << 32)) return MOE_ERR_UNSUPPORTED;
     if (T == 0) return MOE_OK;
+    if (!moe::ffn_a8_fits(f)) return MOE_ERR_UNSUPPORTED;
     need = moe::ffn_a8_ws_bytes(T, k, ex->num_experts, ex->hidden, ex->inter);
     if (ws_bytes < need) return MOE_ERR_WORKSPACE;
     if (!ws) return MOE_ERR_NULL;

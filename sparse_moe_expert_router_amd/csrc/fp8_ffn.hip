@@ -139,6 +139,12 @@ size_t ffn_a8_ws_bytes(int T, int k, int E, int H, int F) {
            up256((size_t)P * F) + up256((size_t)P * fp8_blocks(F) * 4);
 }
 
+bool ffn_a8_fits(const FfnArgs& f) {
+    const long P = (long)f.T * f.k;
+    const int E = f.offsets ? f.E : 1;
+    return fp8_grouped_workgroups(f.H, f.F, (long)a8_max_tiles(P, E, a8_bt(P, E, f.F, f.out_f32))) <= kMaxWorkgroups;
+}
+
 hipError_t launch_ffn_a8(const FfnArgs& f, void* ws, hipStream_t s) {
     Fp8Ffn p{};
     p.T = f.T; p.k = f.k; p.H = f.H; p.F = f.F; p.P = f.T * f.k;

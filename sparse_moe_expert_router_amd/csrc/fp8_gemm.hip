@@ -793,6 +793,12 @@ static hipError_t launch_run(const Fp8Ffn& p, long tiles, hipStream_t s) {
     return hipGetLastError();
 }
 
+long fp8_grouped_workgroups(int H, int F, long max_tiles) {
+    const long up = H / 128 >= kRunMinKB ? 0 : max_tiles * (F / 128);
+    const long down = F / 128 >= kRunMinKBDown ? 0 : max_tiles * ((H + kGN - 1) / kGN);
+    return up > down ? up : down;
+}
+
 template <int TF, int MODE, bool kExact>
 static hipError_t launch_grouped(const Fp8Ffn& p, long tiles, hipStream_t s) {
     const int KB = (MODE == G_GATEUP ? p.H : p.F) / 128;

@@ -40,6 +40,8 @@ long fp8_skinny_workgroups(int M, int N);
 // Tiles of bt rows (256, 128 or 64; fp32 outputs 128 or 64) x 256 outputs.
 hipError_t launch_fp8_gemm(const Fp8Dense& d, int bt, hipStream_t s);
 hipError_t launch_fp8_gemm_gateup(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s);
+// The most workgroups of a pass that takes one a tile (0: both passes take runs of tiles).
+long fp8_grouped_workgroups(int H, int F, long max_tiles);
 hipError_t launch_fp8_gemm_down(const Fp8Ffn& p, int bt, long max_tiles, hipStream_t s);
 
 }  // namespace moe

@@ -71,6 +71,7 @@ hipError_t launch_fp8_matmul(const uint8_t* a, const float* sa, const uint8_t* w
                              int64_t lda, int64_t ldw, int out_f32, void* y, int64_t ldy, hipStream_t s);
 bool fp8_matmul_fits(int M, int N, int out_f32);  // whether a launch holds the product's workgroups
 size_t ffn_a8_ws_bytes(int T, int k, int E, int H, int F);
+bool ffn_a8_fits(const FfnArgs& f);  // whether its launches hold the call's workgroups
 hipError_t launch_ffn_a8(const FfnArgs& f, void* ws, hipStream_t s);
 
 // ---- the whole layer for few tokens (few.hip)

@@ -122,3 +122,14 @@ def test_matmul_refuses_more_tiles_than_a_launch_holds():
     assert mm(most, most) == UNSUP and mm(1 << 23, 1 << 20) == UNSUP
     # above 64 rows the largest tiles count: 2^23 - 8 of 256 x 256
     assert mm(256, most) == UNSUP
+
+
+def test_experts_refuse_more_tiles_than_a_launch_holds():
+    """Shallow banks launch one workgroup a tile: 2^23 - 8 of them at most."""
+    def ffn(T, k, H, F, dt=0):
+        b = _bank(H=H, F=F, E=64)
+        return moe.lib().moe_grouped_ffn_a8(FAKE, T, k, ctypes.byref(b), FAKE, FAKE, dt, FAKE, FAKE, 1 << 60, None)
+    T = (1 << 25) - 64
+    assert ffn(T, 31, 128, 2048) == UNSUP              # gate/up of one block of 128: 4 million tiles of 16 column groups
+    assert ffn(T, 4, 128, 2048, 1) == UNSUP            # fp32 rows have tiles of 128 rows at most
+    assert ffn(T // 128, 64 * 60, 16384, 256) == UNSUP  # down of two blocks
