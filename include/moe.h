@@ -291,7 +291,9 @@ size_t moe_layer_workspace_bytes(int32_t T, int32_t k, const moe_experts *expert
  * x -> MOE_ERR_SHAPE.  Other requirements and errors as moe_layer's.
  *   ws: moe_layer_few_workspace_bytes(T, k, experts, shared) bytes, 16-byte
  *   aligned, of any content.  Two calls that may run at the same time need
- *   two workspaces (one call clearing the other's counters can leave y NaN).
+ *   two workspaces: on one, each clears the other's counters and overwrites its
+ *   products, and both calls' y is undefined (values of the other call, elements
+ *   never written, NaN), without an error.
  */
 moe_status moe_layer_few(const uint16_t *x, int32_t T, const uint16_t *w_router, int32_t k,
                          const moe_experts *experts, const moe_experts *shared, const float *shared_scale,

@@ -20,8 +20,10 @@
 // The wait always ends: it begins when no gate/up item is left untaken, so each
 // of them is in the hands of a running workgroup, and those wait for nothing
 // before they have finished it.  (No workgroup needs another to be resident
-// that is not, whatever else runs on the GPU.)  It is bounded all the same, for
-// a workspace that a second call clears meanwhile: then y is NaN.
+// that is not, whatever else runs on the GPU.)  It is bounded all the same, so
+// that a second call which clears the workspace meanwhile cannot hang the GPU.
+// Where the bound is met y is NaN, but that is no detection: such calls can as
+// well read each other's h, or leave outputs unwritten; y is undefined.
 // Items are counted in 16 ranges, a cache line each: one counter for all took
 // 20 ns an item, more than the item's work.
 // h passes between compute dies, whose L2s are not coherent within a kernel:
