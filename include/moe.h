@@ -422,7 +422,7 @@ moe_status moe_nvfp4_quantize(const uint16_t *x, int32_t T, int32_t n, float act
  * scales [T][ceil(n/128)] fp32 are contiguous and may not overlap x.  This is
  * the form moe_fp8_matmul reads; moe_grouped_ffn_a8 quantises by itself.
  * n % 16 == 0, a row stride of whole 16-byte pieces, x and codes 16-byte
- * aligned (MOE_ERR_UNSUPPORTED otherwise); T < 0, n < 1 or a stride below n ->
+ * aligned, T * ceil(n/128) below 2^28 (MOE_ERR_UNSUPPORTED otherwise); T < 0, n < 1 or a stride below n ->
  * MOE_ERR_SHAPE; a null pointer with T > 0 -> MOE_ERR_NULL.
  */
 moe_status moe_fp8_quantize(const void *x, int32_t x_dtype, int32_t T, int32_t n, int64_t x_stride,
@@ -433,17 +433,22 @@ moe_status moe_fp8_quantize(const void *x, int32_t x_dtype, int32_t T, int32_t n
  *   y[m][n] = sum_kb a_scales[m][kb] * w_scales[n/128][kb]
  *                    * sum_{i in block kb} e4m3(a[m][i]) * e4m3(w[n][i])
  * accumulated in fp32 and rounded once to out_dtype.  With bf16 outputs the
- * products of a block run on the FP8 matrix cores, which cut the products of
- * every 8 consecutive inputs below 2^-13 of the largest (about 1e-5 of the
- * result in all); with fp32 outputs they run in full fp32 precision on the
- * bf16 matrix cores, at half the rate.  a [M][K] and w [N][K]
+ * products of a block run on the FP8 matrix cores, which align the products of
+ * every 8 consecutive inputs to the largest of them and cut what lies below
+ * 2^-13 of it: before its rounding y is off by at most 7 * 2^-13 times the sum
+ * of the eights' largest products (and by the fp32 additions).  That is about
+ * 1e-5 of the result on normally distributed values, but where the largest
+ * products cancel, the small ones beside them are lost.  With fp32 outputs the
+ * products run in full fp32 precision on the bf16 matrix cores, at half the
+ * rate; that is the form to take where sums cancel.  The two scales of a block
+ * are multiplied first: their fp32 product should be a normal number.
+ * a [M][K] and w [N][K]
  * (one row per output, as in the FP8 banks) have row strides lda, ldw >= K in
  * bytes; a_scales [M][ceil(K/128)] and w_scales [ceil(N/128)][ceil(K/128)] are
  * contiguous fp32; y has row stride ldy >= N in elements; it may not overlap
  * the inputs, and nothing past column N of a row is written.  Any M and N
- * of which 2^23 - 8 tiles hold the outputs (a tile is 256 outputs of 64 to 256
- * rows, so any N up to 2^31 - 2048 for few rows);
- * K, lda and ldw multiples of 16 and the strides at most 4 MiB; a and w
+ * whose outputs 2^23 - 8 tiles hold (a tile is 256 outputs of 64 to 256 rows, so
+ * any N up to 2^31 - 2048 for few rows); K, lda and ldw multiples of 16 and the strides at most 4 MiB; a and w
  * 16-byte aligned, the rest aligned to its element (MOE_ERR_UNSUPPORTED
  * otherwise).  A row of a that holds a NaN (or whose scale is one) gives NaN
  * in that row of y only.  No workspace.
@@ -458,11 +463,20 @@ moe_status moe_fp8_matmul(const uint8_t *a, const float *a_scales, const uint8_t
  * does (h per row and group of 128 inner columns, from its fp32 values), and
  * all three products are computed as moe_fp8_matmul computes them for outputs
  * of out_dtype: on the FP8 matrix cores for bf16 rows, in full fp32 precision
- * for fp32 rows (1.1 to 1.8 times the time).  Same arguments, layouts and
- * errors as moe_grouped_ffn; any other format -> MOE_ERR_UNSUPPORTED, as are
+ * for fp32 rows (1.1 to 1.8 times the time).  Through the quantisation of h the
+ * cut products count for more than in moe_fp8_matmul, as an h near a tie takes
+ * the neighbouring code: against the definition in 64 bits, hidden states with a
+ * few large channels (hidden 2560, inter 640) give bf16 rows that are off by
+ * 2.1e-3 in the 2-norm, 1.7e-3 of it the rounding to bf16, and fp32 rows that
+ * are off by 1e-7 to 1e-4.  Quantising the activations is a larger step: against
+ * moe_grouped_ffn on the same bank the rows differ by 3.7e-2.  moe_grouped_ffn is
+ * the more exact call and up to 16 tokens of 512 experts also the faster one (1
+ * token 28 us against 31, 16 tokens 131 against 139); from 64 tokens on this one
+ * is (331 us against 373, 4096 tokens 590 against 780).  Same arguments, layouts
+ * and errors as moe_grouped_ffn; any other format -> MOE_ERR_UNSUPPORTED, as are
  * T * hidden >= 2^32 values and, with hidden < 1024 or inter < 512, more than
- * 2^23 - 8 tiles (of 64 to 256 rows x 128 inner or 256 output columns).  A row of x that holds an infinity or a NaN gives
- * NaN in its own rows only.
+ * 2^23 - 8 tiles (of 64 to 256 rows x 128 inner or 256 output columns).  A row of
+ * x that holds an infinity or a NaN gives NaN in its own rows only.
  * Workspace: moe_workspace_bytes(MOE_OP_GROUPED_FFN_A8, T, k, E, H, F).
  */
 moe_status moe_grouped_ffn_a8(const uint16_t *x, int32_t T, int32_t k, const moe_experts *ex,

@@ -433,6 +433,8 @@ def fp8_quantize(x, codes=None, scales=None):
 def fp8_matmul(a_codes, a_scales, w_codes, w_scales, out_dtype=None, y=None):
     """y [M, N] = (a . a_scales) (w . w_scales)^T of E4M3 codes a [M, K] and w [N, K] (uint8, K % 16 == 0, rows
     may be strided), scales fp32 [M, ceil(K/128)] and [ceil(N/128), ceil(K/128)]; fp32 sums, one rounding.
+    bf16 outputs take the FP8 matrix cores, which cut the products of every 8 inputs below 2^-13 of the largest: about
+    1e-5 of the result, but all of what is left where the largest cancel.  fp32 outputs have full fp32 precision.
     y's dtype, or out_dtype (OUT_BF16 unless given), says whether y is bf16 or fp32; y's rows may be strided."""
     name = "moe_fp8_matmul"
     _require(a_codes.dim() == 2 and w_codes.dim() == 2 and a_codes.dtype == torch.uint8 and
@@ -464,7 +466,10 @@ def fp8_matmul(a_codes, a_scales, w_codes, w_scales, out_dtype=None, y=None):
 def grouped_ffn_a8(x, k: int, bank: dict, offsets=None, sorted_pair=None, out_dtype=OUT_BF16, ws=None, rows=None):
     """grouped_ffn of an "fp8" bank with the activations quantised to FP8 too (x and the SwiGLU product, per row
     and 128 values): rows [T*k, H] in grouped order (identity order when offsets is None).  Without `ws` a
-    workspace is allocated for the call, so that calls on several streams or in several graphs do not meet."""
+    workspace is allocated for the call, so that calls on several streams or in several graphs do not meet.
+    fp32 rows are made in full fp32 precision, bf16 rows on the FP8 matrix cores (see fp8_matmul); quantising the
+    activations moves the rows by some 1e-2, so for few tokens (up to 16 of 512 experts) grouped_ffn is the better
+    call, and from about 64 on this one is the faster."""
     name = "moe_grouped_ffn_a8"
     _require(bank["fmt"] == "fp8", name, f"needs an fp8 bank, got {bank['fmt']}")
     E, H, F = bank_dims(bank)
