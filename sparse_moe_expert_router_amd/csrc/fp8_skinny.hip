@@ -48,11 +48,13 @@ __device__ __forceinline__ void fp8_wave_product(f32x4_t (&acc)[TF], __amdgpu_bu
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int kb = min(kbase + u * kstep, KB - 1);
+            // past the last block both scales are zero (an infinite one times zero is none)
+            const int kb = kbase + u * kstep;
+            const float ws = kb < KB ? sw[min(kb, KB - 1)] : 0.0f;
 #pragma unroll
             for (int t = 0; t < TF; ++t) {
                 const f32x4_t d = mfma_fp8<kExact>(w[u], a[u][t]);
-                const float c = s[u][t] * sw[kb];
+                const float c = s[u][t] * ws;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[t][j] = fmaf(c, d[j], acc[t][j]);
             }

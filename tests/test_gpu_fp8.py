@@ -612,3 +612,18 @@ def test_matmul_over_more_outputs_than_streaming_workgroups(M):
         av = R.decode(a.to(DEV)) * sa.to(DEV).double()
         ref, bound = R.product(av, R.weights(w[lo:lo + n], sw[lo // 128:lo // 128 + -(-n // 128)]), K, False)
         assert ((got.double() - ref).abs() <= bound + 2.0 ** -8 * (ref.abs() + bound)).all()
+
+
+@pytest.mark.parametrize("out", [moe.OUT_BF16, moe.OUT_F32])
+@pytest.mark.parametrize("M,K", [(1, 128), (3, 400), (40, 640), (700, 400), (700, 128), (2000, 400), (2000, 128), (40000, 272)])
+def test_matmul_infinite_weight_scale(M, K, out):
+    """Positive codes times an infinite scale are infinite: no block behind the last one adds 0 * inf."""
+    N, kb = 300, -(-K // 128)
+    g = _gen(K)
+    a, w = (torch.randint(1, 120, s, generator=g).to(torch.uint8) for s in ((M, K), (N, K)))
+    sa, sw = torch.rand((M, kb), generator=g) + 0.5, torch.rand((3, kb), generator=g) + 0.5
+    clean = moe.fp8_matmul(*(t.to(DEV) for t in (a, sa, w, sw)), out_dtype=out)
+    sw[1, kb - 1] = float("inf")
+    y = moe.fp8_matmul(*(t.to(DEV) for t in (a, sa, w, sw)), out_dtype=out)
+    assert (y[:, 128:256] == float("inf")).all()
+    assert torch.equal(y[:, :128], clean[:, :128]) and torch.equal(y[:, 256:], clean[:, 256:])
