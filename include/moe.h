@@ -280,9 +280,10 @@ size_t moe_layer_workspace_bytes(int32_t T, int32_t k, const moe_experts *expert
  *   y[t] = sum_j topk_gate[t][j] * expert(topk_idx[t][j], x[t])
  *          + shared_scale[t] * shared(x[t])
  * for decode steps where launches and the waits between them cost as much as
- * the weights: at one or two tokens it takes 0.6 to 0.8 of moe_layer's time, at
- * four about the same, and towards 16 moe_layer is the faster.  Routing is moe_route's, exactly (topk_idx, nullable [T][k],
- * receives it).  The gated SwiGLU products are rounded to bf16, everything
+ * the weights: at one token it takes 0.6 to 0.8 of moe_layer's time, at two 0.8
+ * to 0.95, at four the same, and from there on moe_layer is the faster (at 16 by
+ * 1.15 to 1.5 times).  Routing is moe_route's, exactly (topk_idx, nullable
+ * [T][k], receives it).  The gated SwiGLU products are rounded to bf16, everything
  * after them stays in fp32 until y is rounded to bf16 (moe_layer rounds the
  * products before the gate, and the experts' rows to bf16 on the
  * way, so the two differ by those roundings).  experts: bf16, FP8 or

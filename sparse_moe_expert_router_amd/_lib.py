@@ -603,7 +603,7 @@ class FewTokenLayer:
     into a graph are the caller's to order (their replays with each other and
     with other calls), and the object has to live as long as the graph.
 
-    For one or two tokens, where it takes 0.6 to 0.8 of LayerCall's time; from
+    For one or two tokens, where it takes 0.6 to 0.95 of LayerCall's time; from
     four on LayerCall is as fast or faster."""
 
     def __init__(self, w_router, k: int, bank: dict, shared: dict | None = None, max_tokens: int = FEW_MAX_TOKENS,

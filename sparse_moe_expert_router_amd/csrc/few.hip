@@ -40,11 +40,11 @@
 // fetched from memory.
 //
 // Measured, hidden 2560, 10 of 512 experts of 640, a shared expert of 640: one
-// token in 38 (FP8), 39 (4-bit) and 47 us (bf16), of which the bytes need 13, 8
-// and 24; the layer of separate kernels takes 55 to 65, 63 to 69 and 59 to 67.
-// Four tokens take the same either way (70 to 98 us).  16 take 188, 179 and 284
-// us here and 155, 137 and 251 there: of the 188 the front takes 12, selection
-// 9, gate/up 98 (4.6 TB/s), the items' ends and the wait 11.
+// token in 38 (FP8), 39 (4-bit) and 48 us (bf16), of which the bytes need 13, 8
+// and 24; the layer of separate kernels takes 55 to 63, 63 to 66 and 60 to 65.
+// Four tokens take the same either way (71 to 101 us).  16 take 188 to 198, 182
+// and 291 us here and 155 to 159, 117 to 121 and 250 to 255 there: of 188 the
+// front took 12, selection 9, gate/up 98 (4.6 TB/s), the items' ends and the wait 11.
 #include "fp8.h"
 #include "ffn_internal.h"
 #include "select.h"
@@ -515,9 +515,9 @@ struct FewLists {
 static_assert(FewLists::bytes(kFewMaxPairs, 1024) <= 64 * 1024, "what a launch gets without asking");
 
 // Top k of token t's E <= 512 logits by one wave.  Lane i holds experts 8 i ..
-// 8 i + 7.  Fewer than k of the lanes' largest logits lie above some lane's
-// largest only if that is at least the k-th largest logit of all; the smallest
-// such bounds the top k from below, usually leaving little more than k
+// 8 i + 7.  Of the lanes' largest logits, those with fewer than k others above
+// them are at least k; all of these are logits at or above the smallest of them,
+// so that one bounds the top k from below.  It usually leaves little more than k
 // candidates, and each finds its rank by comparing itself with the others.
 // Against k rounds of a wave-wide maximum this has no long chain, and a third
 // of the instructions, which every workgroup of the launch executes.
@@ -681,7 +681,8 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_experts_kernel(const FewAr
     // few items are cut finely, many keep a wave on longer runs, and the 4-bit
     // rows, half as long, take the coarser cut.  (Hidden 2560, 640 columns, cut in
     // 8 / 4 / 2.  16 tokens, about 138 experts: FP8 195 / 188 / 189 us, 4-bit 203 /
-    // 187 / 179; 4 tokens: FP8 70 / 72 / -, 4-bit 74 / 71 / -.)
+    // 187 / 179; 4 tokens: FP8 70 / 72 / -, 4-bit 74 / 71 / -; 1 token: FP8 37.9 /
+    // 37.3 / 43.0, 4-bit 39.2 / 38.1 / 45.3, bf16 48.2 / 49.2 / 59.2.)
     const int cols8 = slots * (a.F / 8);
     const int ks = cols8 < 1024 ? 8 : cols8 < 4096 ? (FMT == F_AWQ ? 4 : 8) : FMT == F_AWQ ? 2 : 4;
     const int cw = kFewWaves / ks;

@@ -66,10 +66,15 @@ static size_t a8_max_tiles(long P, int E, int bt) { return (size_t)(P / bt + (P 
 // Measured with hidden 2560, inter 640, tiles of 64 / 128 / 256 rows, us.  Rows on
 // average over 64 experts: 8 79 / 91 / 128, 48 92 / 101 / 136, 80 112 / 109 / 142, 128
 // 140 / 119 / 150, 320 234 / 202 / 226; over 256: 64 330 / 295 / 380, 128 446 / 397 /
-// 412, 192 583 / 491 / 442, 640 1507 / 1251 / 1199, 1280 2863 / 2332 / 2160.  Hidden
-// 4096, inter 1152, 128 rows on average over 8 experts: 56 / 61 / 83.  fp32 rows
-// (exact products) have the first two, us: over 512 experts 5 rows on average 496 /
-// 688, 80 932 / 790; over 256 128 605 / 582, 1280 4497 / 3757.
+// 412, 192 583 / 491 / 442, 256 702 / 601 / 617, 384 1008 / 827 / 807, 640 1507 / 1251
+// / 1199, 1280 2863 / 2332 / 2160.  Hidden 4096, inter 1152, over 8 experts: 128 rows
+// 56 / 61 / 83, 512 131 / 122 / 114, 1024 217 / 193 / 203.  (How a tile's size divides
+// an expert's rows matters as much as it: at 256 rows over 256 experts the rule is 3 %
+// off the best, at 512 over 8 experts 7 %.)  One row per expert, where the bytes of
+// the touched experts' weights need less than the steps of a tile: 1 token of ten
+// experts 31 / 40 / 58, its bytes 10; 16 tokens 136 / 150 / 219, its bytes 137.  fp32
+// rows (exact products) have the first two, us: over 512 experts 5 rows on average
+// 496 / 688, 80 932 / 790; over 256 128 605 / 582, 1280 4497 / 3757.
 static int a8_bt(long P, int E, int F, int out_f32) {
     const long active = P < E ? P : E, avg = P / active, cols = F / 128;
     auto tiles = [&](long rows) { return (P / rows + active / 2) * cols; };
@@ -118,8 +123,9 @@ __device__ __forceinline__ void a8_tile_table(const int32_t* __restrict__ offset
 }
 
 // What the products need first, in one launch: workgroup 0 writes the tile table,
-// the others quantise x.  (Against two launches, 16 tokens of 512 experts: 139.5
-// -> 136.5 us.)
+// the others quantise x.  (Against two launches, 16 tokens of 512 experts: 137.2
+// -> 134.3 us, 4096 tokens 580 -> 577, 32768 tokens of 256 no difference: between
+// the experts' passes the quantiser takes 58 us in either launch.)
 __global__ __launch_bounds__(kPrepThreads) void a8_prepare_kernel(const Fp8Ffn p, const uint16_t* __restrict__ x, int bt, int most,
                                                                   int32_t* __restrict__ tiles, uint8_t* __restrict__ xq,
                                                                   float* __restrict__ xs) {
