@@ -423,8 +423,8 @@ moe_status moe_nvfp4_quantize(const uint16_t *x, int32_t T, int32_t n, float act
  * scales [T][ceil(n/128)] fp32 are contiguous and may not overlap x.  This is
  * the form moe_fp8_matmul reads; moe_grouped_ffn_a8 quantises by itself.
  * n % 16 == 0, a row stride of whole 16-byte pieces, x and codes 16-byte
- * aligned, T * ceil(n/128) below 2^28 (MOE_ERR_UNSUPPORTED otherwise); T < 0, n < 1 or a stride below n ->
- * MOE_ERR_SHAPE; a null pointer with T > 0 -> MOE_ERR_NULL.
+ * aligned, T * ceil(n/128) below 2^28 (MOE_ERR_UNSUPPORTED otherwise); T < 0, n < 1
+ * or a stride below n -> MOE_ERR_SHAPE; a null pointer with T > 0 -> MOE_ERR_NULL.
  */
 moe_status moe_fp8_quantize(const void *x, int32_t x_dtype, int32_t T, int32_t n, int64_t x_stride,
                             uint8_t *codes, float *scales, void *stream);
@@ -449,10 +449,10 @@ moe_status moe_fp8_quantize(const void *x, int32_t x_dtype, int32_t T, int32_t n
  * contiguous fp32; y has row stride ldy >= N in elements; it may not overlap
  * the inputs, and nothing past column N of a row is written.  Any M and N
  * whose outputs 2^23 - 8 tiles hold (a tile is 256 outputs of 64 to 256 rows, so
- * any N up to 2^31 - 2048 for few rows); K, lda and ldw multiples of 16 and the strides at most 4 MiB; a and w
- * 16-byte aligned, the rest aligned to its element (MOE_ERR_UNSUPPORTED
- * otherwise).  A row of a that holds a NaN (or whose scale is one) gives NaN
- * in that row of y only.  No workspace.
+ * any N up to 2^31 - 2048 for few rows); K, lda and ldw multiples of 16 and the
+ * strides at most 4 MiB; a and w 16-byte aligned, the rest aligned to its element
+ * (MOE_ERR_UNSUPPORTED otherwise).  A row of a that holds a NaN (or whose scale is
+ * one) gives NaN in that row of y only.  No workspace.
  */
 moe_status moe_fp8_matmul(const uint8_t *a, const float *a_scales, const uint8_t *w, const float *w_scales,
                           int32_t M, int32_t N, int32_t K, int64_t lda, int64_t ldw, int32_t out_dtype,

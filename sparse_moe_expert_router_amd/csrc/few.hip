@@ -356,8 +356,9 @@ __device__ __forceinline__ void store_h(__amdgpu_buffer_rsrc_t r, uint32_t row, 
 // 16 outputs from o0.  expert(slot), hoff(slot): the slot's expert and the byte
 // offset of the lane's token's h (kOob: not routed to it; the token's sum is
 // then left alone, as zeros times the expert's weights are no zeros where those
-// hold an infinity or a NaN).  `ready` is called once the first U units are under way.  The next U units' weights are loaded
-// before the present ones are used (16 tokens, FP8: 205 -> 189 us, bf16 320 -> 285).
+// hold an infinity or a NaN).  `ready` is called once the first U units are under
+// way.  The next U units' weights are loaded before the present ones are used
+// (16 tokens, FP8: 205 -> 189 us, bf16 320 -> 285).
 template <int FMT, int U, class Expert, class Hoff, class Ready>
 __device__ __forceinline__ void down_units(f32x4_t& acc, const FewProj& pd, int H, int F, int o0, __amdgpu_buffer_rsrc_t rh,
                                            int v0, int v1, Expert expert, Hoff hoff, Ready ready) {

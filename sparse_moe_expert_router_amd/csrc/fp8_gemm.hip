@@ -28,12 +28,13 @@
 //
 // Measured: 8192 x 8192 x 8192 in 477 to 505 us by the card, 2.18 to 2.30 PFLOP/s;
 // 32768 tokens to 10 of 256 experts (hidden 2560, inter 640): gate/up 1260 us, 1.70
-// PFLOP/s, down 820 us, of which its 1.7 GB of rows need 340.  The MFMA is busy 54, 44 and 34 % of
-// the cycles, other vector instructions 35, 40 and 27 % (1.93 GHz under this load):
-// every 128 products of an output need an fp32 multiply-add outside it.  Gate/up
-// spends about 35 us on SwiGLU and 48 on the quantisation, and both passes compute
-// the rows that pad each expert's last tile.  In down, with five steps a tile, the
-// matrix cores also stand still while all waves convert and store a tile together.
+// PFLOP/s, down 820 us, of which its 1.7 GB of rows need 340.  The MFMA is busy 54,
+// 44 and 34 % of the cycles, other vector instructions 35, 40 and 27 % (1.93 GHz
+// under this load): every 128 products of an output need an fp32 multiply-add
+// outside it.  Gate/up spends about 35 us on SwiGLU and 48 on the quantisation, and
+// both passes compute the rows that pad each expert's last tile.  In down, with
+// five steps a tile, the matrix cores also stand still while all waves convert and
+// store a tile together.
 #include "fp8.h"
 #include "ffn_internal.h"
 #include "fp8_internal.h"
