@@ -32,7 +32,8 @@
  *    or moe_layer_workspace_bytes().  Calls on different streams need
  *    distinct workspaces.
  *  - Results are deterministic: the same inputs give the same bits.
- *  - T = 0 is a valid no-op for every call.
+ *  - T = 0 is a valid no-op for every call (sums over tokens that a call
+ *    overwrites are set to 0: its comment says so).
  *
  * Layouts (row-major, all contiguous):
  *  x           [T][H]        bf16 hidden states (already normalised)
@@ -134,7 +135,8 @@ typedef struct {
 enum { MOE_OP_ROUTE = 0, MOE_OP_PERMUTE = 1, MOE_OP_GROUPED_FFN = 2, MOE_OP_REFILL_SCORE = 3,
        MOE_OP_GROUPED_FFN_NVFP4 = 4, /* grouped FFN of an NVFP4 bank (adds the quantised input) */
        MOE_OP_ROUTE_PERMUTE = 5,
-       MOE_OP_GROUPED_FFN_A8 = 6 };
+       MOE_OP_GROUPED_FFN_A8 = 6,
+       MOE_OP_ADD_RMSNORM_BACKWARD = 7, MOE_OP_BALANCE_LOSS = 8 };
 
 /*
  * Router: logits, softmax, top-k, renormalised gates.
@@ -484,6 +486,124 @@ moe_status moe_grouped_ffn_a8(const uint16_t *x, int32_t T, int32_t k, const moe
                               const int32_t *expert_offsets, const int32_t *sorted_pair,
                               int32_t out_dtype, void *rows, void *ws, size_t ws_bytes,
                               void *stream);
+
+/*
+ * Residual addition and root-mean-square norm of T rows of H values (the
+ * architecture sheet's pre-norm with gain 1 + w, eps 1e-6): the step before the
+ * layer, whose x is y here.  Per row, in fp32:
+ *   s = x + residual, rounded to res_dtype     (s = x without a residual)
+ *   r = 1 / sqrt(mean(s^2) + eps)
+ *   v = s r (gain_offset + weight)
+ * x, y, residual and residual_out have row strides in elements of at least H;
+ * weight [H] is contiguous.  residual and residual_out (nullable, together; of
+ * res_dtype): residual_out receives s.  y (nullable) receives v as bf16.  codes
+ * [T][H] and scales [T][ceil(H/128)] (nullable, together, contiguous) receive v
+ * as moe_fp8_quantize quantises, from its fp32 values: the form moe_fp8_matmul
+ * reads.  rstd (nullable, [T] fp32) receives r, which the backward pass reads.
+ * One of y and codes must be given.  x_dtype, res_dtype and w_dtype are
+ * MOE_OUT_BF16 or MOE_OUT_F32.  An output may be an input of the same type and
+ * stride (residual_out = residual, y = x); any other overlap of an output with
+ * an input or another output -> MOE_ERR_SHAPE.  A row that holds an infinity or a
+ * NaN gives NaN (and 0) in its own row only; squares are summed in fp32, so a row
+ * of values above about 1e18 gives zeros.
+ * H % 8 == 0 (with codes H % 16 == 0), H <= 16384, rows of whole 16-byte pieces,
+ * x, residuals, weight, y and codes 16-byte aligned, scales and rstd 4-byte
+ * (MOE_ERR_UNSUPPORTED otherwise); eps not in (0, 3e38) or gain_offset not
+ * finite -> MOE_ERR_SHAPE.
+ */
+moe_status moe_add_rmsnorm(const void *x, int32_t x_dtype, int64_t x_stride, const void *residual,
+                           int64_t residual_stride, void *residual_out, int64_t residual_out_stride,
+                           int32_t res_dtype, const void *weight, int32_t w_dtype, float gain_offset, float eps,
+                           int32_t T, int32_t H, uint16_t *y, int64_t y_stride, uint8_t *codes, float *scales,
+                           float *rstd, void *stream);
+
+/*
+ * Gradients of moe_add_rmsnorm's y: with s the rows that were normalised
+ * (residual_out, or x without a residual), r = rstd as the forward pass gave it,
+ * h = s r and u = dy (gain_offset + weight), in fp32:
+ *   dx = r (u - h mean(u h)) + dres      for x and for the residual alike
+ *   dw = sum over the rows of dy h       [H] fp32, overwritten
+ * dres (nullable) is the gradient that reaches residual_out from elsewhere.  dy
+ * is of dy_dtype; s, dres and dx are of s_dtype; all four have row strides.  dx
+ * may be dy, s or dres where type and stride are the same; any other overlap ->
+ * MOE_ERR_SHAPE.  The sums over rows are taken in a fixed order.  T = 0 sets dw to
+ * 0.  Sizes, alignment and errors as moe_add_rmsnorm's; workspace:
+ * moe_workspace_bytes(MOE_OP_ADD_RMSNORM_BACKWARD, T, 1, 1, H, 0), 16-byte aligned.
+ */
+moe_status moe_add_rmsnorm_backward(const void *dy, int32_t dy_dtype, int64_t dy_stride, const void *s,
+                                    int64_t s_stride, int32_t s_dtype, const float *rstd, const void *weight,
+                                    int32_t w_dtype, float gain_offset, const void *dres, int64_t dres_stride,
+                                    int32_t T, int32_t H, void *dx, int64_t dx_stride, float *dw, void *ws,
+                                    size_t ws_bytes, void *stream);
+
+/*
+ * Routed pairs per expert: counts[e] (uint32 [E]) = the number of slots of
+ * topk_idx [T][k] (as moe_route gives it) that name expert e, over the tokens
+ * with token_valid[t] != 0 (uint8 [T], nullable = all); with accumulate != 0
+ * they are added to what counts holds.  Ids outside [0, E) are not counted.
+ * T = 0 clears counts unless accumulate is set.  k <= E <= 1024.
+ */
+moe_status moe_expert_counts(const int32_t *topk_idx, int32_t T, int32_t k, int32_t E, const uint8_t *token_valid,
+                             int32_t accumulate, uint32_t *counts, void *stream);
+
+/*
+ * Balance loss of the router and the gradient of its logits (architecture
+ * sheet, training entries: load-balancing loss over the global batch).  With c
+ * the counts, C their sum, f_e = c_e / C, p_t the softmax of the logits of token
+ * t and S_e the sum of p_te over the valid tokens of this call:
+ *   loss          = coef E k / C * sum_e f_e S_e
+ *   dlogits[t][e] = coef E k / C * p_te (f_e - sum_j f_j p_tj)
+ * (f counts decisions and has no gradient).  C / k is the number of tokens that
+ * were counted: with this call's own counts the loss is coef E sum_e f_e
+ * mean(p_e); with counts of a larger batch (added over micro-batches, summed
+ * over ranks) it is this call's share of that batch's loss, and the shares and
+ * gradients add up to it.  C = 0 gives loss 0 and no gradient.
+ * With topk_idx, topk_gate and dgate ([T][k]; all three or none, and then
+ * dlogits is required) the gradient dgate of the gates is taken through their
+ * renormalised softmax and added:
+ *   dlogits[t][idx_j] += g_j (dgate_j - sum_i g_i dgate_i)
+ * (slots that name the same expert add up; an id outside [0, E) receives nothing).
+ * logits [T][E] and dlogits (nullable) have row strides in elements and are bf16
+ * or fp32; dlogits may be logits itself where types and strides are the same
+ * (any other overlap -> MOE_ERR_SHAPE).  Logits of -inf (experts that are masked
+ * out) have probability 0; a token whose logits are all -inf and a token that is
+ * not valid count for nothing and get gradient 0 (the latter whatever its logits,
+ * gates and ids hold; the former still gets its gates').  NaN or +inf gives NaN in
+ * the token's row and in the sums.  loss [1] and prob_sum (nullable, S [E]) are
+ * fp32, overwritten; T = 0 sets them to 0.  Sums over tokens are taken in a fixed
+ * order.  k <= E <= 1024, k <= 64; coef not finite -> MOE_ERR_SHAPE.  Workspace:
+ * moe_workspace_bytes(MOE_OP_BALANCE_LOSS, T, k, E, 0, 0), 16-byte aligned.
+ */
+moe_status moe_balance_loss(const void *logits, int32_t logits_dtype, int64_t logits_stride, int32_t T, int32_t E,
+                            int32_t k, const uint32_t *counts, float coef, const uint8_t *token_valid,
+                            const int32_t *topk_idx, const float *topk_gate, const float *dgate, float *loss,
+                            float *prob_sum, void *dlogits, int32_t dlogits_dtype, int64_t dlogits_stride, void *ws,
+                            size_t ws_bytes, void *stream);
+
+/*
+ * Product of bf16 rows with one AWQ matrix as stored (GEMM packing, see
+ * Layouts), for few rows: projections of a decode step in the experts' 4-bit
+ * format.
+ *   y[m][n] = sum_g scales[g][n] * sum_{i in group g} x[m][i] (q[i][n] - z[g][n])
+ * qweight [K][N/8] int32, qzeros [K/group][N/8] int32, scales [K/group][N] fp16,
+ * contiguous; group 32, 64 or 128 inputs.  x [M][K] and y [M][N] (bf16 or fp32
+ * by out_dtype) have row strides ldx >= K, ldy >= N in elements; y may not
+ * overlap x (MOE_ERR_SHAPE).  The codes enter exactly and the sums are fp32: x
+ * (16 + q) and x (16 + z) are summed and subtracted per 32 inputs, so the sums'
+ * roundings are those of values up to 31 |x|.  Every 64 rows read the codes
+ * again: any M works, but the call is made for up to about 64 rows.  A row of x
+ * that holds an infinity or a NaN gives NaN in that row only.
+ * N % 8 == 0, K % group == 0, ldx % 8 == 0, N and K at most 2^24, M at most 2^20,
+ * fewer than 2^23 tiles of 64 rows x 128 columns; x and scales 16-byte aligned,
+ * the rest aligned to its element (MOE_ERR_UNSUPPORTED otherwise).  Workspace:
+ * moe_awq_matmul_workspace_bytes(M, N, K, group), 16-byte aligned, of any content.
+ */
+moe_status moe_awq_matmul(const uint16_t *x, int64_t ldx, const int32_t *qweight, const int32_t *qzeros,
+                          const uint16_t *scales, int32_t M, int32_t N, int32_t K, int32_t group, int32_t out_dtype,
+                          void *y, int64_t ldy, void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace bytes of moe_awq_matmul (0 when none is needed, or for sizes it refuses). */
+size_t moe_awq_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t group);
 
 /* Scratch bytes an operation needs (0 when none).  For MOE_OP_GROUPED_FFN,
  * k is the pairs per token and E the bank's expert count; an NVFP4 bank needs

@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -31,6 +32,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 OP_ROUTE, OP_PERMUTE, OP_GROUPED_FFN, OP_REFILL_SCORE, OP_GROUPED_FFN_NVFP4, OP_ROUTE_PERMUTE = 0, 1, 2, 3, 4, 5
 OP_GROUPED_FFN_A8 = 6
+OP_ADD_RMSNORM_BACKWARD, OP_BALANCE_LOSS = 7, 8
 W_BF16, W_AWQ, W_FP8, W_NVFP4, W_AWQ_OM = 0, 1, 2, 3, 4
 OUT_BF16, OUT_F32 = 0, 1
 
@@ -39,7 +41,9 @@ EXPORTS = ["moe_route", "moe_permute", "moe_route_permute", "moe_grouped_ffn", "
            "moe_layer_few", "moe_layer_few_workspace_bytes", "moe_combine",
            "moe_refill_score",
            "moe_refill_finalize", "moe_prune_slice", "moe_router_norm_keep",
-           "moe_nvfp4_quantize", "moe_fp8_quantize", "moe_fp8_matmul", "moe_grouped_ffn_a8", "moe_awq_to_output_major", "moe_workspace_bytes", "moe_status_string",
+           "moe_nvfp4_quantize", "moe_fp8_quantize", "moe_fp8_matmul", "moe_grouped_ffn_a8", "moe_awq_to_output_major",
+           "moe_add_rmsnorm", "moe_add_rmsnorm_backward", "moe_expert_counts", "moe_balance_loss", "moe_awq_matmul",
+           "moe_awq_matmul_workspace_bytes", "moe_workspace_bytes", "moe_status_string",
            "moe_last_hip_error"]
 
 
@@ -94,6 +98,13 @@ def lib():
                       P, ctypes.POINTER(P)],
     }
     sig["moe_layer_few"] = [P, i32, P, i32, ctypes.POINTER(_Experts), ctypes.POINTER(_Experts), P, P, P, P, sz, P]
+    sig["moe_add_rmsnorm"] = [P, i32, i64, P, i64, P, i64, i32, P, i32, ctypes.c_float, ctypes.c_float, i32, i32, P, i64, P,
+                              P, P, P]
+    sig["moe_add_rmsnorm_backward"] = [P, i32, i64, P, i64, i32, P, P, i32, ctypes.c_float, P, i64, i32, i32, P, i64, P, P,
+                                       sz, P]
+    sig["moe_expert_counts"] = [P, i32, i32, i32, P, i32, P, P]
+    sig["moe_balance_loss"] = [P, i32, i64, i32, i32, i32, P, ctypes.c_float, P, P, P, P, P, P, P, i32, i64, P, sz, P]
+    sig["moe_awq_matmul"] = [P, i64, P, P, P, i32, i32, i32, i32, i32, P, i64, P, sz, P]
     for name, args in sig.items():
         f = getattr(L, name)
         f.argtypes = args
@@ -104,6 +115,8 @@ def lib():
     L.moe_layer_workspace_bytes.restype = ctypes.c_size_t
     L.moe_layer_few_workspace_bytes.argtypes = [i32, i32, ctypes.POINTER(_Experts), ctypes.POINTER(_Experts)]
     L.moe_layer_few_workspace_bytes.restype = ctypes.c_size_t
+    L.moe_awq_matmul_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.moe_awq_matmul_workspace_bytes.restype = ctypes.c_size_t
     L.moe_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
     L.moe_workspace_bytes.restype = ctypes.c_size_t
     L.moe_status_string.argtypes = [ctypes.c_int]
@@ -509,6 +522,199 @@ def awq_to_output_major(bank: dict) -> dict:
     _check("moe_awq_to_output_major", lib().moe_awq_to_output_major(ctypes.byref(src), ctypes.byref(dst),
                                                                     _stream()))
     return out
+
+
+_DTYPES = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
+
+
+def _matrix(name, what, t, shape=None, dtype=None):
+    """(pointer, dtype code, row stride) of a bf16 or fp32 matrix with contiguous rows; (None, 0, 0) for None."""
+    if t is None:
+        return None, OUT_BF16, 0
+    code = _DTYPES.get(t.dtype)
+    if code is None or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise MoeError(f"{name}: {what} must be a bf16 or fp32 matrix with contiguous rows")
+    if (shape is not None and t.shape != shape) or (dtype is not None and t.dtype != dtype):
+        raise MoeError(f"{name}: {what} must be {dtype or 'bf16 or fp32'} {list(shape)}")
+    return t.data_ptr(), code, t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _array(name, what, t, shape, dtype, nullable=True):
+    """Pointer of a contiguous tensor of the given shape and dtype, or None."""
+    if t is None and nullable:
+        return None
+    if t is None or t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise MoeError(f"{name}: {what} must be contiguous {dtype} {list(shape)}")
+    return t.data_ptr()
+
+
+class NormResult(NamedTuple):
+    """What add_rmsnorm wrote; None where it was not asked for."""
+    y: torch.Tensor | None         # bf16 [T, H]
+    residual: torch.Tensor | None  # the sum, in the residual's type
+    codes: torch.Tensor | None     # uint8 E4M3 [T, H] ...
+    scales: torch.Tensor | None    # ... and fp32 [T, ceil(H/128)], as fp8_matmul takes them
+    rstd: torch.Tensor | None      # fp32 [T], for add_rmsnorm_backward
+
+
+def add_rmsnorm(x, weight, residual=None, eps: float = 1e-6, gain_offset: float = 1.0, outputs=None, residual_out=None,
+                y=None, codes=None, scales=None, rstd=None) -> NormResult:
+    """s = x + residual (rounded to the residual's type; x alone without one), then s / sqrt(mean(s^2) + eps) *
+    (gain_offset + weight), row by row of x [T, H] (bf16 or fp32, H % 8 == 0, H <= 16384).
+
+    `outputs` names what is made: "y" (bf16 rows, the layer's input), "fp8" (E4M3 codes with one scale per row and 128
+    values, fp8_matmul's input; H % 16 == 0), "rstd" (for add_rmsnorm_backward).  Tensors given for outputs are
+    written and need not be named; with no names and neither y nor codes given, y is made.  The sum goes to
+    residual_out (new unless given; it may be `residual` itself).  Matrices may have strided rows, codes and scales
+    may not."""
+    name = "moe_add_rmsnorm"
+    px, dx, ldx = _matrix(name, "x", x)
+    T, H = x.shape
+    dev = x.device
+    fp8 = codes is not None or scales is not None
+    if outputs is None:
+        outputs = () if fp8 or y is not None else ("y",)
+    _require(all(o in ("y", "fp8", "rstd") for o in outputs), name, "outputs are among y, fp8 and rstd")
+    fp8, want_y = fp8 or "fp8" in outputs, y is not None or "y" in outputs
+    _require(weight.dtype in _DTYPES and weight.shape == (H,) and weight.is_contiguous(), name,
+             "weight must be contiguous bf16 or fp32 [H]")
+    if want_y and y is None:
+        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    if fp8 and codes is None:
+        codes = torch.empty((T, H), dtype=torch.uint8, device=dev)
+    if fp8 and scales is None:
+        scales = torch.empty((T, -(-H // 128)), dtype=torch.float32, device=dev)
+    if rstd is None and "rstd" in outputs:
+        rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    pr, dr, ldr = _matrix(name, "residual", residual, x.shape)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty((T, H), dtype=residual.dtype, device=dev)
+    _require(residual is not None or residual_out is None, name, "residual_out without a residual")
+    po, _, ldo = _matrix(name, "residual_out", residual_out, x.shape, residual.dtype if residual is not None else None)
+    py, _, ldy = _matrix(name, "y", y, x.shape, torch.bfloat16)
+    pc = _array(name, "codes", codes, x.shape, torch.uint8)
+    ps = _array(name, "scales", scales, (T, -(-H // 128)), torch.float32)
+    pt = _array(name, "rstd", rstd, (T,), torch.float32)
+    _require(T == 0 or py is not None or pc is not None, name, "outputs must name y or fp8")
+    _same_device(name, dev, weight, residual, residual_out, y, codes, scales, rstd)
+    d = _Device(x)
+    d.call(name, px, dx, ldx, pr, ldr, po, ldo, dr, weight.data_ptr(), _DTYPES[weight.dtype], gain_offset, eps, T, H, py, ldy,
+           pc, ps, pt, d.stream)
+    return NormResult(y, residual_out, codes, scales, rstd)
+
+
+def add_rmsnorm_backward(dy, s, rstd, weight, gain_offset: float = 1.0, dres=None, dx=None, dw=None, ws=None):
+    """Gradients of add_rmsnorm's y: (dx [T, H] of s's type, for x and the residual alike; dw fp32 [H]).
+
+    s: what was normalised (NormResult.residual, or x without a residual), rstd: NormResult.rstd, dy: y's gradient,
+    dres (s's type): the gradient that reaches the sum from elsewhere, added to dx.  dx may be dy, s or dres where type
+    and strides are the same.  Without `ws` a workspace is allocated for the call."""
+    name = "moe_add_rmsnorm_backward"
+    ps, ds, lds = _matrix(name, "s", s)
+    T, H = s.shape
+    py, dyt, ldy = _matrix(name, "dy", dy, s.shape)
+    pd, _, ldd = _matrix(name, "dres", dres, s.shape, s.dtype)
+    if dx is None:
+        dx = torch.empty((T, H), dtype=s.dtype, device=s.device)
+    px, _, ldx = _matrix(name, "dx", dx, s.shape, s.dtype)
+    if dw is None:
+        dw = torch.empty(H, dtype=torch.float32, device=s.device)
+    pw = _array(name, "dw", dw, (H,), torch.float32)
+    pt = _array(name, "rstd", rstd, (T,), torch.float32, nullable=False)
+    _require(weight.dtype in _DTYPES and weight.shape == (H,) and weight.is_contiguous(), name,
+             "weight must be contiguous bf16 or fp32 [H]")
+    _same_device(name, s.device, dy, rstd, weight, dres, dx, dw)
+    d = _Device(s)
+    buf, n = (ws or Workspace(s.device)).get(workspace_bytes(OP_ADD_RMSNORM_BACKWARD, T, 1, 1, H))
+    d.call(name, py, dyt, ldy, ps, lds, ds, pt, weight.data_ptr(), _DTYPES[weight.dtype], gain_offset, pd, ldd, T, H, px, ldx,
+           pw, None if buf is None else buf.data_ptr(), n, d.stream)
+    return dx, dw
+
+
+def expert_counts(topk_idx, E: int, token_valid=None, counts=None, accumulate: bool = False):
+    """Routed pairs per expert (int32 [E], read as uint32) of topk_idx [T, k] over the tokens with token_valid (uint8 or
+    bool [T]) set.  With accumulate they are added to `counts`, which must then be given (micro-batches of one batch)."""
+    name = "moe_expert_counts"
+    _require(topk_idx.dim() == 2, name, "topk_idx must be [T, k]")
+    T, k = topk_idx.shape
+    pi = _array(name, "topk_idx", topk_idx, topk_idx.shape, torch.int32)
+    pv = _valid(name, token_valid, T)
+    _require(counts is not None or not accumulate, name, "accumulate needs counts")
+    if counts is None:
+        counts = torch.empty(E, dtype=torch.int32, device=topk_idx.device)
+    pc = _array(name, "counts", counts, (E,), torch.int32)
+    _same_device(name, topk_idx.device, token_valid, counts)
+    d = _Device(topk_idx)
+    d.call(name, pi, T, k, E, pv, int(accumulate), pc, d.stream)
+    return counts
+
+
+def _valid(name, token_valid, T):
+    if token_valid is not None and token_valid.dtype == torch.bool:
+        return _array(name, "token_valid", token_valid, (T,), torch.bool)
+    return _array(name, "token_valid", token_valid, (T,), torch.uint8)
+
+
+def balance_loss(logits, counts, k: int, coef: float, token_valid=None, topk_idx=None, gate=None, dgate=None, dlogits=None,
+                 want_dlogits: bool = True, ws=None):
+    """Balance loss of the router and the gradient of its logits [T, E] (bf16 or fp32, rows may be strided):
+    (loss fp32 [1], prob_sum fp32 [E], dlogits of logits' type unless given, or None without want_dlogits).
+
+      loss = coef E k / C * sum_e f_e S_e,  f = counts / C,  C = counts.sum(),  S_e = sum of softmax(logits)[:, e]
+
+    counts (int32 [E]) are those of this call (expert_counts), or of the larger batch that the loss is of: added over
+    micro-batches, all-reduced over ranks; loss and gradients are then this call's share.  With topk_idx, gate and
+    dgate ([T, k]) the gates' gradient is taken through their renormalised softmax into dlogits too, so that dlogits is
+    the whole gradient of the router's logits.  Without `ws` a workspace is allocated for the call."""
+    name = "moe_balance_loss"
+    pl, dl, ld = _matrix(name, "logits", logits)
+    T, E = logits.shape
+    dev = logits.device
+    if dlogits is None and want_dlogits:
+        dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    pd, dd, ldd = _matrix(name, "dlogits", dlogits, logits.shape)
+    pc = _array(name, "counts", counts, (E,), torch.int32, nullable=False)
+    pv = _valid(name, token_valid, T)
+    pi = _array(name, "topk_idx", topk_idx, (T, k), torch.int32)
+    pg = _array(name, "gate", gate, (T, k), torch.float32)
+    pg2 = _array(name, "dgate", dgate, (T, k), torch.float32)
+    _require((pi is None) == (pg is None) == (pg2 is None) or T == 0, name, "topk_idx, gate and dgate go together")
+    _same_device(name, dev, counts, token_valid, topk_idx, gate, dgate, dlogits)
+    d = _Device(logits)
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    prob_sum = torch.empty(E, dtype=torch.float32, device=dev)
+    buf, n = (ws or Workspace(dev)).get(workspace_bytes(OP_BALANCE_LOSS, T, k, E, 0))
+    d.call(name, pl, dl, ld, T, E, k, pc, coef, pv, pi, pg, pg2, loss.data_ptr(), prob_sum.data_ptr(), pd, dd, ldd,
+           None if buf is None else buf.data_ptr(), n, d.stream)
+    return loss, prob_sum, dlogits
+
+
+def awq_matmul(x, qweight, qzeros, scales, out_dtype=None, y=None, ws=None):
+    """y [M, N] = x [M, K] (bf16, rows may be strided) times one AWQ matrix in GEMM packing: qweight int32 [K, N/8],
+    qzeros int32 [K/group, N/8], scales fp16 [K/group, N], group 32, 64 or 128 (from the shapes); for few rows (up to
+    about 64; every 64 read the codes again).  The codes enter exactly, sums are fp32, rounded once to y's dtype, or
+    out_dtype (OUT_BF16 unless given).  Without `ws` a workspace is allocated for the call where one is needed."""
+    name = "moe_awq_matmul"
+    px, dt, ldx = _matrix(name, "x", x)
+    _require(dt == OUT_BF16, name, "x must be bf16")
+    M, K = x.shape
+    _require(qzeros.dim() == 2 and qzeros.shape[0] > 0 and K % qzeros.shape[0] == 0, name,
+             "qzeros must be [K/group, N/8]")
+    groups, n8 = qzeros.shape
+    N = 8 * n8
+    pq = _array(name, "qweight", qweight, (K, n8), torch.int32, nullable=False)
+    pz = _array(name, "qzeros", qzeros, (groups, n8), torch.int32)
+    psc = _array(name, "scales", scales, (groups, N), torch.float16, nullable=False)
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.float32 if out_dtype == OUT_F32 else torch.bfloat16, device=x.device)
+    py, yt, ldy = _matrix(name, "y", y, (M, N))
+    _require(out_dtype in (None, yt), name, "y must be of out_dtype")
+    _same_device(name, x.device, qweight, qzeros, scales, y)
+    d = _Device(x)
+    need = int(lib().moe_awq_matmul_workspace_bytes(M, N, K, K // groups))
+    buf, n = (ws or Workspace(x.device)).get(need) if need else (None, 0)
+    d.call(name, px, ldx, pq, pz, psc, M, N, K, K // groups, yt, py, ldy, None if buf is None else buf.data_ptr(), n, d.stream)
+    return y
 
 
 def router_norm_keep(w_router, keep: int):

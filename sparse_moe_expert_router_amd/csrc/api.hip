@@ -27,6 +27,40 @@ bool aligned16(const void* p) { return p == nullptr || ((uintptr_t)p % 16) == 0;
 
 constexpr int kMaxE = 1024;
 
+bool dtype_ok(int32_t d) { return d == MOE_OUT_BF16 || d == MOE_OUT_F32; }
+
+// The memory of a matrix (T rows of n elements, `stride` elements apart) or of
+// a contiguous array, for the checks of what may not overlap.
+struct Rows {
+    uintptr_t p;
+    size_t row, step, size;  // bytes of a row, from row to row, and in all (0: no memory)
+    size_t el;
+    Rows(const void* ptr, int64_t stride, int32_t dtype, int32_t T, int32_t n) : p((uintptr_t)ptr), el(dtype == MOE_OUT_F32 ? 4 : 2) {
+        row = (size_t)n * el;
+        step = (size_t)stride * el;
+        size = ptr && T > 0 ? (size_t)(T - 1) * step + row : 0;
+    }
+    Rows(const void* ptr, int64_t, size_t element, size_t count) : p((uintptr_t)ptr), el(element) {
+        row = step = size = ptr ? count * element : 0;
+    }
+    bool pieces() const { return size == 0 || step % 16 == 0; }  // rows of whole 16-byte pieces
+    bool same(const Rows& o) const { return p == o.p && step == o.step && row == o.row && el == o.el; }
+    // Whether the two share a byte.  Views of the same stride are told apart by
+    // their columns; ranges of other strides that cross count as shared.
+    bool meets(const Rows& o) const {
+        if (size == 0 || o.size == 0 || p + size <= o.p || o.p + o.size <= p) return false;
+        if (step != o.step || step == 0) return true;
+        const size_t d = (o.p >= p ? o.p - p : step - (p - o.p) % step) % step;
+        return !(d >= row && d + o.row <= step);
+    }
+};
+
+bool awq_sizes_ok(int32_t M, int32_t N, int32_t K, int32_t group) {
+    if (group != 32 && group != 64 && group != 128) return false;
+    if (N < 1 || K < 1 || N % 8 || K % group || N > (1 << 24) || K > (1 << 24) || M > (1 << 20)) return false;
+    return (int64_t)((N + 127) / 128) * ((M + 63) / 64) < (1 << 23);  // a launch has fewer than 2^32 threads
+}
+
 // Screened routing (approximate MFMA logits + exact recompute of candidates)
 // for batches of at least kFilterMinT tokens and E a multiple of 256;
 // otherwise every logit is computed exactly.
@@ -706,6 +740,144 @@ moe_status moe_grouped_ffn_a8(const uint16_t* x, int32_t T, int32_t k, const moe
     return hip_status(moe::launch_ffn_a8(f, ws, static_cast<hipStream_t>(stream)));
 }
 
+moe_status moe_add_rmsnorm(const void* x, int32_t x_dtype, int64_t x_stride, const void* residual, int64_t residual_stride,
+                           void* residual_out, int64_t residual_out_stride, int32_t res_dtype, const void* weight,
+                           int32_t w_dtype, float gain_offset, float eps, int32_t T, int32_t H, uint16_t* y,
+                           int64_t y_stride, uint8_t* codes, float* scales, float* rstd, void* stream) {
+    if (T < 0 || H < 1 || x_stride < H || (y && y_stride < H)) return MOE_ERR_SHAPE;
+    if ((residual && residual_stride < H) || (residual_out && residual_out_stride < H)) return MOE_ERR_SHAPE;
+    if (!(eps > 0.0f) || !(eps < 3.0e38f) || !(gain_offset - gain_offset == 0.0f)) return MOE_ERR_SHAPE;
+    if (!dtype_ok(x_dtype) || !dtype_ok(w_dtype) || ((residual || residual_out) && !dtype_ok(res_dtype)))
+        return MOE_ERR_UNSUPPORTED;
+    if (H % (codes ? 16 : 8) || H > moe::kNormMaxH) return MOE_ERR_UNSUPPORTED;
+    const Rows in_x(x, x_stride, x_dtype, T, H), in_r(residual, residual_stride, res_dtype, T, H);
+    const Rows out_r(residual_out, residual_out_stride, res_dtype, T, H), out_y(y, y_stride, MOE_OUT_BF16, T, H);
+    if (!in_x.pieces() || !in_r.pieces() || !out_r.pieces() || !out_y.pieces()) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (!x || !weight || (!residual) != (!residual_out) || (!codes) != (!scales) || (!y && !codes)) return MOE_ERR_NULL;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(residual_out) || !aligned16(weight) || !aligned16(y) ||
+        !aligned16(codes) || (uintptr_t)scales % 4 || (uintptr_t)rstd % 4)
+        return MOE_ERR_UNSUPPORTED;
+    const Rows out[5] = {out_r, out_y, Rows(codes, H, 1, (size_t)T * H),
+                         Rows(scales, 1, 4, codes ? (size_t)T * ((H + 127) / 128) : 0), Rows(rstd, 1, 4, (size_t)T)};
+    const Rows w(weight, 1, w_dtype == MOE_OUT_F32 ? 4 : 2, (size_t)H);
+    for (int i = 0; i < 5; ++i) {
+        if ((out[i].meets(in_x) && !out[i].same(in_x)) || (out[i].meets(in_r) && !out[i].same(in_r)) || out[i].meets(w))
+            return MOE_ERR_SHAPE;
+        for (int j = 0; j < i; ++j)
+            if (out[i].meets(out[j])) return MOE_ERR_SHAPE;
+    }
+    moe::NormArgs a{};
+    a.x = x; a.ldx = x_stride; a.x_f32 = x_dtype == MOE_OUT_F32;
+    a.res = residual; a.res_out = residual_out; a.ldr = residual_stride; a.ldro = residual_out_stride;
+    a.r_f32 = res_dtype == MOE_OUT_F32;
+    a.w = weight; a.w_f32 = w_dtype == MOE_OUT_F32; a.offset = gain_offset; a.eps = eps; a.T = T; a.H = H;
+    a.y = y; a.ldy = y_stride; a.codes = codes; a.scales = scales; a.rstd = rstd;
+    return hip_status(moe::launch_add_rmsnorm(a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_add_rmsnorm_backward(const void* dy, int32_t dy_dtype, int64_t dy_stride, const void* s, int64_t s_stride,
+                                    int32_t s_dtype, const float* rstd, const void* weight, int32_t w_dtype,
+                                    float gain_offset, const void* dres, int64_t dres_stride, int32_t T, int32_t H,
+                                    void* dx, int64_t dx_stride, float* dw, void* ws, size_t ws_bytes, void* stream) {
+    if (T < 0 || H < 1 || dy_stride < H || s_stride < H || dx_stride < H || (dres && dres_stride < H)) return MOE_ERR_SHAPE;
+    if (!(gain_offset - gain_offset == 0.0f)) return MOE_ERR_SHAPE;
+    if (!dtype_ok(dy_dtype) || !dtype_ok(s_dtype) || !dtype_ok(w_dtype)) return MOE_ERR_UNSUPPORTED;
+    if (H % 8 || H > moe::kNormMaxH) return MOE_ERR_UNSUPPORTED;
+    const Rows in[3] = {Rows(dy, dy_stride, dy_dtype, T, H), Rows(s, s_stride, s_dtype, T, H),
+                        Rows(dres, dres_stride, s_dtype, T, H)};
+    const Rows out(dx, dx_stride, s_dtype, T, H);
+    if (!in[0].pieces() || !in[1].pieces() || !in[2].pieces() || !out.pieces()) return MOE_ERR_UNSUPPORTED;
+    if (!dw) return MOE_ERR_NULL;
+    if ((uintptr_t)dw % 4) return MOE_ERR_UNSUPPORTED;
+    moe::NormBwdArgs a{};
+    if (T > 0) {
+        if (!dy || !s || !rstd || !weight || !dx) return MOE_ERR_NULL;
+        if (!aligned16(dy) || !aligned16(s) || !aligned16(dres) || !aligned16(weight) || !aligned16(dx) || (uintptr_t)rstd % 4)
+            return MOE_ERR_UNSUPPORTED;
+        const Rows more[2] = {Rows(rstd, 1, 4, (size_t)T), Rows(weight, 1, w_dtype == MOE_OUT_F32 ? 4 : 2, (size_t)H)};
+        const Rows sum(dw, 1, 4, (size_t)H);
+        for (const Rows& r : in)
+            if ((out.meets(r) && !out.same(r)) || sum.meets(r)) return MOE_ERR_SHAPE;
+        for (const Rows& r : more)
+            if (out.meets(r) || sum.meets(r)) return MOE_ERR_SHAPE;
+        if (out.meets(sum)) return MOE_ERR_SHAPE;
+        if (ws_bytes < moe::norm_bwd_ws_bytes(T, H)) return MOE_ERR_WORKSPACE;
+        if (!ws) return MOE_ERR_NULL;
+        if (!aligned16(ws)) return MOE_ERR_UNSUPPORTED;
+    }
+    a.dy = dy; a.ldy = dy_stride; a.y_f32 = dy_dtype == MOE_OUT_F32;
+    a.s = s; a.lds = s_stride; a.s_f32 = s_dtype == MOE_OUT_F32;
+    a.rstd = rstd; a.w = weight; a.w_f32 = w_dtype == MOE_OUT_F32; a.offset = gain_offset;
+    a.dres = dres; a.lddr = dres_stride; a.T = T; a.H = H; a.dx = dx; a.lddx = dx_stride; a.dw = dw;
+    return hip_status(moe::launch_add_rmsnorm_backward(a, ws, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_expert_counts(const int32_t* topk_idx, int32_t T, int32_t k, int32_t E, const uint8_t* token_valid,
+                             int32_t accumulate, uint32_t* counts, void* stream) {
+    if (T < 0 || E < 1 || k < 1 || k > E) return MOE_ERR_SHAPE;
+    if (E > kMaxE || (int64_t)T * k > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (T == 0 && accumulate) return MOE_OK;
+    if (!counts || (T > 0 && !topk_idx)) return MOE_ERR_NULL;
+    if ((uintptr_t)topk_idx % 4 || (uintptr_t)counts % 4) return MOE_ERR_UNSUPPORTED;
+    return hip_status(moe::launch_expert_counts(topk_idx, T, k, E, token_valid, accumulate != 0, counts,
+                                                static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_balance_loss(const void* logits, int32_t logits_dtype, int64_t logits_stride, int32_t T, int32_t E, int32_t k,
+                            const uint32_t* counts, float coef, const uint8_t* token_valid, const int32_t* topk_idx,
+                            const float* topk_gate, const float* dgate, float* loss, float* prob_sum, void* dlogits,
+                            int32_t dlogits_dtype, int64_t dlogits_stride, void* ws, size_t ws_bytes, void* stream) {
+    if (T < 0 || E < 1 || k < 1 || k > E || logits_stride < E || (dlogits && dlogits_stride < E)) return MOE_ERR_SHAPE;
+    if (!(coef - coef == 0.0f)) return MOE_ERR_SHAPE;
+    if (E > kMaxE || k > 64 || (int64_t)T * k > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (!dtype_ok(logits_dtype) || (dlogits && !dtype_ok(dlogits_dtype))) return MOE_ERR_UNSUPPORTED;
+    if (!counts || !loss) return MOE_ERR_NULL;
+    if ((uintptr_t)counts % 4 || (uintptr_t)loss % 4 || (uintptr_t)prob_sum % 4) return MOE_ERR_UNSUPPORTED;
+    moe::BalanceArgs a{};
+    if (T > 0) {
+        if (!logits) return MOE_ERR_NULL;
+        if ((!topk_idx) != (!dgate) || (!topk_gate) != (!dgate) || (dgate && !dlogits)) return MOE_ERR_NULL;
+        const size_t el = logits_dtype == MOE_OUT_F32 ? 4 : 2, dl = dlogits_dtype == MOE_OUT_F32 ? 4 : 2;
+        if ((uintptr_t)logits % el || (dlogits && (uintptr_t)dlogits % dl) || (uintptr_t)topk_idx % 4 ||
+            (uintptr_t)topk_gate % 4 || (uintptr_t)dgate % 4)
+            return MOE_ERR_UNSUPPORTED;
+        const Rows in(logits, logits_stride, logits_dtype, T, E), out(dlogits, dlogits_stride, dlogits_dtype, T, E);
+        if (out.meets(in) && !out.same(in)) return MOE_ERR_SHAPE;
+        if (ws_bytes < moe::balance_ws_bytes(T, k, E)) return MOE_ERR_WORKSPACE;
+        if (!ws) return MOE_ERR_NULL;
+        if (!aligned16(ws)) return MOE_ERR_UNSUPPORTED;
+    }
+    a.logits = logits; a.ld = logits_stride; a.in_f32 = logits_dtype == MOE_OUT_F32;
+    a.T = T; a.E = E; a.k = k; a.coef = coef; a.counts = counts; a.valid = token_valid;
+    a.idx = topk_idx; a.gate = topk_gate; a.dgate = dgate;
+    a.dlogits = dlogits; a.ldd = dlogits_stride; a.out_f32 = dlogits_dtype == MOE_OUT_F32;
+    return hip_status(moe::launch_balance_loss(a, loss, prob_sum, ws, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_awq_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t group) {
+    return M > 0 && awq_sizes_ok(M, N, K, group) ? moe::awq_matmul_ws_bytes(M, N, K, group) : 0;
+}
+
+moe_status moe_awq_matmul(const uint16_t* x, int64_t ldx, const int32_t* qweight, const int32_t* qzeros,
+                          const uint16_t* scales, int32_t M, int32_t N, int32_t K, int32_t group, int32_t out_dtype,
+                          void* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+    if (M < 0 || N < 1 || K < 1 || ldx < K || ldy < N) return MOE_ERR_SHAPE;
+    if (!dtype_ok(out_dtype) || ldx % 8 || !awq_sizes_ok(M, N, K, group)) return MOE_ERR_UNSUPPORTED;
+    if (M == 0) return MOE_OK;
+    if (!x || !qweight || !qzeros || !scales || !y) return MOE_ERR_NULL;
+    if (!aligned16(x) || !aligned16(scales) || (uintptr_t)qweight % 4 || (uintptr_t)qzeros % 4 ||
+        (uintptr_t)y % (out_dtype == MOE_OUT_F32 ? 4 : 2))
+        return MOE_ERR_UNSUPPORTED;
+    if (Rows(y, ldy, out_dtype, M, N).meets(Rows(x, ldx, MOE_OUT_BF16, M, K))) return MOE_ERR_SHAPE;
+    const size_t need = moe::awq_matmul_ws_bytes(M, N, K, group);
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+    if (need && !ws) return MOE_ERR_NULL;
+    if (need && !aligned16(ws)) return MOE_ERR_UNSUPPORTED;
+    return hip_status(moe::launch_awq_matmul(x, ldx, qweight, qzeros, scales, M, N, K, group, out_dtype == MOE_OUT_F32, y, ldy,
+                                             ws, static_cast<hipStream_t>(stream)));
+}
+
 size_t moe_workspace_bytes(int32_t op, int32_t T, int32_t k, int32_t E, int32_t H, int32_t F) {
     if (T <= 0 || k <= 0 || E <= 0) return 0;
     switch (op) {
@@ -716,6 +888,8 @@ size_t moe_workspace_bytes(int32_t op, int32_t T, int32_t k, int32_t E, int32_t 
         case MOE_OP_ROUTE_PERMUTE: return route_permute_ws(T, k, E, H);
         case MOE_OP_GROUPED_FFN_A8: return moe::ffn_a8_ws_bytes(T, k, E, H, F);
         case MOE_OP_REFILL_SCORE: return moe::refill_ws_bytes(T, k);
+        case MOE_OP_ADD_RMSNORM_BACKWARD: return H < 1 ? 0 : moe::norm_bwd_ws_bytes(T, H);
+        case MOE_OP_BALANCE_LOSS: return moe::balance_ws_bytes(T, k, E);
         default: return 0;
     }
 }

@@ -82,6 +82,74 @@ hipError_t launch_layer_few(const uint16_t* x, int T, const uint16_t* router, in
                             const moe_experts* sh, const float* shared_scale, uint16_t* y, int32_t* topk_idx, void* ws,
                             hipStream_t s);
 
+// ---- residual addition and norm, forward and backward (norm.hip)
+constexpr int kNormMaxH = 16384;
+struct NormArgs {
+    const void* x;         // [T][H], row stride ldx; *_f32: fp32, else bf16
+    int64_t ldx;
+    int x_f32;
+    const void* res;       // [T][H] or nullptr
+    void* res_out;
+    int64_t ldr, ldro;
+    int r_f32;
+    const void* w;         // [H]
+    int w_f32;
+    float offset, eps;
+    int T, H;
+    uint16_t* y;           // bf16 rows or nullptr
+    int64_t ldy;
+    uint8_t* codes;        // [T][H], with scales [T][ceil(H/128)], or nullptr
+    float* scales;
+    float* rstd;           // [T] or nullptr
+};
+hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s);
+struct NormBwdArgs {
+    const void* dy;        // [T][H]
+    int64_t ldy;
+    int y_f32;
+    const void* s;         // [T][H], and the type of dres and dx
+    int64_t lds;
+    int s_f32;
+    const float* rstd;     // [T]
+    const void* w;         // [H]
+    int w_f32;
+    float offset;
+    const void* dres;      // [T][H] or nullptr
+    int64_t lddr;
+    int T, H;
+    void* dx;              // [T][H]
+    int64_t lddx;
+    float* dw;             // [H]
+};
+size_t norm_bwd_ws_bytes(int T, int H);
+hipError_t launch_add_rmsnorm_backward(const NormBwdArgs& a, void* ws, hipStream_t s);
+
+// ---- counts, balance loss and the router's gradient (balance.hip)
+hipError_t launch_expert_counts(const int32_t* idx, int T, int k, int E, const uint8_t* valid, int accumulate, uint32_t* counts,
+                                hipStream_t s);
+struct BalanceArgs {
+    const void* logits;    // [T][E], row stride ld
+    int64_t ld;
+    int in_f32;
+    int T, E, k;
+    float coef;
+    const uint32_t* counts;  // [E]
+    const uint8_t* valid;    // [T] or nullptr
+    const int32_t* idx;      // [T][k] with gate and dgate, or all three nullptr
+    const float* gate;
+    const float* dgate;
+    void* dlogits;         // [T][E], row stride ldd, or nullptr
+    int64_t ldd;
+    int out_f32;
+};
+size_t balance_ws_bytes(int T, int k, int E);
+hipError_t launch_balance_loss(const BalanceArgs& a, float* loss, float* prob_sum, void* ws, hipStream_t s);
+
+// ---- product with one 4-bit matrix (awq_matmul.hip)
+size_t awq_matmul_ws_bytes(int M, int N, int K, int group);
+hipError_t launch_awq_matmul(const uint16_t* x, int64_t ldx, const int32_t* qweight, const int32_t* qzeros, const uint16_t* scales,
+                             int M, int N, int K, int group, int out_f32, void* y, int64_t ldy, void* ws, hipStream_t s);
+
 // ---- combine (combine.hip); pair_to_row == nullptr: row of pair p is p
 hipError_t launch_combine(const void* rows, int rows_f32, const int32_t* pair_to_row,
                           const float* gate, int T, int k, int H, const uint16_t* shared,
