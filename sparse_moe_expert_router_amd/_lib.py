@@ -692,7 +692,7 @@ def balance_loss(logits, counts, k: int, coef: float, token_valid=None, topk_idx
 def awq_matmul(x, qweight, qzeros, scales, out_dtype=None, y=None, ws=None):
     """y [M, N] = x [M, K] (bf16, rows may be strided) times one AWQ matrix in GEMM packing: qweight int32 [K, N/8],
     qzeros int32 [K/group, N/8], scales fp16 [K/group, N], group 32, 64 or 128 (from the shapes); for few rows (up to
-    about 64; every 64 read the codes again).  The codes enter exactly, sums are fp32, rounded once to y's dtype, or
+    about 64; every 32 read the codes again).  The codes enter exactly, sums are fp32, rounded once to y's dtype, or
     out_dtype (OUT_BF16 unless given).  Without `ws` a workspace is allocated for the call where one is needed."""
     name = "moe_awq_matmul"
     px, dt, ldx = _matrix(name, "x", x)

@@ -58,7 +58,7 @@ struct Rows {
 bool awq_sizes_ok(int32_t M, int32_t N, int32_t K, int32_t group) {
     if (group != 32 && group != 64 && group != 128) return false;
     if (N < 1 || K < 1 || N % 8 || K % group || N > (1 << 24) || K > (1 << 24) || M > (1 << 20)) return false;
-    return (int64_t)((N + 127) / 128) * ((M + 63) / 64) < (1 << 23);  // a launch has fewer than 2^32 threads
+    return (int64_t)((N + 127) / 128) * ((M + 31) / 32) < (1 << 23);  // a launch has fewer than 2^32 threads
 }
 
 // Screened routing (approximate MFMA logits + exact recompute of candidates)
@@ -856,21 +856,21 @@ moe_status moe_balance_loss(const void* logits, int32_t logits_dtype, int64_t lo
 }
 
 size_t moe_awq_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t group) {
-    return M > 0 && awq_sizes_ok(M, N, K, group) ? moe::awq_matmul_ws_bytes(M, N, K, group) : 0;
+    return M > 0 && awq_sizes_ok(M, N, K, group) ? moe::awq_matmul_ws_bytes(M, N, K) : 0;
 }
 
 moe_status moe_awq_matmul(const uint16_t* x, int64_t ldx, const int32_t* qweight, const int32_t* qzeros,
                           const uint16_t* scales, int32_t M, int32_t N, int32_t K, int32_t group, int32_t out_dtype,
                           void* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
     if (M < 0 || N < 1 || K < 1 || ldx < K || ldy < N) return MOE_ERR_SHAPE;
-    if (!dtype_ok(out_dtype) || ldx % 8 || !awq_sizes_ok(M, N, K, group)) return MOE_ERR_UNSUPPORTED;
+    if (!dtype_ok(out_dtype) || ldx % 8 || ldx > (1 << 24) || !awq_sizes_ok(M, N, K, group)) return MOE_ERR_UNSUPPORTED;
     if (M == 0) return MOE_OK;
     if (!x || !qweight || !qzeros || !scales || !y) return MOE_ERR_NULL;
     if (!aligned16(x) || !aligned16(scales) || (uintptr_t)qweight % 4 || (uintptr_t)qzeros % 4 ||
         (uintptr_t)y % (out_dtype == MOE_OUT_F32 ? 4 : 2))
         return MOE_ERR_UNSUPPORTED;
     if (Rows(y, ldy, out_dtype, M, N).meets(Rows(x, ldx, MOE_OUT_BF16, M, K))) return MOE_ERR_SHAPE;
-    const size_t need = moe::awq_matmul_ws_bytes(M, N, K, group);
+    const size_t need = moe::awq_matmul_ws_bytes(M, N, K);
     if (ws_bytes < need) return MOE_ERR_WORKSPACE;
     if (need && !ws) return MOE_ERR_NULL;
     if (need && !aligned16(ws)) return MOE_ERR_UNSUPPORTED;
