@@ -54,18 +54,6 @@ __global__ __launch_bounds__(1024) void count_kernel(const int32_t* __restrict__
 
 // ------------------------------------------------------------------ loss and gradient
 
-// e^x for x <= 0: 2^t with t = x log2(e) rounded to fp32, corrected by the
-// rounding's error (an fma gives it exactly) and by the part of log2(e) below
-// fp32; within 2 units in the last place where a bare 2^t is off by |x| / 2.
-// Gives 0 below about -87 and NaN for NaN.
-__device__ __forceinline__ float exp_neg(float x) {
-    const float kL = 1.44269502f, kLlo = 1.92596299e-8f;  // log2(e) = kL + kLlo
-    const float t = x * kL;
-    const float p = __builtin_amdgcn_exp2f(t);
-    const float c = fmaf(x, kLlo, fmaf(x, kL, -t));
-    return x < -104.0f ? 0.0f : fmaf(p * c, 0.693147182f, p);
-}
-
 // Sum and maximum over the kL lanes that hold a token.
 template <int kL>
 __device__ __forceinline__ float lanes_sum(float v) {
@@ -110,54 +98,93 @@ __device__ __forceinline__ void store_v(void* p, int64_t i, int f32, const float
 
 constexpr int kBalWaves = 8;
 
-// Workspace: partial sums of p [workgroups][E] fp32, then per workgroup the
-// sum of f' p over its tokens (fp64) and the number of tokens that count.
+// Workspace: partial sums of p [workgroups][E rounded up to 4] fp32, then per
+// workgroup the sum of f' p over its tokens and the number of tokens that count.
 struct BalancePart {
     double fp;
-    int64_t rows;
+    double rows;
 };
+__host__ __device__ __forceinline__ int bal_pitch(int E) { return (E + 3) / 4 * 4; }
 
-// Adds v to row[id]; the row is LDS of the token's own lanes.  Slots that name
-// the same expert add in the order of the slots.
-template <int kL>
+__device__ __forceinline__ void lds_settled() {  // LDS writes of a wave are seen by its later reads
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// row[id] = the sum of v over the token's slots that name id; row is LDS of the
+// token's own lanes, and slots that name the same expert add in their order.
 __device__ __forceinline__ void add_slots(float* row, int slot, int k, int id, float v) {
     // a lane's claim is its slot's number, and a lane that does not find its own
     // there shares its expert
-    const bool have = slot < k && id >= 0;
+    const bool have = id >= 0;
     if (have) row[id] = (float)slot;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    const bool shared = have && row[id] != (float)slot;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    const bool any = __any(shared);
+    lds_settled();
+    const bool any = __any(have && row[id] != (float)slot);
+    lds_settled();
     if (have) row[id] = any ? 0.0f : v;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    lds_settled();
     if (any) {
         for (int j = 0; j < k; ++j) {
             if (have && slot == j) row[id] += v;
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+            lds_settled();
         }
     }
 }
 
-template <int kL, int kV, int kI>
-__global__ __launch_bounds__(64 * kBalWaves) void balance_kernel(BalanceArgs a, float* __restrict__ part, BalancePart* __restrict__ tail) {
-    extern __shared__ __align__(16) float lds[];  // gates: one row of E values (rounded up to 4) per token in work; at the end the sums of p
+__device__ __forceinline__ float balance_value(double fp, double rows, double total, int E, int k, float coef) {
+    return total > 0.0 ? (float)((double)coef * E * k / total * (fp + rows / E)) : 0.0f;
+}
+
+// kGates: the gates' gradient is taken in.  prob_sum and loss are written here
+// when there is one workgroup, else the partial sums.
+template <int kL, int kV, int kI, bool kGates>
+__global__ __launch_bounds__(64 * kBalWaves) void balance_kernel(BalanceArgs a, float* __restrict__ part, BalancePart* __restrict__ tail,
+                                                                 float* __restrict__ prob_sum, float* __restrict__ loss) {
+    extern __shared__ __align__(16) float lds[];  // a row of E values (rounded up to 4) for each token in work
+    constexpr int kTeams = kBalWaves * 64 / kL;   // tokens in work at a time
     __shared__ unsigned long long total_s[kBalWaves];
-    __shared__ double fp_s[kBalWaves * 64 / kL];
-    __shared__ int64_t rows_s[kBalWaves * 64 / kL];
-    constexpr int kTeams = kBalWaves * 64 / kL;  // tokens in work at a time
+    __shared__ double fp_s[kTeams], rows_s[kTeams];
     const int t = threadIdx.x, l = t % kL, team = t / kL;
-    const int E = a.E;
+    const int E = a.E, pitch = bal_pitch(E);
+    float* row_lds = lds + team * pitch;
+
+    struct Token {
+        float v[kI][kV];
+        int id;
+        float g, dg;
+        bool on;
+    };
+    auto fetch = [&](int64_t row, Token& f) {
+        f.on = row < a.T && (!a.valid || a.valid[row]);
+#pragma unroll
+        for (int i = 0; i < kI; ++i) {
+            const int e = kV * (kL * i + l);
+#pragma unroll
+            for (int j = 0; j < kV; ++j) f.v[i][j] = -__builtin_inff();
+            if (f.on && e < E) load_v<kV>(a.logits, row * a.ld + e, a.in_f32, f.v[i]);
+        }
+        f.id = -1;
+        f.g = f.dg = 0.0f;
+        if (kGates && f.on && l < a.k) {
+            const int64_t p = row * a.k + l;
+            f.id = a.idx[p];
+            f.g = a.gate[p];
+            f.dg = a.dgate[p];
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * kTeams;
+    int64_t first = (int64_t)blockIdx.x * kTeams + t / 64 * (64 / kL);  // of the wave: its teams make the same rounds
+    const int off = kL == 64 ? 0 : t % 64 / kL;
+    Token next;
+    fetch(first + off, next);
 
     unsigned long long total = 0;
     for (int e = t; e < E; e += 64 * kBalWaves) total += a.counts[e];
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) total += __shfl_xor(total, m, kWave);
     if (t % 64 == 0) total_s[t / 64] = total;
+    if (kGates)
+        for (int e = l; e < pitch; e += kL) row_lds[e] = 0.0f;
     __syncthreads();
     total = 0;
 #pragma unroll
@@ -174,100 +201,68 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_kernel(BalanceArgs a, 
             f[i][j] = e < E ? (float)((double)((int64_t)a.counts[e] * E - (int64_t)total) * inv) : 0.0f;
             sum[i][j] = 0.0f;
         }
-    const int pitch = (E + 3) / 4 * 4;
-    float* row_lds = lds + team * pitch;
-    if (a.dgate) {
-        for (int e = l; e < pitch; e += kL) row_lds[e] = 0.0f;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-    }
 
     double fp = 0.0;
-    int64_t rows = 0;
-    const int64_t step = (int64_t)gridDim.x * kTeams;
-    // every team of a wave makes the same number of rounds
-    for (int64_t first = (int64_t)blockIdx.x * kTeams + t / 64 * (64 / kL); first < a.T; first += step) {
-        const int64_t row = first + (kL == 64 ? 0 : t % 64 / kL);
-        const bool live = row < a.T;
-        const bool on = live && (!a.valid || a.valid[row]);
-        float v[kI][kV];
+    int rows = 0;
+    for (; first < a.T; first += step) {
+        const int64_t row = first + off;
+        Token f0 = next;
+        if (first + step < a.T) fetch(row + step, next);
+        auto& v = f0.v;
         float m = -__builtin_inff();
 #pragma unroll
-        for (int i = 0; i < kI; ++i) {
-            const int e = kV * (kL * i + l);
-            if (on && e < E) {
-                load_v<kV>(a.logits, row * a.ld + e, a.in_f32, v[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kV; ++j) v[i][j] = -__builtin_inff();
-            }
+        for (int i = 0; i < kI; ++i)
 #pragma unroll
             for (int j = 0; j < kV; ++j) m = fmaxf(m, v[i][j]);
-        }
         m = lanes_max<kL>(m);
-        // no expert left (and nothing that is not a number): the token counts for nothing
-        float z = 0.0f;
+        if (m == -__builtin_inff()) m = 0.0f;  // no expert left: every exponential is 0 (NaN stay what they are)
+        float z = 0.0f, q = 0.0f;
 #pragma unroll
         for (int i = 0; i < kI; ++i)
 #pragma unroll
             for (int j = 0; j < kV; ++j) {
-                // v = m = -inf would give NaN; a NaN stays one
-                v[i][j] = v[i][j] == -__builtin_inff() ? 0.0f : exp_neg(v[i][j] - m);
+                v[i][j] = __builtin_amdgcn_exp2f((v[i][j] - m) * 1.44269504f);
                 z += v[i][j];
+                q = fmaf(f[i][j], v[i][j], q);
             }
         z = lanes_sum<kL>(z);
+        q = lanes_sum<kL>(q);
         const bool empty = z == 0.0f;
         const float rz = empty ? 0.0f : __fdiv_rn(1.0f, z);
-        float q = 0.0f;
+        q *= rz;
+        if (!empty) {
+            fp += (double)q;
+            rows += 1;
+        }
 #pragma unroll
         for (int i = 0; i < kI; ++i)
 #pragma unroll
             for (int j = 0; j < kV; ++j) {
                 v[i][j] *= rz;
                 sum[i][j] += v[i][j];
-                q = fmaf(f[i][j], v[i][j], q);
             }
-        q = lanes_sum<kL>(q);
-        if (!empty) {
-            fp += (double)q;
-            rows += 1;
-        }
         if (!a.dlogits) continue;
-        int id = -1;
-        if (a.dgate) {
-            const bool slot = on && l < a.k;
-            float g = 0.0f, dg = 0.0f;
-            if (slot) {
-                const int64_t p = row * a.k + l;
-                id = a.idx[p];
-                if ((uint32_t)id >= (uint32_t)E) id = -1;
-                g = a.gate[p];
-                dg = a.dgate[p];
-            }
-            const float mean = lanes_sum<kL>(g * dg);
-            add_slots<kL>(row_lds, l, a.k, id, g * (dg - mean));
+        if (kGates) {
+            if ((uint32_t)f0.id >= (uint32_t)E) f0.id = -1;
+            add_slots(row_lds, l, a.k, f0.id, f0.g * (f0.dg - lanes_sum<kL>(f0.g * f0.dg)));
         }
-        if (live) {
+        if (row < a.T) {
+            const float sq = scale * q;
 #pragma unroll
             for (int i = 0; i < kI; ++i) {
                 const int e = kV * (kL * i + l);
                 if (e < E) {
                     float d[kV];
 #pragma unroll
-                    for (int j = 0; j < kV; ++j) {
-                        d[j] = scale * v[i][j] * (f[i][j] - q);
-                        if (a.dgate) d[j] += row_lds[e + j];
-                    }
+                    for (int j = 0; j < kV; ++j) d[j] = fmaf(v[i][j], fmaf(scale, f[i][j], -sq), kGates ? row_lds[e + j] : 0.0f);
                     store_v<kV>(a.dlogits, row * a.ldd + e, a.out_f32, d);
                 }
             }
         }
-        if (a.dgate) {
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            if (id >= 0) row_lds[id] = 0.0f;
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+        if (kGates) {
+            lds_settled();
+            if (f0.id >= 0) row_lds[f0.id] = 0.0f;
+            lds_settled();
         }
     }
 
@@ -276,52 +271,52 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_kernel(BalanceArgs a, 
         fp_s[team] = fp;
         rows_s[team] = rows;
     }
-    __syncthreads();
 #pragma unroll
     for (int i = 0; i < kI; ++i)
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
             const int e = kV * (kL * i + l) + j;
-            if (e < E) row_lds[e] = sum[i][j];
+            if (e < pitch) row_lds[e] = sum[i][j];
         }
     __syncthreads();
-    for (int e = t; e < E; e += 64 * kBalWaves) {
+    const bool alone = gridDim.x == 1;
+    for (int e = t; e < pitch; e += 64 * kBalWaves) {
         float s = 0.0f;
+#pragma unroll
         for (int w = 0; w < kTeams; ++w) s += lds[w * pitch + e];
-        part[(size_t)blockIdx.x * E + e] = s;
+        if (!alone) part[(size_t)blockIdx.x * pitch + e] = s;
+        else if (prob_sum && e < E) prob_sum[e] = s;
     }
     if (t == 0) {
-        BalancePart b = {0.0, 0};
+        BalancePart b = {0.0, 0.0};
         for (int w = 0; w < kTeams; ++w) {
             b.fp += fp_s[w];
             b.rows += rows_s[w];
         }
-        tail[blockIdx.x] = b;
+        if (!alone) tail[blockIdx.x] = b;
+        else loss[0] = balance_value(b.fp, b.rows, (double)total, E, a.k, a.coef);
     }
 }
 
-// The partial sums of `parts` workgroups: 64 experts a workgroup, its 16 waves
-// each every sixteenth row, then the waves in turn; workgroup 0 adds the loss.
+// The partial sums of `parts` workgroups, in a fixed order: 32 experts (whole
+// lines) a workgroup; thread (p, q) adds rows p, p + 128, .. of experts 4q..4q+3,
+// eight loads on their way at a time, then the 128 sums are added in order of p
+// modulo 16.  Workgroup 0 adds the loss.
 __global__ __launch_bounds__(1024) void balance_sum_kernel(const float* __restrict__ part, const BalancePart* __restrict__ tail,
                                                            int parts, int E, int k, float coef, const uint32_t* __restrict__ counts,
                                                            float* __restrict__ prob_sum, float* __restrict__ loss) {
-    __shared__ float red[16][64];
-    __shared__ double fp_s[16];
-    __shared__ double rows_s[16];
-    __shared__ double total_s[16];
+    __shared__ __align__(16) f32x4_t red[128][8];
+    __shared__ double fp_s[16], rows_s[16], total_s[16];
     const int t = threadIdx.x, lane = t % 64, w = t / 64;
-    const int e = blockIdx.x * 64 + lane;
-    if (prob_sum) {
-        float v = 0.0f;
-        if (e < E)
-            for (int p = w; p < parts; p += 16) v += part[(size_t)p * E + e];
-        red[w][lane] = v;
-    }
+    const int q = t % 8, p0 = t / 8, pitch = bal_pitch(E), e = blockIdx.x * 32 + 4 * q;
+    f32x4_t v = f32x4_t(0.0f);
+    if (prob_sum && e < pitch) v = sum_rows(part + e, parts, pitch, p0);
+    red[p0][q] = v;
     if (blockIdx.x == 0) {
         double fp = 0.0, rows = 0.0, total = 0.0;
         for (int p = t; p < parts; p += 1024) {
             fp += tail[p].fp;
-            rows += (double)tail[p].rows;
+            rows += tail[p].rows;
         }
         for (int i = t; i < E; i += 1024) total += (double)counts[i];
         fp = wave_sum_f64(fp);
@@ -334,11 +329,11 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(const float* __restri
         }
     }
     __syncthreads();
-    if (prob_sum && w == 0 && e < E) {
-        float s = 0.0f;
+    v = sum_128(v, red, p0, q);
+    if (prob_sum && p0 == 0) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s += red[i][lane];
-        prob_sum[e] = s;
+        for (int j = 0; j < 4; ++j)
+            if (e + j < E) prob_sum[e + j] = v[j];
     }
     if (blockIdx.x == 0 && t == 0) {
         double fp = 0.0, rows = 0.0, total = 0.0;
@@ -347,26 +342,26 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(const float* __restri
             rows += rows_s[i];
             total += total_s[i];
         }
-        loss[0] = total > 0.0 ? (float)((double)coef * E * k / total * (fp + rows / E)) : 0.0f;
+        loss[0] = balance_value(fp, rows, total, E, k, coef);
     }
 }
 
 namespace {
-
-size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 
 int bal_lanes(int E, int k) { return E <= 64 && k <= 16 ? 16 : 64; }
 
 int bal_grid(int T, int E, int k) {
     const int teams = kBalWaves * 64 / bal_lanes(E, k);
     const int need = (int)(((int64_t)T + teams - 1) / teams);
-    return need < 1024 ? need : 1024;
+    return need < 512 ? need : 512;
 }
 
 template <int kL, int kV, int kI>
-hipError_t run_balance(const BalanceArgs& a, float* part, BalancePart* tail, int grid, hipStream_t s) {
-    const size_t lds = (size_t)(kBalWaves * 64 / kL) * ((a.E + 3) / 4 * 4) * sizeof(float);
-    hipLaunchKernelGGL((balance_kernel<kL, kV, kI>), dim3(grid), dim3(64 * kBalWaves), lds, s, a, part, tail);
+hipError_t run_balance(const BalanceArgs& a, float* part, BalancePart* tail, float* prob_sum, float* loss, int grid, hipStream_t s) {
+    const size_t lds = (size_t)(kBalWaves * 64 / kL) * bal_pitch(a.E) * sizeof(float);
+    const dim3 g(grid), b(64 * kBalWaves);
+    if (a.dgate) hipLaunchKernelGGL((balance_kernel<kL, kV, kI, true>), g, b, lds, s, a, part, tail, prob_sum, loss);
+    else hipLaunchKernelGGL((balance_kernel<kL, kV, kI, false>), g, b, lds, s, a, part, tail, prob_sum, loss);
     return hipGetLastError();
 }
 
@@ -395,31 +390,31 @@ hipError_t launch_expert_counts(const int32_t* idx, int T, int k, int E, const u
 
 size_t balance_ws_bytes(int T, int k, int E) {
     const int grid = bal_grid(T, E, k);
-    return align16((size_t)grid * E * sizeof(float)) + (size_t)grid * sizeof(BalancePart);
+    return (size_t)grid * (bal_pitch(E) * sizeof(float) + sizeof(BalancePart));
 }
 
 hipError_t launch_balance_loss(const BalanceArgs& a, float* loss, float* prob_sum, void* ws, hipStream_t s) {
     const int grid = a.T ? bal_grid(a.T, a.E, a.k) : 0;
     float* part = static_cast<float*>(ws);
-    BalancePart* tail = reinterpret_cast<BalancePart*>(static_cast<char*>(ws) + align16((size_t)grid * a.E * sizeof(float)));
+    BalancePart* tail = reinterpret_cast<BalancePart*>(part + (size_t)grid * bal_pitch(a.E));
     if (grid) {
         const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && (uintptr_t)a.logits % (a.in_f32 ? 16 : 8) == 0 &&
                          (!a.dlogits || (a.ldd % 4 == 0 && (uintptr_t)a.dlogits % (a.out_f32 ? 16 : 8) == 0));
         hipError_t e;
+#define MOE_BALANCE(kL, kV, kI) run_balance<kL, kV, kI>(a, part, tail, prob_sum, loss, grid, s)
         if (bal_lanes(a.E, a.k) == 16)
-            e = vec ? run_balance<16, 4, 1>(a, part, tail, grid, s) : run_balance<16, 1, 4>(a, part, tail, grid, s);
+            e = vec ? MOE_BALANCE(16, 4, 1) : MOE_BALANCE(16, 1, 4);
         else if (vec)
-            e = a.E <= 256   ? run_balance<64, 4, 1>(a, part, tail, grid, s)
-                : a.E <= 512 ? run_balance<64, 4, 2>(a, part, tail, grid, s)
-                             : run_balance<64, 4, 4>(a, part, tail, grid, s);
+            e = a.E <= 256 ? MOE_BALANCE(64, 4, 1) : a.E <= 512 ? MOE_BALANCE(64, 4, 2) : MOE_BALANCE(64, 4, 4);
         else
-            e = a.E <= 128   ? run_balance<64, 1, 2>(a, part, tail, grid, s)
-                : a.E <= 256 ? run_balance<64, 1, 4>(a, part, tail, grid, s)
-                : a.E <= 512 ? run_balance<64, 1, 8>(a, part, tail, grid, s)
-                             : run_balance<64, 1, 16>(a, part, tail, grid, s);
-        if (e != hipSuccess) return e;
+            e = a.E <= 128   ? MOE_BALANCE(64, 1, 2)
+                : a.E <= 256 ? MOE_BALANCE(64, 1, 4)
+                : a.E <= 512 ? MOE_BALANCE(64, 1, 8)
+                             : MOE_BALANCE(64, 1, 16);
+#undef MOE_BALANCE
+        if (e != hipSuccess || grid == 1) return e;
     }
-    hipLaunchKernelGGL(balance_sum_kernel, dim3((a.E + 63) / 64), dim3(1024), 0, s, part, tail, grid, a.E, a.k, a.coef, a.counts,
+    hipLaunchKernelGGL(balance_sum_kernel, dim3((a.E + 31) / 32), dim3(1024), 0, s, part, tail, grid, a.E, a.k, a.coef, a.counts,
                        prob_sum, loss);
     return hipGetLastError();
 }

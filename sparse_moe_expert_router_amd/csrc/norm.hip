@@ -12,7 +12,9 @@
 // neighbouring values (16 or 32 bytes), piece c of thread t being values
 // 8 (c n + t) .. +7 of the row for n threads, so a group of 128 values lies in
 // 16 neighbouring lanes.  A workgroup of as few waves as the row needs takes
-// one row after another.
+// one row after another; short rows take 16 lanes.  (32768 x 2560, residual and
+// codes: 107 us, 5.5 TB/s; the gradients 125 us, 5.4 TB/s; a large copy runs
+// at 5.2.)
 #include "fp8.h"
 #include "kernels.h"
 #include "rows.h"
@@ -39,53 +41,112 @@ __device__ __forceinline__ uint32_t max16_u32(uint32_t v) {
     return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));  // row_mirror
 }
 
-template <int C>
+// A row's threads: the workgroup (kL = 64), or 16 lanes (kL = 16, for rows of up
+// to 256 values) with 16 rows to a workgroup.
+constexpr int kRowsOf16 = 16;  // rows of a workgroup with kL = 16
+template <int kL>
+struct Team {
+    int n, t, team, teams;  // threads of a row, this one among them; rows in work, this one among them
+    __device__ __forceinline__ Team() {
+        n = kL == 16 ? 16 : blockDim.x;
+        t = kL == 16 ? threadIdx.x % 16 : threadIdx.x;
+        team = kL == 16 ? threadIdx.x / 16 : 0;
+        teams = kL == 16 ? kRowsOf16 : 1;
+    }
+    __device__ __forceinline__ float sum(float v, float* red) const {
+        return kL == 16 ? sum16_f32(v) : row_sum(v, red, n / kWave);
+    }
+};
+
+// Eight values as they lie in memory: a row's loads are all issued before the
+// first is converted (with the types known at run time only they are not: 32768 x
+// 2560 to codes 107 -> 126 us).
+template <bool kF32>
+struct Raw8 {
+    uint4 v[kF32 ? 2 : 1];
+};
+template <bool kF32>
+__device__ __forceinline__ Raw8<kF32> raw8(const void* p, int64_t i) {
+    Raw8<kF32> r;
+    if constexpr (kF32) {
+        const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+        r.v[0] = s[0];
+        r.v[1] = s[1];
+    } else {
+        r.v[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    }
+    return r;
+}
+template <bool kF32>
+__device__ __forceinline__ f32x8_t values(const Raw8<kF32>& r) {
+    return load8(r.v, 0, kF32);
+}
+
+// kX: x is fp32; kR: 0 no residual, 1 bf16, 2 fp32.  The next row's loads are on
+// their way while a row is summed and written.
+template <int kL, int C, bool kX, int kR>
 __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
     __shared__ float red[2][kMaxWaves];
-    const int n = blockDim.x, waves = n / kWave, t = threadIdx.x;
-    const int nb = fp8_blocks(a.H);
-    bool in[C];
+    const Team<kL> m;
+    const int n = m.n, t = m.t, nb = fp8_blocks(a.H);
+    const int64_t step = (int64_t)gridDim.x * m.teams;
+    struct Row {
+        Raw8<kX> x[C];
+        Raw8<kR == 2> r[C];
+    } cur, next;
+    auto fetch = [&](int64_t row, Row& f) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int i = 8 * (c * n + t);
+            if (i >= a.H || row >= a.T) continue;
+            f.x[c] = raw8<kX>(a.x, row * a.ldx + i);
+            if constexpr (kR != 0) f.r[c] = raw8<kR == 2>(a.res, row * a.ldr + i);
+        }
+    };
+    int64_t first = (int64_t)blockIdx.x * m.teams;
+    fetch(first + m.team, cur);
     f32x8_t gain[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int i = 8 * (c * n + t);
-        in[c] = i < a.H;
-        gain[c] = in[c] ? load8(a.w, i, a.w_f32) + a.offset : f32x8_t(0.0f);
-    }
+    for (int c = 0; c < C; ++c) gain[c] = 8 * (c * n + t) < a.H ? load8(a.w, 8 * (c * n + t), a.w_f32) : f32x8_t(0.0f);
     int flip = 0;
-    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, flip ^= 1) {
+    // (the lanes of a wave stay together: rows past the last one are empty)
+    for (; first < a.T; first += step, flip ^= 1) {
+        const int64_t row = first + m.team;
+        if (first + step < a.T) fetch(row + step, next);
+        bool in[C];
         f32x8_t s[C];
         float sq = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int i = 8 * (c * n + t);
+            in[c] = i < a.H && row < a.T;
             s[c] = f32x8_t(0.0f);
             if (in[c]) {
-                s[c] = load8(a.x, row * a.ldx + i, a.x_f32);
-                if (a.res) {
-                    s[c] += load8(a.res, row * a.ldr + i, a.r_f32);
-                    if (!a.r_f32) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) s[c][j] = bf16_to_f32(f32_to_bf16_bits(s[c][j]));
+                s[c] = values(cur.x[c]);
+                if constexpr (kR != 0) {
+                    s[c] += values(cur.r[c]);
+                    if constexpr (kR == 1) {
+                        const uint4 q = pack8(s[c]);
+                        s[c] = load8(&q, 0, 0);
                     }
-                    store8(a.res_out, row * a.ldro + i, a.r_f32, s[c]);
+                    store8(a.res_out, row * a.ldro + i, kR == 2, s[c]);
                 }
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) sq = fmaf(s[c][j], s[c][j], sq);
         }
-        const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(row_sum(sq, red[flip], waves), (float)a.H) + a.eps));
-        if (a.rstd && t == 0) a.rstd[row] = r;
+        const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(m.sum(sq, red[flip]), (float)a.H) + a.eps));
+        if (a.rstd && t == 0 && row < a.T) a.rstd[row] = r;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int i = 8 * (c * n + t);
-            const f32x8_t v = s[c] * r * gain[c];
+            const f32x8_t v = s[c] * r * (gain[c] + a.offset);
             if (a.y && in[c]) store8(a.y, row * a.ldy + i, 0, v);
             if (a.codes) {
-                uint32_t m = 0;
+                uint32_t top = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
-                const float sc = fp8_scale(max16_u32(m));
+                for (int j = 0; j < 8; ++j) top = max(top, in[c] ? abs_bits(v[j]) : 0u);
+                const float sc = fp8_scale(max16_u32(top));
                 const Fp8Div d = fp8_div(in[c] ? sc : 1.0f);
                 if (in[c]) {
                     const uint2 q = make_uint2(fp8_pack4(v[0], v[1], v[2], v[3], d), fp8_pack4(v[4], v[5], v[6], v[7], d));
@@ -94,116 +155,199 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
                 }
             }
         }
+        cur = next;
     }
 }
 
-template <int C>
-__global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs a, float* __restrict__ part) {
+// kY: dy is fp32; kS: s, dres and dx are.  `part` gets one row of sums of dy h
+// from each workgroup.
+template <int kL, int C, bool kY, bool kS>
+__global__ __launch_bounds__(kL == 16 ? 16 * kRowsOf16 : 1024) void norm_bwd_kernel(NormBwdArgs a, float* __restrict__ part) {
     __shared__ float red[2][kMaxWaves];
-    const int n = blockDim.x, waves = n / kWave, t = threadIdx.x;
-    bool in[C];
+    constexpr bool kEarly = C == 1 || !kS;  // dres is loaded with the rest (two fp32 pieces would not fit the registers)
+    const Team<kL> m;
+    const int n = m.n, t = m.t;
     f32x8_t gain[C], dw[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int i = 8 * (c * n + t);
-        in[c] = i < a.H;
-        gain[c] = in[c] ? load8(a.w, i, a.w_f32) + a.offset : f32x8_t(0.0f);
+        gain[c] = i < a.H ? load8(a.w, i, a.w_f32) + a.offset : f32x8_t(0.0f);
         dw[c] = f32x8_t(0.0f);
     }
     int flip = 0;
-    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, flip ^= 1) {
-        const float r = a.rstd[row];
+    for (int64_t first = (int64_t)blockIdx.x * m.teams; first < a.T; first += (int64_t)gridDim.x * m.teams, flip ^= 1) {
+        const int64_t row = first + m.team;
+        const float r = row < a.T ? a.rstd[row] : 0.0f;
+        bool in[C];
+        Raw8<kS> rs[C], rd[C];
+        Raw8<kY> ry[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int i = 8 * (c * n + t);
+            in[c] = i < a.H && row < a.T;
+            if (!in[c]) continue;
+            rs[c] = raw8<kS>(a.s, row * a.lds + i);
+            ry[c] = raw8<kY>(a.dy, row * a.ldy + i);
+            if (kEarly && a.dres) rd[c] = raw8<kS>(a.dres, row * a.lddr + i);
+        }
         f32x8_t h[C], u[C];
         float dot = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int i = 8 * (c * n + t);
             h[c] = u[c] = f32x8_t(0.0f);
             if (in[c]) {
-                h[c] = load8(a.s, row * a.lds + i, a.s_f32) * r;
-                const f32x8_t dy = load8(a.dy, row * a.ldy + i, a.y_f32);
+                h[c] = values(rs[c]) * r;
+                const f32x8_t dy = values(ry[c]);
                 dw[c] += dy * h[c];
                 u[c] = dy * gain[c];
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) dot = fmaf(u[c][j], h[c][j], dot);
         }
-        const float mean = __fdiv_rn(row_sum(dot, red[flip], waves), (float)a.H);
+        const float mean = __fdiv_rn(m.sum(dot, red[flip]), (float)a.H);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int i = 8 * (c * n + t);
             if (!in[c]) continue;
             f32x8_t d = (u[c] - h[c] * mean) * r;
-            if (a.dres) d += load8(a.dres, row * a.lddr + i, a.s_f32);
-            store8(a.dx, row * a.lddx + i, a.s_f32, d);
+            if (a.dres) d += values(kEarly ? rd[c] : raw8<kS>(a.dres, row * a.lddr + i));
+            store8(a.dx, row * a.lddx + i, kS, d);
         }
+    }
+    if constexpr (kL == 16) {
+        // the workgroup's 16 rows of sums, in order
+        __shared__ __align__(16) f32x8_t sums[C][kRowsOf16][16];
+#pragma unroll
+        for (int c = 0; c < C; ++c) sums[c][m.team][t] = dw[c];
+        __syncthreads();
+        if (m.team != 0) return;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            for (int i = 1; i < kRowsOf16; ++i) dw[c] += sums[c][i][t];
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int i = 8 * (c * n + t);
-        if (in[c]) store8(part, (int64_t)blockIdx.x * a.H + i, 1, dw[c]);
+        if (i < a.H) store8(part, (int64_t)blockIdx.x * a.H + i, 1, dw[c]);
     }
 }
 
-// dw [H] = sum of the `parts` partial rows, in a fixed order: 64 columns a
-// workgroup, its 16 waves each every sixteenth row, then the waves in turn.
+// dw [H] = sum of the `parts` partial rows: 32 columns (whole lines) a workgroup.
 __global__ __launch_bounds__(1024) void norm_dw_kernel(const float* __restrict__ part, int parts, int H, float* __restrict__ dw) {
-    __shared__ float red[16][64];
-    const int lane = threadIdx.x % 64, w = threadIdx.x / 64;
-    const int col = blockIdx.x * 64 + lane;
-    float v = 0.0f;
-    if (col < H)
-        for (int p = w; p < parts; p += 16) v += part[(size_t)p * H + col];
-    red[w][lane] = v;
+    __shared__ __align__(16) f32x4_t red[128][8];
+    const int q = threadIdx.x % 8, p0 = threadIdx.x / 8;
+    const int col = blockIdx.x * 32 + 4 * q;
+    f32x4_t v = col < H ? sum_rows(part + col, parts, H, p0) : f32x4_t(0.0f);
+    red[p0][q] = v;
     __syncthreads();
-    if (w == 0 && col < H) {
-        float s = 0.0f;
+    v = sum_128(v, red, p0, q);
+    if (p0 == 0 && col < H) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s += red[i][lane];
-        dw[col] = s;
+        for (int j = 0; j < 4; ++j) dw[col + j] = v[j];  // (dw has no more than its element's alignment)
     }
 }
 
 namespace {
 
-// Pieces a thread for a row of H values: one while 16 waves hold the row so, else two (kNormMaxH values).
-int pieces(int H) { return H <= 8 * 64 * kMaxWaves ? 1 : 2; }
-int waves_for(int H, int c) { return (H + 512 * c - 1) / (512 * c); }
+struct Plan {
+    int lanes, c, block, grid;
+};
 
-// Workgroups: each compute unit holds 32 waves at most, two rounds of them.
-int norm_grid(int T, int waves) {
-    const int most = 256 * (32 / waves) * 2;
-    return T < most ? T : most;
+// Rows of up to 256 values take 16 lanes (32768 x 64: 8.6 -> 4.6 us).  Longer ones take whole waves, with c pieces a
+// thread: two where 16 waves of one would not do, or as asked.
+Plan shape(int H, bool two) {
+    Plan p;
+    p.lanes = H <= 256 ? 16 : 64;
+    p.c = p.lanes == 16 ? (H <= 128 ? 1 : 2) : two || H > 8 * 64 * kMaxWaves ? 2 : 1;
+    p.block = p.lanes == 16 ? 16 * kRowsOf16 : (H + 512 * p.c - 1) / (512 * p.c) * 64;
+    p.grid = 0;
+    return p;
 }
-int bwd_grid(int T, int H) {
-    const int most = 256 * (16 / waves_for(H, pieces(H)) + 1);
-    return T < most ? T : most;
+int workgroups(const Plan& p, int T, int most) {
+    const int rows = p.lanes == 16 ? kRowsOf16 : 1, need = (int)(((int64_t)T + rows - 1) / rows);
+    return need < most ? need : most;
+}
+
+// Many rows take two pieces a thread (32768 x 2560 to codes: 110 -> 107 us; one row 2.7 against 2.9), and up to eight
+// rounds of the workgroups that the card holds (two rounds 116).
+Plan norm_plan(int T, int H) {
+    Plan p = shape(H, T >= 8192);
+    p.grid = workgroups(p, T, 256 * (2048 / p.block) * 8);
+    return p;
+}
+
+// Each workgroup writes one partial row of dw, so there are no more than keep the memory busy, about ten waves a
+// compute unit (32768 x 2560: 512 workgroups 125 us, 1024 154; 32768 x 640: 512 85, 1280 53, 1536 53).
+Plan bwd_plan(int T, int H) {
+    Plan p = shape(H, false);
+    const int waves = p.block / 64;
+    p.grid = workgroups(p, T, 256 * ((10 + waves - 1) / waves));
+    return p;
+}
+
+template <int kL, int C>
+void run_norm(const NormArgs& a, const Plan& p, hipStream_t s) {
+    const dim3 grid(p.grid), block(p.block);
+#define MOE_NORM(kX, kR) hipLaunchKernelGGL((norm_kernel<kL, C, kX, kR>), grid, block, 0, s, a)
+    if (a.x_f32) {
+        if (!a.res) MOE_NORM(true, 0);
+        else if (a.r_f32) MOE_NORM(true, 2);
+        else MOE_NORM(true, 1);
+    } else {
+        if (!a.res) MOE_NORM(false, 0);
+        else if (a.r_f32) MOE_NORM(false, 2);
+        else MOE_NORM(false, 1);
+    }
+#undef MOE_NORM
+}
+
+template <int kL, int C>
+void run_norm_bwd(const NormBwdArgs& a, const Plan& p, float* part, hipStream_t s) {
+    const dim3 grid(p.grid), block(p.block);
+#define MOE_NORM_BWD(kY, kS) hipLaunchKernelGGL((norm_bwd_kernel<kL, C, kY, kS>), grid, block, 0, s, a, part)
+    if (a.y_f32) {
+        if (a.s_f32) MOE_NORM_BWD(true, true);
+        else MOE_NORM_BWD(true, false);
+    } else {
+        if (a.s_f32) MOE_NORM_BWD(false, true);
+        else MOE_NORM_BWD(false, false);
+    }
+#undef MOE_NORM_BWD
 }
 
 }  // namespace
 
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s) {
-    const int c = pieces(a.H), w = waves_for(a.H, c);
-    const dim3 grid(norm_grid(a.T, w)), block(64 * w);
-    if (c == 1) hipLaunchKernelGGL((norm_kernel<1>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((norm_kernel<2>), grid, block, 0, s, a);
+    const Plan p = norm_plan(a.T, a.H);
+    if (p.lanes == 16) {
+        if (p.c == 1) run_norm<16, 1>(a, p, s);
+        else run_norm<16, 2>(a, p, s);
+    } else {
+        if (p.c == 1) run_norm<64, 1>(a, p, s);
+        else run_norm<64, 2>(a, p, s);
+    }
     return hipGetLastError();
 }
 
-size_t norm_bwd_ws_bytes(int T, int H) { return (size_t)bwd_grid(T, H) * H * sizeof(float); }
+size_t norm_bwd_ws_bytes(int T, int H) { return (size_t)bwd_plan(T, H).grid * H * sizeof(float); }
 
 hipError_t launch_add_rmsnorm_backward(const NormBwdArgs& a, void* ws, hipStream_t s) {
-    const int c = pieces(a.H), w = waves_for(a.H, c);
-    const int parts = a.T ? bwd_grid(a.T, a.H) : 0;
     float* part = static_cast<float*>(ws);
-    if (parts) {
-        const dim3 grid(parts), block(64 * w);
-        if (c == 1) hipLaunchKernelGGL((norm_bwd_kernel<1>), grid, block, 0, s, a, part);
-        else hipLaunchKernelGGL((norm_bwd_kernel<2>), grid, block, 0, s, a, part);
+    int parts = 0;
+    if (a.T) {
+        const Plan p = bwd_plan(a.T, a.H);
+        parts = p.grid;
+        if (p.lanes == 16) {
+            if (p.c == 1) run_norm_bwd<16, 1>(a, p, part, s);
+            else run_norm_bwd<16, 2>(a, p, part, s);
+        } else {
+            if (p.c == 1) run_norm_bwd<64, 1>(a, p, part, s);
+            else run_norm_bwd<64, 2>(a, p, part, s);
+        }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(norm_dw_kernel, dim3((a.H + 63) / 64), dim3(1024), 0, s, part, parts, a.H, a.dw);
+    hipLaunchKernelGGL(norm_dw_kernel, dim3((a.H + 31) / 32), dim3(1024), 0, s, part, parts, a.H, a.dw);
     return hipGetLastError();
 }
 
