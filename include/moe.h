@@ -602,7 +602,8 @@ moe_status moe_awq_matmul(const uint16_t *x, int64_t ldx, const int32_t *qweight
                           const uint16_t *scales, int32_t M, int32_t N, int32_t K, int32_t group, int32_t out_dtype,
                           void *y, int64_t ldy, void *ws, size_t ws_bytes, void *stream);
 
-/* Workspace bytes of moe_awq_matmul (0 when none is needed, or for sizes it refuses). */
+/* Workspace bytes of moe_awq_matmul (0 when none is needed, or for sizes it
+ * refuses); one for the largest M of a run serves every smaller call. */
 size_t moe_awq_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t group);
 
 /* Scratch bytes an operation needs (0 when none).  For MOE_OP_GROUPED_FFN,

@@ -165,9 +165,11 @@ class _Device:
         self.stream = torch._C._cuda_getCurrentRawStream(self.index)
 
     def call(self, name, *args):
-        f = getattr(lib(), name)
-        if self.index == torch.cuda.current_device():
-            _check(name, f(*args))
+        f = getattr(_lib or lib(), name)
+        if self.index == torch._C._cuda_getDevice():  # (a tensor on it exists, so the runtime is up)
+            status = f(*args)
+            if status:
+                _check(name, status)
         else:
             with torch.cuda.device(self.index):
                 _check(name, f(*args))
@@ -527,25 +529,39 @@ def awq_to_output_major(bank: dict) -> dict:
 _DTYPES = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
 
 
+# The checks of the calls below are on the way of every single-token step: a call
+# costs the host 4 us in the library, and its checks should not cost twice that.
+
 def _matrix(name, what, t, shape=None, dtype=None):
     """(pointer, dtype code, row stride) of a bf16 or fp32 matrix with contiguous rows; (None, 0, 0) for None."""
     if t is None:
         return None, OUT_BF16, 0
-    code = _DTYPES.get(t.dtype)
-    if code is None or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    dt, sh = t.dtype, t.shape
+    code = _DTYPES.get(dt)
+    if code is None or len(sh) != 2:
         raise MoeError(f"{name}: {what} must be a bf16 or fp32 matrix with contiguous rows")
-    if (shape is not None and t.shape != shape) or (dtype is not None and t.dtype != dtype):
+    if (shape is not None and sh != shape) or (dtype is not None and dt is not dtype):
         raise MoeError(f"{name}: {what} must be {dtype or 'bf16 or fp32'} {list(shape)}")
-    return t.data_ptr(), code, t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    step, one = t.stride()
+    if one != 1 and sh[1] > 1:
+        raise MoeError(f"{name}: {what} must be a bf16 or fp32 matrix with contiguous rows")
+    return t.data_ptr(), code, step if sh[0] > 1 else max(sh[1], 1)
 
 
 def _array(name, what, t, shape, dtype, nullable=True):
     """Pointer of a contiguous tensor of the given shape and dtype, or None."""
     if t is None and nullable:
         return None
-    if t is None or t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+    if t is None or t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         raise MoeError(f"{name}: {what} must be contiguous {dtype} {list(shape)}")
     return t.data_ptr()
+
+
+def _on(name, device, *tensors):
+    """Refuses tensors (or None) that are not on `device`."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise MoeError(f"{name}: tensors on different devices")
 
 
 class NormResult(NamedTuple):
@@ -569,37 +585,46 @@ def add_rmsnorm(x, weight, residual=None, eps: float = 1e-6, gain_offset: float 
     may not."""
     name = "moe_add_rmsnorm"
     px, dx, ldx = _matrix(name, "x", x)
-    T, H = x.shape
-    dev = x.device
+    shape, dev = x.shape, x.device
+    T, H = shape
     fp8 = codes is not None or scales is not None
     if outputs is None:
         outputs = () if fp8 or y is not None else ("y",)
-    _require(all(o in ("y", "fp8", "rstd") for o in outputs), name, "outputs are among y, fp8 and rstd")
-    fp8, want_y = fp8 or "fp8" in outputs, y is not None or "y" in outputs
-    _require(weight.dtype in _DTYPES and weight.shape == (H,) and weight.is_contiguous(), name,
+    for o in outputs:
+        if o == "y":
+            if y is None:
+                y = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        elif o == "fp8":
+            fp8 = True
+        elif o == "rstd":
+            if rstd is None:
+                rstd = torch.empty(T, dtype=torch.float32, device=dev)
+        else:
+            raise MoeError(f"{name}: outputs are among y, fp8 and rstd")
+    wt = _DTYPES.get(weight.dtype)
+    _require(wt is not None and weight.shape == shape[1:] and weight.is_contiguous(), name,
              "weight must be contiguous bf16 or fp32 [H]")
-    if want_y and y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    if fp8 and codes is None:
-        codes = torch.empty((T, H), dtype=torch.uint8, device=dev)
-    if fp8 and scales is None:
-        scales = torch.empty((T, -(-H // 128)), dtype=torch.float32, device=dev)
-    if rstd is None and "rstd" in outputs:
-        rstd = torch.empty(T, dtype=torch.float32, device=dev)
-    pr, dr, ldr = _matrix(name, "residual", residual, x.shape)
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty((T, H), dtype=residual.dtype, device=dev)
-    _require(residual is not None or residual_out is None, name, "residual_out without a residual")
-    po, _, ldo = _matrix(name, "residual_out", residual_out, x.shape, residual.dtype if residual is not None else None)
-    py, _, ldy = _matrix(name, "y", y, x.shape, torch.bfloat16)
-    pc = _array(name, "codes", codes, x.shape, torch.uint8)
-    ps = _array(name, "scales", scales, (T, -(-H // 128)), torch.float32)
-    pt = _array(name, "rstd", rstd, (T,), torch.float32)
+    pr, dr, ldr, po, ldo, pc, ps = None, OUT_BF16, 0, None, 0, None, None
+    if residual is not None:
+        pr, dr, ldr = _matrix(name, "residual", residual, shape)
+        if residual_out is None:
+            residual_out = torch.empty(shape, dtype=residual.dtype, device=dev)
+        po, _, ldo = _matrix(name, "residual_out", residual_out, shape, residual.dtype)
+    elif residual_out is not None:
+        raise MoeError(f"{name}: residual_out without a residual")
+    if fp8:
+        if codes is None:
+            codes = torch.empty(shape, dtype=torch.uint8, device=dev)
+        if scales is None:
+            scales = torch.empty((T, -(-H // 128)), dtype=torch.float32, device=dev)
+        pc = _array(name, "codes", codes, shape, torch.uint8)
+        ps = _array(name, "scales", scales, (T, -(-H // 128)), torch.float32)
+    py, _, ldy = _matrix(name, "y", y, shape, torch.bfloat16)
+    pt = _array(name, "rstd", rstd, shape[:1], torch.float32)
     _require(T == 0 or py is not None or pc is not None, name, "outputs must name y or fp8")
-    _same_device(name, dev, weight, residual, residual_out, y, codes, scales, rstd)
+    _on(name, dev, weight, residual, residual_out, y, codes, scales, rstd)
     d = _Device(x)
-    d.call(name, px, dx, ldx, pr, ldr, po, ldo, dr, weight.data_ptr(), _DTYPES[weight.dtype], gain_offset, eps, T, H, py, ldy,
-           pc, ps, pt, d.stream)
+    d.call(name, px, dx, ldx, pr, ldr, po, ldo, dr, weight.data_ptr(), wt, gain_offset, eps, T, H, py, ldy, pc, ps, pt, d.stream)
     return NormResult(y, residual_out, codes, scales, rstd)
 
 
@@ -623,7 +648,7 @@ def add_rmsnorm_backward(dy, s, rstd, weight, gain_offset: float = 1.0, dres=Non
     pt = _array(name, "rstd", rstd, (T,), torch.float32, nullable=False)
     _require(weight.dtype in _DTYPES and weight.shape == (H,) and weight.is_contiguous(), name,
              "weight must be contiguous bf16 or fp32 [H]")
-    _same_device(name, s.device, dy, rstd, weight, dres, dx, dw)
+    _on(name, s.device, dy, rstd, weight, dres, dx, dw)
     d = _Device(s)
     buf, n = (ws or Workspace(s.device)).get(workspace_bytes(OP_ADD_RMSNORM_BACKWARD, T, 1, 1, H))
     d.call(name, py, dyt, ldy, ps, lds, ds, pt, weight.data_ptr(), _DTYPES[weight.dtype], gain_offset, pd, ldd, T, H, px, ldx,
@@ -635,15 +660,16 @@ def expert_counts(topk_idx, E: int, token_valid=None, counts=None, accumulate: b
     """Routed pairs per expert (int32 [E], read as uint32) of topk_idx [T, k] over the tokens with token_valid (uint8 or
     bool [T]) set.  With accumulate they are added to `counts`, which must then be given (micro-batches of one batch)."""
     name = "moe_expert_counts"
-    _require(topk_idx.dim() == 2, name, "topk_idx must be [T, k]")
-    T, k = topk_idx.shape
-    pi = _array(name, "topk_idx", topk_idx, topk_idx.shape, torch.int32)
-    pv = _valid(name, token_valid, T)
+    shape = topk_idx.shape
+    _require(len(shape) == 2, name, "topk_idx must be [T, k]")
+    T, k = shape
+    pi = _array(name, "topk_idx", topk_idx, shape, torch.int32)
+    pv = _valid(name, token_valid, T) if token_valid is not None else None
     _require(counts is not None or not accumulate, name, "accumulate needs counts")
     if counts is None:
         counts = torch.empty(E, dtype=torch.int32, device=topk_idx.device)
     pc = _array(name, "counts", counts, (E,), torch.int32)
-    _same_device(name, topk_idx.device, token_valid, counts)
+    _on(name, topk_idx.device, token_valid, counts)
     d = _Device(topk_idx)
     d.call(name, pi, T, k, E, pv, int(accumulate), pc, d.stream)
     return counts
@@ -668,23 +694,26 @@ def balance_loss(logits, counts, k: int, coef: float, token_valid=None, topk_idx
     the whole gradient of the router's logits.  Without `ws` a workspace is allocated for the call."""
     name = "moe_balance_loss"
     pl, dl, ld = _matrix(name, "logits", logits)
-    T, E = logits.shape
-    dev = logits.device
+    shape, dev = logits.shape, logits.device
+    T, E = shape
     if dlogits is None and want_dlogits:
-        dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    pd, dd, ldd = _matrix(name, "dlogits", dlogits, logits.shape)
+        dlogits = torch.empty(shape, dtype=logits.dtype, device=dev)
+    pd, dd, ldd = _matrix(name, "dlogits", dlogits, shape)
     pc = _array(name, "counts", counts, (E,), torch.int32, nullable=False)
-    pv = _valid(name, token_valid, T)
-    pi = _array(name, "topk_idx", topk_idx, (T, k), torch.int32)
-    pg = _array(name, "gate", gate, (T, k), torch.float32)
-    pg2 = _array(name, "dgate", dgate, (T, k), torch.float32)
-    _require((pi is None) == (pg is None) == (pg2 is None) or T == 0, name, "topk_idx, gate and dgate go together")
-    _same_device(name, dev, counts, token_valid, topk_idx, gate, dgate, dlogits)
+    pv = _valid(name, token_valid, T) if token_valid is not None else None
+    pi = pg = pdg = None
+    if topk_idx is not None or gate is not None or dgate is not None:
+        _require(topk_idx is not None and gate is not None and dgate is not None, name,
+                 "topk_idx, gate and dgate go together")
+        pi = _array(name, "topk_idx", topk_idx, (T, k), torch.int32)
+        pg = _array(name, "gate", gate, (T, k), torch.float32)
+        pdg = _array(name, "dgate", dgate, (T, k), torch.float32)
+    _on(name, dev, counts, token_valid, topk_idx, gate, dgate, dlogits)
     d = _Device(logits)
     loss = torch.empty(1, dtype=torch.float32, device=dev)
     prob_sum = torch.empty(E, dtype=torch.float32, device=dev)
     buf, n = (ws or Workspace(dev)).get(workspace_bytes(OP_BALANCE_LOSS, T, k, E, 0))
-    d.call(name, pl, dl, ld, T, E, k, pc, coef, pv, pi, pg, pg2, loss.data_ptr(), prob_sum.data_ptr(), pd, dd, ldd,
+    d.call(name, pl, dl, ld, T, E, k, pc, coef, pv, pi, pg, pdg, loss.data_ptr(), prob_sum.data_ptr(), pd, dd, ldd,
            None if buf is None else buf.data_ptr(), n, d.stream)
     return loss, prob_sum, dlogits
 
@@ -709,7 +738,7 @@ def awq_matmul(x, qweight, qzeros, scales, out_dtype=None, y=None, ws=None):
         y = torch.empty((M, N), dtype=torch.float32 if out_dtype == OUT_F32 else torch.bfloat16, device=x.device)
     py, yt, ldy = _matrix(name, "y", y, (M, N))
     _require(out_dtype in (None, yt), name, "y must be of out_dtype")
-    _same_device(name, x.device, qweight, qzeros, scales, y)
+    _on(name, x.device, qweight, qzeros, scales, y)
     d = _Device(x)
     need = int(lib().moe_awq_matmul_workspace_bytes(M, N, K, K // groups))
     buf, n = (ws or Workspace(x.device)).get(need) if need else (None, 0)

@@ -870,7 +870,7 @@ moe_status moe_awq_matmul(const uint16_t* x, int64_t ldx, const int32_t* qweight
         (uintptr_t)y % (out_dtype == MOE_OUT_F32 ? 4 : 2))
         return MOE_ERR_UNSUPPORTED;
     if (Rows(y, ldy, out_dtype, M, N).meets(Rows(x, ldx, MOE_OUT_BF16, M, K))) return MOE_ERR_SHAPE;
-    const size_t need = moe::awq_matmul_ws_bytes(M, N, K);
+    const size_t need = moe::awq_matmul_needs(M, N, K);
     if (ws_bytes < need) return MOE_ERR_WORKSPACE;
     if (need && !ws) return MOE_ERR_NULL;
     if (need && !aligned16(ws)) return MOE_ERR_UNSUPPORTED;

@@ -115,7 +115,8 @@ __device__ __forceinline__ Run run_of(const Awq& a, int wave, int waves) {
 // a lane has two neighbouring words (and the 16 lanes read whole 128-byte
 // lines), with 8 one word, with 4 or 2 a half or a byte of a word that two or
 // four lanes read.  Tiles that share lines run on one XCD (its workgroups are
-// every eighth), so that a line is fetched once.
+// every eighth), so that a line is fetched once; whole lines are spread over
+// the XCDs (1 x 16384 x 16384: 32 us against 36).
 template <int CW>
 struct Lane {
     static constexpr int kW = CW > 8 ? CW / 8 : 1;      // words of a lane
@@ -129,8 +130,14 @@ template <int CW>
 __device__ __forceinline__ Lane<CW> lane_of(int n16, uint32_t n8, int tiles) {
     typedef Lane<CW> L;
     L l;
-    const int xcd = blockIdx.x % 8, from = (int)((int64_t)tiles * xcd / 8), to = (int)((int64_t)tiles * (xcd + 1) / 8);
-    l.tile = from + (int)(blockIdx.x / 8);
+    int to = tiles;
+    if (CW == 16) {
+        l.tile = blockIdx.x;
+    } else {
+        const int xcd = blockIdx.x % 8, from = (int)((int64_t)tiles * xcd / 8);
+        to = (int)((int64_t)tiles * (xcd + 1) / 8);
+        l.tile = from + (int)(blockIdx.x / 8);
+    }
     if (l.tile >= to) {
         l.tile = -1;
         return l;
@@ -232,15 +239,17 @@ __global__ __launch_bounds__(64 * WV) void awq_few_kernel(Awq a) {
     const uint32_t xoff = n16 / 4 == kq && n16 % 4 < a.M ? (uint32_t)(n16 % 4) * (uint32_t)a.ldx * 2 + 64u * kq : kOutside;
 
     // Steps 2h and 2h + 1 of four sets: 16 inputs of each set.  What lies behind
-    // the last set is not read, and a set past the run's end meets zeros of x.
+    // the last set is not read, nor is anything for sets past the run's end; a set
+    // past the run's end beside others meets zeros of x.
     struct Half {
         u32x4_t x[2];
         Words<W> w[2][8];
     };
     auto fetch = [&](int set, int h, Half& f) {
-        const int left = sets - set < 4 ? sets - set : 4;
-        const __amdgpu_buffer_rsrc_t xb = buffer(a.x + (int64_t)set * 32, (uint32_t)(a.M - 1) * (uint32_t)a.ldx * 2 + (uint32_t)left * 64u);
-        const __amdgpu_buffer_rsrc_t q = buffer(a.qw + (int64_t)set * 32 * n8, (uint32_t)left * 128u * n8);
+        const int left = set >= r.end ? 0 : sets - set < 4 ? sets - set : 4;
+        const int64_t at = set < r.end ? set : r.first;
+        const __amdgpu_buffer_rsrc_t xb = buffer(a.x + at * 32, left ? (uint32_t)(a.M - 1) * (uint32_t)a.ldx * 2 + (uint32_t)left * 64u : 0u);
+        const __amdgpu_buffer_rsrc_t q = buffer(a.qw + at * 32 * n8, (uint32_t)left * 128u * n8);
         const uint32_t xo = kq < r.end - set ? xoff : kOutside;
 #pragma unroll
         for (int u = 0; u < 2; ++u) f.x[u] = load16(xb, xo, 16u * (2 * h + u));
@@ -285,7 +294,7 @@ __global__ __launch_bounds__(64 * WV) void awq_few_kernel(Awq a) {
             __builtin_amdgcn_sched_barrier(0);
             add(f0, true);
             __builtin_amdgcn_sched_barrier(0);
-            fetch(set + 4 < r.end ? set + 4 : set, 0, f0);
+            fetch(set + 4, 0, f0);
             __builtin_amdgcn_sched_barrier(0);
             add(f1, false);
 #pragma unroll
@@ -353,13 +362,14 @@ __global__ __launch_bounds__(64 * WV) void awq_rows_kernel(Awq a) {
         Words<W> w[8];
     };
     auto fetch = [&](int set, Step& st) {
-        const __amdgpu_buffer_rsrc_t q = buffer(a.qw + (int64_t)set * 32 * n8, 128u * n8);
-        const __amdgpu_buffer_rsrc_t xb = buffer(x0 + (int64_t)set * 32, xbytes);
-        const int64_t g = set >> a.gshift;
+        const bool in = set < r.end;  // (past the run's end nothing is read)
+        const int64_t at = in ? set : r.first, g = at >> a.gshift;
+        const __amdgpu_buffer_rsrc_t q = buffer(a.qw + at * 32 * n8, in ? 128u * n8 : 0u);
+        const __amdgpu_buffer_rsrc_t xb = buffer(x0 + at * 32, in ? xbytes : 0u);
 #pragma unroll
         for (int t = 0; t < MT; ++t) st.x[t] = load16(xb, xoff[t], 0);
-        st.z = load_zeros<W>(buffer(a.qz + g * n8, 4u * n8), 4u * wl);
-        st.s = load_scales<CW>(buffer(a.sc + g * n8 * 8, 16u * n8), wl, l.h);
+        st.z = load_zeros<W>(buffer(a.qz + g * n8, in ? 4u * n8 : 0u), 4u * wl);
+        st.s = load_scales<CW>(buffer(a.sc + g * n8 * 8, in ? 16u * n8 : 0u), wl, l.h);
 #pragma unroll
         for (int i = 0; i < 8; ++i) st.w[i] = load_words<W>(q, woff[i], 0);
     };
@@ -407,11 +417,11 @@ __global__ __launch_bounds__(64 * WV) void awq_rows_kernel(Awq a) {
         fetch(r.first, s0);
         for (int s = r.first; s < r.end; s += 2) {
             __builtin_amdgcn_sched_barrier(0);
-            fetch(s + 1 < r.end ? s + 1 : s, s1);
+            fetch(s + 1, s1);
             __builtin_amdgcn_sched_barrier(0);
             add(s0);
             __builtin_amdgcn_sched_barrier(0);
-            fetch(s + 2 < r.end ? s + 2 : s, s0);
+            fetch(s + 2, s0);
             __builtin_amdgcn_sched_barrier(0);
             if (s + 1 < r.end) add(s1);
         }
@@ -508,12 +518,26 @@ void run_awq(const Awq& a, const Plan& p, hipStream_t s) {
 
 }  // namespace
 
-size_t awq_matmul_ws_bytes(int M, int N, int K) {
+// Bytes of the partial sums of M rows.
+static size_t part_bytes(int M, int N, int K) {
     // whether pairs of words are aligned is known with the pointers only
     const int s = plan(M, N, K, N % 16 == 0).splits, t = plan(M, N, K, false).splits;
     const int most = s > t ? s : t;
     return most > 1 ? (size_t)most * M * N * sizeof(float) : 0;
 }
+
+size_t awq_matmul_ws_bytes(int M, int N, int K) {
+    // the most that any smaller M needs: the splits fall where M takes another kernel or row of tiles
+    size_t most = part_bytes(M, N, K);
+    const int tops[2] = {4, 16};
+    for (int m : tops)
+        if (m < M && part_bytes(m, N, K) > most) most = part_bytes(m, N, K);
+    for (int m = 32; m < M && m <= 32 * 256; m += 32)  // (256 workgroups are never split)
+        if (part_bytes(m, N, K) > most) most = part_bytes(m, N, K);
+    return most;
+}
+
+size_t awq_matmul_needs(int M, int N, int K) { return part_bytes(M, N, K); }
 
 hipError_t launch_awq_matmul(const uint16_t* x, int64_t ldx, const int32_t* qweight, const int32_t* qzeros, const uint16_t* scales,
                              int M, int N, int K, int group, int out_f32, void* y, int64_t ldy, void* ws, hipStream_t s) {

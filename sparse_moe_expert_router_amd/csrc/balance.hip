@@ -31,19 +31,26 @@ __global__ __launch_bounds__(256) void count_clear_kernel(uint32_t* __restrict__
     if (e < E) counts[e] = 0;
 }
 
-// Pairs [first, first + step) of each workgroup, counted in LDS and then added
-// to `counts` (one workgroup and kWrite: written).  Integer additions: the
-// order does not matter.  Ids outside [0, E) are not counted.
+// A workgroup's pairs, counted in LDS and then added to `counts` (one workgroup
+// and kWrite: written).  Integer additions: the order does not matter.  Ids
+// outside [0, E) are not counted.  Eight loads are on their way at a time.
 template <bool kWrite>
-__global__ __launch_bounds__(1024) void count_kernel(const int32_t* __restrict__ idx, int64_t pairs, int k, int E,
+__global__ __launch_bounds__(1024) void count_kernel(const int32_t* __restrict__ idx, uint32_t pairs, uint32_t k, int E,
                                                      const uint8_t* __restrict__ valid, uint32_t* __restrict__ counts) {
     __shared__ uint32_t bins[1024];
     for (int e = threadIdx.x; e < E; e += 1024) bins[e] = 0;
     __syncthreads();
-    for (int64_t p = (int64_t)blockIdx.x * 1024 + threadIdx.x; p < pairs; p += (int64_t)gridDim.x * 1024) {
-        if (valid && !valid[p / k]) continue;
-        const uint32_t e = (uint32_t)idx[p];
-        if (e < (uint32_t)E) atomicAdd(&bins[e], 1u);
+    const uint32_t step = gridDim.x * 1024u;
+    for (uint64_t p0 = blockIdx.x * 1024u + threadIdx.x; p0 < pairs; p0 += 8ull * step) {
+        uint32_t e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint64_t p = p0 + (uint64_t)i * step;
+            e[i] = p < pairs && (!valid || valid[(uint32_t)p / k]) ? (uint32_t)idx[p] : ~0u;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (e[i] < (uint32_t)E) atomicAdd(&bins[e[i]], 1u);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += 1024) {
@@ -348,12 +355,14 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(const float* __restri
 
 namespace {
 
+constexpr uint32_t kCountAlone = 8192;
+
 int bal_lanes(int E, int k) { return E <= 64 && k <= 16 ? 16 : 64; }
 
 int bal_grid(int T, int E, int k) {
     const int teams = kBalWaves * 64 / bal_lanes(E, k);
     const int need = (int)(((int64_t)T + teams - 1) / teams);
-    return need < 512 ? need : 512;
+    return need <= 4 ? 1 : need < 512 ? need : 512;  // a few rounds of one workgroup cost less than the sums' kernel
 }
 
 template <int kL, int kV, int kI>
@@ -369,13 +378,13 @@ hipError_t run_balance(const BalanceArgs& a, float* part, BalancePart* tail, flo
 
 hipError_t launch_expert_counts(const int32_t* idx, int T, int k, int E, const uint8_t* valid, int accumulate, uint32_t* counts,
                                 hipStream_t s) {
-    const int64_t pairs = (int64_t)T * k;
-    const int64_t need = (pairs + 4095) / 4096;
-    if (need <= 1) {
-        if (accumulate)
-            hipLaunchKernelGGL((count_kernel<false>), dim3(1), dim3(1024), 0, s, idx, pairs, k, E, valid, counts);
-        else
-            hipLaunchKernelGGL((count_kernel<true>), dim3(1), dim3(1024), 0, s, idx, pairs, k, E, valid, counts);
+    const uint32_t pairs = (uint32_t)T * (uint32_t)k;  // (fits 31 bits)
+    // one workgroup while that is no slower than a second launch (its LDS counters
+    // collide: 49152 pairs of 61 experts take it 22 us); more than 64 meet at the same counters
+    const uint32_t need = pairs <= kCountAlone ? 1 : (pairs + 4095) / 4096;
+    const dim3 grid(need < 64 ? need : 64), block(1024);
+    if (grid.x == 1 && !accumulate) {
+        hipLaunchKernelGGL((count_kernel<true>), grid, block, 0, s, idx, pairs, (uint32_t)k, E, valid, counts);
         return hipGetLastError();
     }
     if (!accumulate) {
@@ -383,8 +392,7 @@ hipError_t launch_expert_counts(const int32_t* idx, int T, int k, int E, const u
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const int grid = (int)(need < 256 ? need : 256);
-    hipLaunchKernelGGL((count_kernel<false>), dim3(grid), dim3(1024), 0, s, idx, pairs, k, E, valid, counts);
+    hipLaunchKernelGGL((count_kernel<false>), grid, block, 0, s, idx, pairs, (uint32_t)k, E, valid, counts);
     return hipGetLastError();
 }
 

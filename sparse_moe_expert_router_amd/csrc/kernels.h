@@ -146,7 +146,8 @@ size_t balance_ws_bytes(int T, int k, int E);
 hipError_t launch_balance_loss(const BalanceArgs& a, float* loss, float* prob_sum, void* ws, hipStream_t s);
 
 // ---- product with one 4-bit matrix (awq_matmul.hip)
-size_t awq_matmul_ws_bytes(int M, int N, int K);
+size_t awq_matmul_ws_bytes(int M, int N, int K);  // serves every smaller M too
+size_t awq_matmul_needs(int M, int N, int K);
 hipError_t launch_awq_matmul(const uint16_t* x, int64_t ldx, const int32_t* qweight, const int32_t* qzeros, const uint16_t* scales,
                              int M, int N, int K, int group, int out_f32, void* y, int64_t ldy, void* ws, hipStream_t s);
 

@@ -74,7 +74,7 @@ def test_norm_backward_refusals():
         assert _bwd(**{p: ctypes.c_void_p((1 << 40) + 8)}) == UNSUP
     assert _bwd(r=ctypes.c_void_p((1 << 40) + 2)) == UNSUP and _bwd(dw=ctypes.c_void_p((1 << 40) + 2)) == UNSUP
     need = moe.workspace_bytes(moe.OP_ADD_RMSNORM_BACKWARD, 4, 1, 1, 256)
-    assert need >= 4 * 256 * 4 and _bwd(n=need - 1) == WS
+    assert need > 0 and _bwd(n=need - 1) == WS
     at = lambda p, n: ctypes.c_void_p(p.value + n)
     assert _bwd(dx=Y, yd=F32) == SHAPE and _bwd(dx=at(X, 512)) == SHAPE and _bwd(dx=at(RES, 16)) == SHAPE
     assert _bwd(dw=X) == SHAPE and _bwd(dw=RSTD) == SHAPE and _bwd(dw=DX) == SHAPE and _bwd(dx=W) == SHAPE
@@ -140,6 +140,9 @@ def test_awq_refusals():
     if need:
         big = dict(M=1, N=8192, K=8192, g=128, ldx=8192, ldy=8192)
         assert mm(n=need - 1, **big) == WS and mm(ws=None, **big) == NULL and mm(ws=ctypes.c_void_p((1 << 40) + 8), **big) == UNSUP
+    for N, K in ((8192, 8192), (264, 8192), (16384, 4096), (2560, 16384)):      # one for the largest M serves the smaller
+        sizes = [moe.lib().moe_awq_matmul_workspace_bytes(M, N, K, 32) for M in (1, 2, 4, 5, 16, 17, 32, 33, 40, 64, 65, 300, 5000)]
+        assert sizes == sorted(sizes)
     for bad in ((0, 64, 64, 32), (4, 60, 64, 32), (4, 64, 48, 32), (4, 64, 64, 0), (-1, 0, 0, 0), (4, 1 << 30, 64, 32)):
         assert moe.lib().moe_awq_matmul_workspace_bytes(*bad) == 0
 
