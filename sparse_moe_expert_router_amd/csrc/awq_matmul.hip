@@ -80,19 +80,33 @@ __device__ __forceinline__ Halves halves(const uint32_t* w, uint32_t select) {
     }
     return v;
 }
+// Masks and constants of the two conversions.  As literals they would cost an
+// instruction each (v_and_or_b32 takes none), so a mask is kept in a vector and a
+// constant in a scalar register, out of the compiler's sight.  The instruction
+// itself is the compiler's: an MFMA has to wait two states for an operand that
+// a vector instruction writes, and inside inline assembly it would not see that
+// one does (and_or there gave wrong columns).
+struct Bits {
+    uint32_t mq, cq, mz, cz;
+    __device__ __forceinline__ Bits() : mq(0x00780078u), cq(0x41804180u), mz(0x00780000u), cz(0x41800000u) {
+        asm("" : "+v"(mq), "+v"(mz));
+        asm("" : "+s"(cq), "+s"(cz));
+    }
+};
+
 // 16 + q of nibble j, 8 inputs.
-__device__ __forceinline__ bf16x8_t column(const Halves& v, int j) {
+__device__ __forceinline__ bf16x8_t column(const Halves& v, int j, const Bits& k) {
     uint32_t b[4];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
         const uint32_t h = j < 4 ? v.lo[p] : v.hi[p];
-        b[p] = and_or(j % 4 == 0 ? h << 3 : h >> (4 * (j % 4) - 3), 0x00780078u, 0x41804180u);
+        b[p] = ((j % 4 == 0 ? h << 3 : h >> (4 * (j % 4) - 3)) & k.mq) | k.cq;
     }
     return __builtin_bit_cast(bf16x8_t, make_uint4(b[0], b[1], b[2], b[3]));
 }
 // 16 + z of nibble j.
-__device__ __forceinline__ float zero_point(uint32_t z, int j) {
-    return __uint_as_float(and_or(j < 5 ? z << (19 - 4 * j) : z >> (4 * j - 19), 0x00780000u, 0x41800000u));
+__device__ __forceinline__ float zero_point(uint32_t z, int j, const Bits& k) {
+    return __uint_as_float(((j < 5 ? z << (19 - 4 * j) : z >> (4 * j - 19)) & k.mz) | k.cz);
 }
 __device__ __forceinline__ f32x4_t mfma(u32x4_t x, bf16x8_t b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x), b, c, 0, 0, 0);
@@ -259,6 +273,7 @@ __global__ __launch_bounds__(64 * WV) void awq_few_kernel(Awq a) {
             for (int i = 0; i < 8; ++i) f.w[u][i] = load_words<W>(q, woff[i], 32u * (2 * h + u) * n8);
     };
     const f32x4_t none = f32x4_t(0.0f);
+    const Bits bits;
     f32x4_t d[CW], sx;
     auto add = [&](const Half& f, bool begin) {
 #pragma unroll
@@ -271,7 +286,7 @@ __global__ __launch_bounds__(64 * WV) void awq_few_kernel(Awq a) {
                 for (int i = 0; i < 8; ++i) w[i] = f.w[u][i].v[v];
                 const Halves h = halves(w, l.select);
 #pragma unroll
-                for (int j = 0; j < CW / W; ++j) d[8 * v + j] = mfma(f.x[u], column(h, j), begin && u == 0 ? none : d[8 * v + j]);
+                for (int j = 0; j < CW / W; ++j) d[8 * v + j] = mfma(f.x[u], column(h, j, bits), begin && u == 0 ? none : d[8 * v + j]);
             }
         }
     };
@@ -299,7 +314,7 @@ __global__ __launch_bounds__(64 * WV) void awq_few_kernel(Awq a) {
             add(f1, false);
 #pragma unroll
             for (int j = 0; j < CW; ++j) {
-                const float zj = zero_point(z.v[j / 8] >> (CW < 8 ? 4 * CW * l.h : 0), j % 8), sj = scale_of<CW>(s, j, l.h);
+                const float zj = zero_point(z.v[j / 8] >> (CW < 8 ? 4 * CW * l.h : 0), j % 8, bits), sj = scale_of<CW>(s, j, l.h);
 #pragma unroll
                 for (int i = 0; i < MM; ++i) acc[j][i] = fmaf(sj, fmaf(-zj, sx[i], d[j][i]), acc[j][i]);
             }
@@ -379,6 +394,7 @@ __global__ __launch_bounds__(64 * WV) void awq_rows_kernel(Awq a) {
 #pragma unroll
         for (int j = 0; j < CW; ++j) acc[t][j] = f32x4_t(0.0f);
     const f32x4_t none = f32x4_t(0.0f);
+    const Bits bits;
     auto add = [&](const Step& st) {
         f32x4_t sx[MT];
 #pragma unroll
@@ -395,13 +411,13 @@ __global__ __launch_bounds__(64 * WV) void awq_rows_kernel(Awq a) {
                     for (int i = 0; i < 8; ++i) w[i] = st.w[i].v[j / 8];
                     h = halves(w, l.select);
                 }
-                const bf16x8_t b = column(h, j % 8);
+                const bf16x8_t b = column(h, j % 8, bits);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) d[j % 2][t] = mfma(st.x[t], b, none);
             }
             if (j > 0) {
                 const int o = j - 1;
-                const float zj = zero_point(st.z.v[o / 8] >> (CW < 8 ? 4 * CW * l.h : 0), o % 8), sj = scale_of<CW>(st.s, o, l.h);
+                const float zj = zero_point(st.z.v[o / 8] >> (CW < 8 ? 4 * CW * l.h : 0), o % 8, bits), sj = scale_of<CW>(st.s, o, l.h);
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
 #pragma unroll

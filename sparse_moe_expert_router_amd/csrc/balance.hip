@@ -76,7 +76,9 @@ __device__ __forceinline__ float lanes_max(float v) {
     return fmaxf(fmaxf(readlane_f32(v, 0), readlane_f32(v, 16)), fmaxf(readlane_f32(v, 32), readlane_f32(v, 48)));
 }
 
-// kV neighbouring values of a row (kV = 4: one aligned load), and their store.
+// kV neighbouring values of a row (kV = 4: one aligned load), and their store
+// (non-temporal: a gradient of 64 MB is not read back from L2; 41.1 -> 39.5 us
+// for 32768 tokens of 512 experts).
 template <int kV>
 __device__ __forceinline__ void load_v(const void* p, int64_t i, int f32, float* v) {
     if constexpr (kV == 4) {
@@ -95,8 +97,11 @@ __device__ __forceinline__ void load_v(const void* p, int64_t i, int f32, float*
 template <int kV>
 __device__ __forceinline__ void store_v(void* p, int64_t i, int f32, const float* v) {
     if constexpr (kV == 4) {
-        if (f32) *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
-        else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        if (f32)
+            __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + i));
+        else
+            __builtin_nontemporal_store(u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])},
+                                        reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(p) + i));
     } else {
         if (f32) static_cast<float*>(p)[i] = v[0];
         else static_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_bf16_bits(v[0]);
@@ -362,7 +367,7 @@ int bal_lanes(int E, int k) { return E <= 64 && k <= 16 ? 16 : 64; }
 int bal_grid(int T, int E, int k) {
     const int teams = kBalWaves * 64 / bal_lanes(E, k);
     const int need = (int)(((int64_t)T + teams - 1) / teams);
-    return need <= 4 ? 1 : need < 512 ? need : 512;  // a few rounds of one workgroup cost less than the sums' kernel
+    return need <= 4 ? 1 : need < 768 ? need : 768;  // a few rounds of one workgroup cost less than the sums' kernel
 }
 
 template <int kL, int kV, int kI>

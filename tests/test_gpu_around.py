@@ -400,7 +400,10 @@ def _check_awq(y, x, q, z, s):
 
 
 AWQ = [(1, 8, 32), (1, 128, 64), (3, 136, 96), (16, 1000, 1312), (1, 2560, 2560), (5, 640, 2560), (17, 264, 640), (32, 520, 1024),
-       (33, 256, 288), (64, 2560, 640), (65, 384, 320), (130, 72, 4096), (2, 24, 16384), (1, 8192, 2048), (16, 4096, 8192), (7, 16, 30720 // 2)]
+       (33, 256, 288), (64, 2560, 640), (65, 384, 320), (130, 72, 4096), (2, 24, 16384), (1, 8192, 2048), (16, 4096, 8192), (7, 16, 30720 // 2),
+       # the large matrices' forms: pairs of words (N % 16 == 0) and single ones, split and not, every number of rows
+       (1, 8192, 4096), (1, 4112, 8192), (2, 8200, 8192), (4, 16384, 2048), (3, 65536, 512), (5, 8192, 4352), (17, 4096, 8320),
+       (40, 8208, 4224), (33, 4104, 8192)]
 
 
 @pytest.mark.parametrize("out", [BF, F32])
