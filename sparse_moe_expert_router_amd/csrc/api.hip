@@ -888,8 +888,8 @@ size_t moe_workspace_bytes(int32_t op, int32_t T, int32_t k, int32_t E, int32_t 
         case MOE_OP_ROUTE_PERMUTE: return route_permute_ws(T, k, E, H);
         case MOE_OP_GROUPED_FFN_A8: return moe::ffn_a8_ws_bytes(T, k, E, H, F);
         case MOE_OP_REFILL_SCORE: return moe::refill_ws_bytes(T, k);
-        case MOE_OP_ADD_RMSNORM_BACKWARD: return H < 1 ? 0 : moe::norm_bwd_ws_bytes(T, H);
-        case MOE_OP_BALANCE_LOSS: return moe::balance_ws_bytes(T, k, E);
+        case MOE_OP_ADD_RMSNORM_BACKWARD: return H < 1 || H > moe::kNormMaxH ? 0 : moe::norm_bwd_ws_bytes(T, H);
+        case MOE_OP_BALANCE_LOSS: return E > kMaxE ? 0 : moe::balance_ws_bytes(T, k, E);
         default: return 0;
     }
 }

@@ -120,9 +120,9 @@ struct Run {
     int first, end;
 };
 __device__ __forceinline__ Run run_of(const Awq& a, int wave, int waves) {
-    const int groups = a.K >> (5 + a.gshift);
-    const int slices = gridDim.y * waves, slice = blockIdx.y * waves + wave;
-    return {(int)((int64_t)groups * slice / slices) << a.gshift, (int)((int64_t)groups * (slice + 1) / slices) << a.gshift};
+    // (at most 2^19 groups and 2^11 slices)
+    const uint32_t groups = (uint32_t)a.K >> (5 + a.gshift), slices = gridDim.y * waves, slice = blockIdx.y * waves + wave;
+    return {(int)(groups * slice / slices << a.gshift), (int)(groups * (slice + 1) / slices << a.gshift)};
 }
 
 // How the 16 lanes of a group share out a tile of 16 CW columns: with CW = 16
@@ -148,8 +148,8 @@ __device__ __forceinline__ Lane<CW> lane_of(int n16, uint32_t n8, int tiles) {
     if (CW == 16) {
         l.tile = blockIdx.x;
     } else {
-        const int xcd = blockIdx.x % 8, from = (int)((int64_t)tiles * xcd / 8);
-        to = (int)((int64_t)tiles * (xcd + 1) / 8);
+        const int xcd = blockIdx.x % 8, from = tiles * xcd / 8;  // (at most 2^19 tiles)
+        to = tiles * (xcd + 1) / 8;
         l.tile = from + (int)(blockIdx.x / 8);
     }
     if (l.tile >= to) {
@@ -474,20 +474,22 @@ __global__ __launch_bounds__(64 * WV) void awq_rows_kernel(Awq a) {
         }
 }
 
-// y = the `splits` partial sums, in order.
+// y = the `splits` partial sums, in order; a row of y a grid row.
 __global__ __launch_bounds__(256) void awq_sum_kernel(Awq a, int splits) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = (int64_t)a.M * a.N;
-    if (i >= n) return;
+    const int n = blockIdx.x * 256 + threadIdx.x;
+    if (n >= a.N) return;
+    const int64_t m = blockIdx.y, one = (int64_t)a.M * a.N;
+    const float* part = a.part + m * a.N + n;
     float v = 0.0f;
     for (int s = 0; s < splits; s += 8) {
         float p[8];  // eight loads on their way at a time
 #pragma unroll
-        for (int u = 0; u < 8; ++u) p[u] = a.part[(s + u < splits ? s + u : s) * n + i];
+        for (int u = 0; u < 8; ++u) p[u] = part[(s + u < splits ? s + u : s) * one];
 #pragma unroll
         for (int u = 0; u < 8; ++u)
             if (s + u < splits) v += p[u];
     }
-    put(a, i / a.N, (int)(i % a.N), v);
+    put(a, m, n, v);
 }
 
 // How a call is cut up.  Measured (one, 13 or 16 rows; us, sum kernel included):
@@ -578,8 +580,7 @@ hipError_t launch_awq_matmul(const uint16_t* x, int64_t ldx, const int32_t* qwei
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    const int64_t n = (int64_t)M * N;
-    hipLaunchKernelGGL(awq_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, p.splits);
+    hipLaunchKernelGGL(awq_sum_kernel, dim3((N + 255) / 256, M), dim3(256), 0, s, a, p.splits);  // (split: at most 128 x 32 rows)
     return hipGetLastError();
 }
 

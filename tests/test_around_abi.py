@@ -80,8 +80,11 @@ def test_norm_backward_refusals():
     assert _bwd(dw=X) == SHAPE and _bwd(dw=RSTD) == SHAPE and _bwd(dw=DX) == SHAPE and _bwd(dx=W) == SHAPE
     sizes = [moe.workspace_bytes(moe.OP_ADD_RMSNORM_BACKWARD, T, 1, 1, 2560) for T in (1, 7, 500, 4096, 1 << 20)]
     assert sizes == sorted(sizes)
-    for H in (0, -8, 1, 4, 1 << 20):
-        moe.workspace_bytes(moe.OP_ADD_RMSNORM_BACKWARD, 4, 1, 1, H)
+    for H in (0, -8, 1 << 20, (1 << 31) - 1):
+        assert moe.workspace_bytes(moe.OP_ADD_RMSNORM_BACKWARD, 4, 1, 1, H) == 0
+    assert moe.workspace_bytes(moe.OP_ADD_RMSNORM_BACKWARD, 4, 1, 1, 4) > 0       # (a size that the call refuses)
+    for E in (1025, (1 << 31) - 1):
+        assert moe.workspace_bytes(moe.OP_BALANCE_LOSS, 4, 1, E, 0) == 0
 
 
 def test_counts_refusals():

@@ -25,7 +25,7 @@ def _randn(*shape, seed, dtype=F32, scale=1.0):
 # ------------------------------------------------------------------ add and norm
 
 NORM_SHAPES = [(1, 8), (1, 16), (3, 24), (1, 2560), (2, 144), (5, 520), (7, 688), (33, 1024), (64, 2560), (300, 4104), (17, 8192), (9, 8208),
-               (5, 16384), (4097, 640), (20000, 128)]
+               (5, 16384), (4097, 640), (20000, 128), (9000, 520), (8193, 2560), (40, 256), (15, 264)]
 
 
 def _check_norm(x, w, res, r, eps, offset):
@@ -214,7 +214,7 @@ def test_counts_no_tokens():
 
 BALANCE = [(1, 1, 1), (1, 512, 10), (16, 512, 10), (5, 3, 2), (7, 8, 8), (33, 16, 4), (64, 60, 6), (301, 61, 16), (100, 64, 16), (50, 64, 17),
            (129, 100, 10), (77, 128, 64), (40, 129, 8), (500, 256, 8), (90, 260, 4), (1000, 384, 10), (63, 511, 10), (4099, 512, 10),
-           (30, 520, 10), (21, 1000, 5), (19, 1023, 64), (11, 1024, 1), (70000, 8, 2), (20000, 64, 6), (40000, 132, 4)]
+           (30, 520, 10), (21, 1000, 5), (19, 1023, 64), (11, 1024, 1), (70000, 8, 2), (20000, 64, 6), (40000, 132, 4), (33, 127, 9), (20, 63, 20), (200, 300, 40), (6, 65, 3)]
 
 
 def _routing(T, E, k, dtype, seed):
@@ -403,7 +403,9 @@ AWQ = [(1, 8, 32), (1, 128, 64), (3, 136, 96), (16, 1000, 1312), (1, 2560, 2560)
        (33, 256, 288), (64, 2560, 640), (65, 384, 320), (130, 72, 4096), (2, 24, 16384), (1, 8192, 2048), (16, 4096, 8192), (7, 16, 30720 // 2),
        # the large matrices' forms: pairs of words (N % 16 == 0) and single ones, split and not, every number of rows
        (1, 8192, 4096), (1, 4112, 8192), (2, 8200, 8192), (4, 16384, 2048), (3, 65536, 512), (5, 8192, 4352), (17, 4096, 8320),
-       (40, 8208, 4224), (33, 4104, 8192)]
+       (40, 8208, 4224), (33, 4104, 8192),
+       # wide and shallow
+       (1, 20000, 64), (9, 20000, 96), (40, 16392, 64), (1, 10000, 128), (4, 10000, 160), (20, 10000, 128)]
 
 
 @pytest.mark.parametrize("out", [BF, F32])
@@ -439,6 +441,30 @@ def test_awq_strided_and_untouched_surroundings():
     moe.awq_matmul(x, q, z, s, y=y)
     _check_awq(y, x, q, z, s)
     assert (out[0] == 9).all() and (out[-1] == 9).all() and (out[:, :3] == 9).all() and (out[:, 3 + N:] == 9).all()
+
+
+@pytest.mark.parametrize("M", [1, 3, 12, 40])
+def test_awq_codes_at_any_word(M):
+    """Codes and zeros that begin at an odd word: the same sums as from aligned ones, in both cuts of the columns."""
+    N, K = 8192, 4096
+    q, z, s = _awq(K, N, 32, 11)
+    x = _randn(M, K, seed=12, dtype=BF)
+    shift = lambda t: torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].view(t.shape)
+    for a, b in ((shift(q), z), (q, shift(z)), (shift(q), shift(z))):
+        assert a.data_ptr() % 8 or b.data_ptr() % 8
+        _check_awq(moe.awq_matmul(x, a, b, s, out_dtype=moe.OUT_F32), x, q, z, s)
+
+
+def test_awq_one_workspace_for_every_number_of_rows():
+    N, K = 8192, 8192
+    q, z, s = _awq(K, N, 128, 13)
+    ws = moe.Workspace(DEV)
+    x = _randn(65, K, seed=14, dtype=BF)
+    moe.awq_matmul(x, q, z, s, ws=ws)
+    buf = ws.buf
+    for M in (1, 4, 16, 17, 32, 33, 64):
+        _check_awq(moe.awq_matmul(x[:M], q, z, s, ws=ws), x[:M], q, z, s)
+    assert ws.buf is buf or ws.buf.numel() > buf.numel()
 
 
 @pytest.mark.parametrize("M", [2, 20, 70])
@@ -547,7 +573,8 @@ def test_a_router_training_step(T, H, E, k):
     ref = 0.02 * E * k / c.sum().clamp(min=1) * (torch.softmax(logits, 1) * on * f).sum()
     total = ref + (torch.softmax(logits.gather(1, idx), 1) * d["dgate"].double() * on).sum() + (s * d["dres"].double()).sum()
     gs, gw = torch.autograd.grad(total, (s, w))
-    assert abs(float(loss) - float(ref)) <= 1e-5 * float(ref)
+    ref = float(ref.detach())
+    assert abs(float(loss) - ref) <= 1e-5 * ref
     # fp32 arithmetic throughout, except that autograd's product has y's own rounding nowhere: 1e-5 of the whole
     assert (dx.double() - gs).norm() <= 1e-5 * gs.norm() and (dw.double() - gw).norm() <= 1e-5 * gw.norm() + 1e-9
 
