@@ -594,7 +594,7 @@ moe_status moe_balance_loss(const void *logits, int32_t logits_dtype, int64_t lo
  * again: any M works, but the call is made for up to about 64 rows.  A row of x
  * that holds an infinity or a NaN gives NaN in that row only.
  * N % 8 == 0, K % group == 0, ldx % 8 == 0, N, K and ldx at most 2^24, M at most
- * 2^20, fewer than 2^23 tiles of 32 rows x 128 columns; x and scales 16-byte aligned,
+ * 2^20, fewer than 2^20 tiles of 32 rows x 1024 columns; x and scales 16-byte aligned,
  * the rest aligned to its element (MOE_ERR_UNSUPPORTED otherwise).  Workspace:
  * moe_awq_matmul_workspace_bytes(M, N, K, group), 16-byte aligned, of any content.
  */

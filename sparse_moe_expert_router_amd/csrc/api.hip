@@ -58,7 +58,8 @@ struct Rows {
 bool awq_sizes_ok(int32_t M, int32_t N, int32_t K, int32_t group) {
     if (group != 32 && group != 64 && group != 128) return false;
     if (N < 1 || K < 1 || N % 8 || K % group || N > (1 << 24) || K > (1 << 24) || M > (1 << 20)) return false;
-    return (int64_t)((N + 127) / 128) * ((M + 31) / 32) < (1 << 23);  // a launch has fewer than 2^32 threads
+    // a launch has fewer than 2^32 threads: 512 a tile, the tiles of a row in whole eighths
+    return (int64_t)((N + 1023) / 1024 * 8) * ((M + 31) / 32) < (1 << 23);
 }
 
 // Screened routing (approximate MFMA logits + exact recompute of candidates)

