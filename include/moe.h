@@ -590,7 +590,7 @@ moe_status moe_balance_loss(const void *logits, int32_t logits_dtype, int64_t lo
  * by out_dtype) have row strides ldx >= K, ldy >= N in elements; y may not
  * overlap x (MOE_ERR_SHAPE).  The codes enter exactly and the sums are fp32: x
  * (16 + q) and x (16 + z) are summed and subtracted per 32 inputs, so the sums'
- * roundings are those of values up to 31 |x|.  Every 32 rows read the codes
+ * roundings are those of values up to 31 |x| (and |x| above about 1e36 overflows).  Every 32 rows read the codes
  * again: any M works, but the call is made for up to about 64 rows.  A row of x
  * that holds an infinity or a NaN gives NaN in that row only.
  * N % 8 == 0, K % group == 0, ldx % 8 == 0, N, K and ldx at most 2^24, M at most

@@ -4,10 +4,12 @@
 //
 // Bound by the codes' bytes for large matrices (16 rows x 16384 x 16384: 36 us,
 // 4.4 TB/s with the scales; one row 32 us), by the launch and one or two round
-// trips to memory for small ones (one row x 2560 x 2560: 6.2 us).  A word holds one input of 8 columns, so a lane that
-// reads the words of 8 consecutive inputs holds, for each of the word's 8
-// columns, 8 inputs: its operand of a 16 x 16 x 32 bf16 MFMA for that column
-// (16 lanes: 16 words, 128 columns; 4 groups of 16 lanes: 4 x 8 inputs).  Two
+// trips to memory for small ones (one row x 2560 x 2560: 6.2 us).
+//
+// A word holds one input of 8 columns, so a lane that reads the words of 8
+// consecutive inputs holds, for each of the word's 8 columns, 8 inputs: its
+// operand of a 16 x 16 x 32 bf16 MFMA for that column (16 lanes: 16 words, 128
+// columns; 4 groups of 16 lanes: 4 x 8 inputs).  Two
 // v_perm bring the halves of two inputs' words together, then a shift and a
 // v_and_or make the exact bf16 pair 16 + q of one column.  With fp32 sums
 //   sum x (q - z) = sum x (16 + q) - (16 + z) sum x,
@@ -266,12 +268,14 @@ __global__ __launch_bounds__(64 * WV) void awq_few_kernel(Awq a) {
         const __amdgpu_buffer_rsrc_t xb = buffer(a.x + at * 32, left ? (uint32_t)(a.M - 1) * (uint32_t)a.ldx * 2 + (uint32_t)left * 64u : 0u);
         const __amdgpu_buffer_rsrc_t q = buffer(a.qw + at * 32 * n8, (uint32_t)left * 128u * n8);
         const uint32_t xo = kq < r.end - set ? xoff : kOutside;
+        // (an empty buffer's bound, which the scalar offset is taken from, stays 0)
+        const uint32_t xstep = left ? 16u : 0u, wstep = left ? 32u * n8 : 0u;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) f.x[u] = load16(xb, xo, 16u * (2 * h + u));
+        for (int u = 0; u < 2; ++u) f.x[u] = load16(xb, xo, xstep * (2 * h + u));
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f.w[u][i] = load_words<W>(q, woff[i], 32u * (2 * h + u) * n8);
+            for (int i = 0; i < 8; ++i) f.w[u][i] = load_words<W>(q, woff[i], wstep * (2 * h + u));
     };
     const f32x4_t none = f32x4_t(0.0f);
     const Bits bits;
