@@ -526,8 +526,8 @@ moe_status moe_add_rmsnorm(const void *x, int32_t x_dtype, int64_t x_stride, con
  * dres (nullable) is the gradient that reaches residual_out from elsewhere.  dy
  * is of dy_dtype; s, dres and dx are of s_dtype; all four have row strides.  dx
  * may be dy, s or dres where type and stride are the same; any other overlap ->
- * MOE_ERR_SHAPE.  The sums over rows are taken in a fixed order.  T = 0 sets dw to
- * 0.  Sizes, alignment and errors as moe_add_rmsnorm's; workspace:
+ * MOE_ERR_SHAPE.  The sums over rows are taken in a fixed order (another one where
+ * dx is dy or s).  T = 0 sets dw to 0.  Sizes, alignment and errors as moe_add_rmsnorm's; workspace:
  * moe_workspace_bytes(MOE_OP_ADD_RMSNORM_BACKWARD, T, 1, 1, H, 0), 16-byte aligned.
  */
 moe_status moe_add_rmsnorm_backward(const void *dy, int32_t dy_dtype, int64_t dy_stride, const void *s,

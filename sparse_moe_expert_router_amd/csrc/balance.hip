@@ -33,30 +33,38 @@ __global__ __launch_bounds__(256) void count_clear_kernel(uint32_t* __restrict__
     if (e < E) counts[e] = 0;
 }
 
-// A workgroup's pairs, counted in LDS and then added to `counts` (one workgroup
-// and kWrite: written).  Integer additions: the order does not matter.  Ids
-// outside [0, E) are not counted.  Eight loads are on their way at a time.
-template <bool kWrite>
+// Pairs counted in LDS; ids outside [0, E) are not.  kOwn: a workgroup reads all
+// pairs and counts a share of the experts, which it writes (or adds to).  Else it
+// reads a share of the pairs and adds its counts of all experts to what others
+// add (integers: the order does not matter).  Eight loads are on their way at a
+// time; none stands in a branch, where it would be waited for (49152 pairs by
+// one workgroup 22 us).
+template <bool kOwn>
 __global__ __launch_bounds__(1024) void count_kernel(const int32_t* __restrict__ idx, uint32_t pairs, uint32_t k, int E,
-                                                     const uint8_t* __restrict__ valid, uint32_t* __restrict__ counts) {
+                                                     const uint8_t* __restrict__ valid, int accumulate, uint32_t* __restrict__ counts) {
     __shared__ uint32_t bins[1024];
-    for (int e = threadIdx.x; e < E; e += 1024) bins[e] = 0;
+    const int lo = kOwn ? (int)(E * blockIdx.x / gridDim.x) : 0, n = (kOwn ? (int)(E * (blockIdx.x + 1) / gridDim.x) : E) - lo;
+    for (int e = threadIdx.x; e < n; e += 1024) bins[e] = 0;
     __syncthreads();
-    const uint32_t step = gridDim.x * 1024u;
-    for (uint64_t p0 = blockIdx.x * 1024u + threadIdx.x; p0 < pairs; p0 += 8ull * step) {
-        uint32_t e[8];
+    const uint32_t step = kOwn ? 1024u : gridDim.x * 1024u;
+    for (uint64_t p0 = (kOwn ? 0u : blockIdx.x * 1024u) + threadIdx.x; p0 < pairs; p0 += 8ull * step) {
+        uint32_t e[8], on[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint64_t p = p0 + (uint64_t)i * step;
-            e[i] = p < pairs && (!valid || valid[(uint32_t)p / k]) ? (uint32_t)idx[p] : ~0u;
+            const uint32_t at = p < pairs ? (uint32_t)p : pairs - 1;
+            e[i] = (uint32_t)idx[at];
+            on[i] = valid ? valid[at / k] : 1u;
         }
 #pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = on[i] && p0 + (uint64_t)i * step < pairs ? e[i] - (uint32_t)lo : ~0u;
+#pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (e[i] < (uint32_t)E) atomicAdd(&bins[e[i]], 1u);
+            if (e[i] < (uint32_t)n) atomicAdd(&bins[e[i]], 1u);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += 1024) {
-        if (kWrite) counts[e] = bins[e];
+    for (int e = threadIdx.x; e < n; e += 1024) {
+        if (kOwn) counts[lo + e] = accumulate ? counts[lo + e] + bins[e] : bins[e];
         else if (bins[e]) atomicAdd(&counts[e], bins[e]);
     }
 }
@@ -362,7 +370,11 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(const float* __restri
 
 namespace {
 
-constexpr uint32_t kCountAlone = 8192;
+// Up to here one launch counts: the host gains 3 to 4 us, a captured call loses as
+// much at the end (8191 tokens to 6 of 61 experts: 19.5 against 22.8 us a call
+// with the loss, 15.4 against 13.3 in a graph; 6500 to 10 of 512: 23.1, 23.3 and
+// 22.8, 19.3).
+constexpr uint32_t kCountOwn = 49152;
 
 int bal_lanes(int E, int k) { return E <= 64 && k <= 16 ? 16 : 64; }
 
@@ -386,12 +398,9 @@ hipError_t run_balance(const BalanceArgs& a, float* part, BalancePart* tail, flo
 hipError_t launch_expert_counts(const int32_t* idx, int T, int k, int E, const uint8_t* valid, int accumulate, uint32_t* counts,
                                 hipStream_t s) {
     const uint32_t pairs = (uint32_t)T * (uint32_t)k;  // (fits 31 bits)
-    // one workgroup while that is no slower than a second launch (its LDS counters
-    // collide: 49152 pairs of 61 experts take it 22 us); more than 64 meet at the same counters
-    const uint32_t need = pairs <= kCountAlone ? 1 : (pairs + 4095) / 4096;
-    const dim3 grid(need < 64 ? need : 64), block(1024);
-    if (grid.x == 1 && !accumulate) {
-        hipLaunchKernelGGL((count_kernel<true>), grid, block, 0, s, idx, pairs, (uint32_t)k, E, valid, counts);
+    if (pairs <= kCountOwn) {
+        const dim3 grid(pairs <= 1024 || E < 16 ? 1 : 16), block(1024);
+        hipLaunchKernelGGL((count_kernel<true>), grid, block, 0, s, idx, pairs, (uint32_t)k, E, valid, accumulate, counts);
         return hipGetLastError();
     }
     if (!accumulate) {
@@ -399,7 +408,9 @@ hipError_t launch_expert_counts(const int32_t* idx, int T, int k, int E, const u
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((count_kernel<false>), grid, block, 0, s, idx, pairs, (uint32_t)k, E, valid, counts);
+    const uint32_t need = (pairs + 4095) / 4096;  // (more than 64 meet at the same counters)
+    hipLaunchKernelGGL((count_kernel<false>), dim3(need < 64 ? need : 64), dim3(1024), 0, s, idx, pairs, (uint32_t)k, E, valid, 1,
+                       counts);
     return hipGetLastError();
 }
 

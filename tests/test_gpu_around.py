@@ -151,6 +151,23 @@ def test_norm_backward(T, H, sd, yd, dres):
     assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
 
 
+@pytest.mark.parametrize("T,H", [(768, 72), (769, 72), (767, 256), (700, 264), (768, 1000), (769, 1000), (513, 8200), (130, 16384), (65, 40)])
+@pytest.mark.parametrize("sd,yd", [(BF, BF), (F32, F32), (BF, F32), (F32, BF)])
+def test_norm_backward_of_few_and_many_rows(T, H, sd, yd):
+    s, dy = _randn(T, H + 8, seed=T, dtype=sd, scale=2.0)[:, 8:], _randn(T, H + 16, seed=2, dtype=yd, scale=1e-2)[:, :H]
+    w = _randn(H, seed=1, dtype=sd, scale=0.2)
+    rstd = moe.add_rmsnorm(s, w, outputs=("y", "rstd")).rstd
+    rx, lx, rw, lw = R.norm_backward(dy, s, rstd, w, 1.0, None)
+    dx, dw = moe.add_rmsnorm_backward(dy, s, rstd, w)
+    R.check_rows(dx, rx, 0.0, lx)
+    assert ((dw.double() - rw).abs() <= lw).all()
+    # in place the sums may be taken in another order, and are as good
+    on = s.clone()
+    dx2, dw2 = moe.add_rmsnorm_backward(dy, on, rstd, w, dx=on)
+    assert dx2 is on and torch.equal(dx2, dx)
+    assert ((dw2.double() - rw).abs() <= lw).all()
+
+
 def test_norm_backward_in_place_and_strided():
     T, H = 29, 1288
     wide = _randn(T, 2 * H + 8, seed=11, dtype=BF)
@@ -196,6 +213,22 @@ def test_counts(T, k, E, masked):
     assert torch.equal(moe.expert_counts(idx, E, token_valid=valid, counts=counts), want)
     moe.expert_counts(idx, E, token_valid=valid.to(torch.uint8) if masked else None, counts=counts, accumulate=True)
     assert torch.equal(counts, 2 * want)
+
+
+@pytest.mark.parametrize("T,k,E", [(128, 8, 100), (1025, 1, 15), (1025, 1, 16), (1000, 5, 17), (3000, 3, 1023), (24576, 2, 8), (24577, 2, 8),
+                                   (8192, 6, 61), (8193, 6, 61)])
+def test_counts_of_few_and_many_pairs(T, k, E):
+    idx = torch.randint(-1, E + 1, (T, k), generator=_gen(T), device=DEV, dtype=torch.int32)
+    valid = torch.rand(T, generator=_gen(1), device=DEV) < 0.8
+    for v in (None, valid):
+        want = R.counts(idx, E, v).int()
+        wide = torch.full((E + 2,), 7, dtype=torch.int32, device=DEV)
+        counts = wide[1:E + 1]
+        assert torch.equal(moe.expert_counts(idx, E, token_valid=v, counts=counts), want)
+        for i in (2, 3):
+            moe.expert_counts(idx, E, token_valid=v, counts=counts, accumulate=True)
+            assert torch.equal(counts, i * want)
+        assert wide[0] == 7 and wide[-1] == 7
 
 
 def test_counts_are_the_permutations_groups():
