@@ -46,18 +46,30 @@ __global__ __launch_bounds__(1024) void count_kernel(const int32_t* __restrict__
     const int lo = kOwn ? (int)(E * blockIdx.x / gridDim.x) : 0, n = (kOwn ? (int)(E * (blockIdx.x + 1) / gridDim.x) : E) - lo;
     for (int e = threadIdx.x; e < n; e += 1024) bins[e] = 0;
     __syncthreads();
-    const uint32_t step = kOwn ? 1024u : gridDim.x * 1024u;
-    for (uint64_t p0 = (kOwn ? 0u : blockIdx.x * 1024u) + threadIdx.x; p0 < pairs; p0 += 8ull * step) {
+    const uint32_t step = kOwn ? 1024u : gridDim.x * 1024u, start = (kOwn ? 0u : blockIdx.x * 1024u) + threadIdx.x;
+    // the pair's token and slot go along, which spares a division a pair
+    const uint32_t tokens = pairs / k, dtok = step / k, dslot = step % k;
+    uint32_t tok = start / k, slot = start % k;
+    for (uint32_t p0 = start; p0 < pairs; p0 += 8 * step) {  // (below 2^31 + 2^19)
         uint32_t e[8], on[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint64_t p = p0 + (uint64_t)i * step;
-            const uint32_t at = p < pairs ? (uint32_t)p : pairs - 1;
-            e[i] = (uint32_t)idx[at];
-            on[i] = valid ? valid[at / k] : 1u;
+            const uint32_t p = p0 + i * step;
+            e[i] = (uint32_t)idx[p < pairs ? p : pairs - 1];
+            if (valid) {
+                on[i] = valid[tok < tokens ? tok : tokens - 1];
+                tok += dtok;
+                slot += dslot;
+                if (slot >= k) {
+                    slot -= k;
+                    ++tok;
+                }
+            } else {
+                on[i] = 1u;
+            }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = on[i] && p0 + (uint64_t)i * step < pairs ? e[i] - (uint32_t)lo : ~0u;
+        for (int i = 0; i < 8; ++i) e[i] = on[i] && p0 + i * step < pairs ? e[i] - (uint32_t)lo : ~0u;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (e[i] < (uint32_t)n) atomicAdd(&bins[e[i]], 1u);
@@ -370,10 +382,10 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(const float* __restri
 
 namespace {
 
-// Up to here one launch counts: the host gains 3 to 4 us, a captured call loses as
-// much at the end (8191 tokens to 6 of 61 experts: 19.5 against 22.8 us a call
-// with the loss, 15.4 against 13.3 in a graph; 6500 to 10 of 512: 23.1, 23.3 and
-// 22.8, 19.3).
+// Up to here one launch counts: the host gains 3 to 4 us a call, a captured call
+// loses as much at the end (counts and loss, 8191 tokens to 6 of 61 experts: 19.5
+// against 22.8 us a call, 16.0 against 13.3 in a graph; 6500 to 10 of 512: 23.1
+// against 23.3, and 22.8 against 19.3).
 constexpr uint32_t kCountOwn = 49152;
 
 int bal_lanes(int E, int k) { return E <= 64 && k <= 16 ? 16 : 64; }
