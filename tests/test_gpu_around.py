@@ -328,6 +328,15 @@ def test_balance_same_expert_twice_and_foreign_ids(E, k):
     assert all(torch.equal(a, b) for a, b in zip(got, moe.balance_loss(logits, counts, k, 0.01, **args)))
 
 
+@pytest.mark.parametrize("E,k", [(65, 3), (100, 16), (128, 17), (130, 32), (200, 32), (200, 33), (255, 5), (256, 10)])
+def test_balance_of_middle_widths(E, k):
+    for T in (1, 15, 65, 3001):
+        test_balance(T, E, k, F32)
+        test_balance(T, E, k, BF)
+    test_balance_masked_experts_and_empty_rows(E)
+    test_balance_same_expert_twice_and_foreign_ids(E, max(k, 4))
+
+
 def test_balance_even_load_has_no_gradient():
     T, E = 96, 12
     idx = (torch.arange(T, device=DEV, dtype=torch.int32) % E)[:, None].contiguous()
