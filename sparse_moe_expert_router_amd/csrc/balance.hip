@@ -76,8 +76,9 @@ __global__ __launch_bounds__(1024) void count_kernel(const int32_t* __restrict__
     }
     __syncthreads();
     for (int e = threadIdx.x; e < n; e += 1024) {
-        if (kOwn) counts[lo + e] = accumulate ? counts[lo + e] + bins[e] : bins[e];
-        else if (bins[e]) atomicAdd(&counts[e], bins[e]);
+        // (also where this workgroup alone has the expert: another stream's call may add to it)
+        if (kOwn && !accumulate) counts[lo + e] = bins[e];
+        else if (bins[e]) atomicAdd(&counts[lo + e], bins[e]);
     }
 }
 

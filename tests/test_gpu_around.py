@@ -231,6 +231,21 @@ def test_counts_of_few_and_many_pairs(T, k, E):
         assert wide[0] == 7 and wide[-1] == 7
 
 
+def test_counts_added_from_two_streams():
+    E, parts = 61, [(8000, 6), (9000, 6), (100, 3), (20000, 2)]
+    idx = [torch.randint(0, E, p, generator=_gen(i), device=DEV, dtype=torch.int32) for i, p in enumerate(parts)]
+    want = sum(R.counts(i, E, None) for i in idx).int() * 20
+    counts = torch.zeros(E, dtype=torch.int32, device=DEV)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for j, i in enumerate(idx):
+            with torch.cuda.stream(streams[j % 2]):
+                moe.expert_counts(i, E, counts=counts, accumulate=True)
+    torch.cuda.synchronize()
+    assert torch.equal(counts, want)
+
+
 def test_counts_are_the_permutations_groups():
     x, w = _randn(777, 256, seed=1, dtype=BF), _randn(64, 256, seed=2, dtype=BF, scale=0.05)
     idx, _, _, off, _, _ = moe.route_permute(x, w, 4)
