@@ -307,7 +307,9 @@ __global__ __launch_bounds__(64 * WV) void awq_few_kernel(Awq a) {
         for (int set = r.first; set < r.end; set += 4) {
             __builtin_amdgcn_sched_barrier(0);
             fetch(set, 1, f1);
-            const int left = sets - set < 4 ? sets - set : 4;
+            // (zeros and scales of the run's own groups only: its lanes past the end meet
+            // scales of 0, as another run's infinity times their sum of 0 were NaN)
+            const int left = r.end - set < 4 ? r.end - set : 4;
             const int g = set >> a.gshift, groups = (left + (1 << a.gshift) - 1) >> a.gshift;
             const Words<W> z = load_zeros<W>(buffer(a.qz + (int64_t)g * n8, (uint32_t)groups * 4u * n8), 4u * goff);
             const Scales<CW> s = load_scales<CW>(buffer(a.sc + (int64_t)g * n8 * 8, (uint32_t)groups * 16u * n8), goff, l.h);
