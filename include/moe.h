@@ -501,9 +501,9 @@ moe_status moe_grouped_ffn_a8(const uint16_t *x, int32_t T, int32_t k, const moe
  * as moe_fp8_quantize quantises, from its fp32 values: the form moe_fp8_matmul
  * reads.  rstd (nullable, [T] fp32) receives r, which the backward pass reads.
  * One of y and codes must be given.  x_dtype, res_dtype and w_dtype are
- * MOE_OUT_BF16 or MOE_OUT_F32.  An output may be an input of the same type and
- * stride (residual_out = residual, y = x); any other overlap of an output with
- * an input or another output -> MOE_ERR_SHAPE.  A row that holds an infinity or a
+ * MOE_OUT_BF16 or MOE_OUT_F32.  residual_out and y may be an input of the same
+ * type and stride (residual_out = residual, y = x); any other overlap of an output
+ * with an input or another output -> MOE_ERR_SHAPE.  A row that holds an infinity or a
  * NaN gives NaN (and 0) in its own row only; squares are summed in fp32, so a row
  * of values above about 1e18 gives zeros.
  * H % 8 == 0 (with codes H % 16 == 0), H <= 16384, rows of whole 16-byte pieces,

@@ -763,7 +763,10 @@ moe_status moe_add_rmsnorm(const void* x, int32_t x_dtype, int64_t x_stride, con
                          Rows(scales, 1, 4, codes ? (size_t)T * ((H + 127) / 128) : 0), Rows(rstd, 1, 4, (size_t)T)};
     const Rows w(weight, 1, w_dtype == MOE_OUT_F32 ? 4 : 2, (size_t)H);
     for (int i = 0; i < 5; ++i) {
-        if ((out[i].meets(in_x) && !out[i].same(in_x)) || (out[i].meets(in_r) && !out[i].same(in_r)) || out[i].meets(w))
+        // (residual_out and y only: rstd of H rows has the bytes of one row of x)
+        const bool over = i < 2;
+        if ((out[i].meets(in_x) && !(over && out[i].same(in_x))) || (out[i].meets(in_r) && !(over && out[i].same(in_r))) ||
+            out[i].meets(w))
             return MOE_ERR_SHAPE;
         for (int j = 0; j < i; ++j)
             if (out[i].meets(out[j])) return MOE_ERR_SHAPE;
