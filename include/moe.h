@@ -565,8 +565,8 @@ moe_status moe_expert_counts(const int32_t *topk_idx, int32_t T, int32_t k, int3
  *   dlogits[t][idx_j] += g_j (dgate_j - sum_i g_i dgate_i)
  * (slots that name the same expert add up; an id outside [0, E) receives nothing).
  * logits [T][E] and dlogits (nullable) have row strides in elements and are bf16
- * or fp32; dlogits may be logits itself where types and strides are the same
- * (any other overlap -> MOE_ERR_SHAPE).  Logits of -inf (experts that are masked
+ * or fp32; dlogits may be logits itself where types and strides are the same (any
+ * other overlap of an output with an input or another output -> MOE_ERR_SHAPE).  Logits of -inf (experts that are masked
  * out) have probability 0; a token whose logits are all -inf and a token that is
  * not valid count for nothing and get gradient 0 (the latter whatever its logits,
  * gates and ids hold; the former still gets its gates').  NaN or +inf gives NaN in

@@ -846,8 +846,21 @@ moe_status moe_balance_loss(const void* logits, int32_t logits_dtype, int64_t lo
         if ((uintptr_t)logits % el || (dlogits && (uintptr_t)dlogits % dl) || (uintptr_t)topk_idx % 4 ||
             (uintptr_t)topk_gate % 4 || (uintptr_t)dgate % 4)
             return MOE_ERR_UNSUPPORTED;
-        const Rows in(logits, logits_stride, logits_dtype, T, E), out(dlogits, dlogits_stride, dlogits_dtype, T, E);
-        if (out.meets(in) && !out.same(in)) return MOE_ERR_SHAPE;
+    }
+    // (the second kernel reads the counts beside the workgroups that write prob_sum)
+    const size_t pairs = (size_t)T * k;
+    const Rows in(logits, logits_stride, logits_dtype, T, E);
+    const Rows out[3] = {Rows(dlogits, dlogits_stride, dlogits_dtype, T, E), Rows(loss, 1, 4, 1), Rows(prob_sum, 1, 4, (size_t)E)};
+    const Rows more[5] = {Rows(counts, 1, 4, (size_t)E), Rows(token_valid, 1, 1, (size_t)T), Rows(topk_idx, 1, 4, pairs),
+                          Rows(topk_gate, 1, 4, pairs), Rows(dgate, 1, 4, pairs)};
+    for (int i = 0; i < 3; ++i) {
+        if (out[i].meets(in) && !(i == 0 && out[i].same(in))) return MOE_ERR_SHAPE;
+        for (const Rows& r : more)
+            if (out[i].meets(r)) return MOE_ERR_SHAPE;
+        for (int j = 0; j < i; ++j)
+            if (out[i].meets(out[j])) return MOE_ERR_SHAPE;
+    }
+    if (T > 0) {
         if (ws_bytes < moe::balance_ws_bytes(T, k, E)) return MOE_ERR_WORKSPACE;
         if (!ws) return MOE_ERR_NULL;
         if (!aligned16(ws)) return MOE_ERR_UNSUPPORTED;

@@ -1,6 +1,14 @@
 """Memory that the operators around the layer refuse to share between an output and anything else, before any HIP call (the
 pointers are never dereferenced)."""
-from tests.test_around_abi import F32, RES, RSTD, SHAPE, W, X, Y, _bwd, _norm
+import ctypes
+
+from tests.test_around_abi import CODES, DX, F32, P, RES, RSTD, SCALES, SHAPE, W, X, Y, _bal, _bwd, _norm
+
+VALID = P(12)
+
+
+def at(p, n):
+    return ctypes.c_void_p(p.value + n)
 
 
 def test_norm_small_outputs_are_never_an_inputs_rows():
@@ -20,3 +28,23 @@ def test_norm_small_outputs_are_never_an_inputs_rows():
 def test_norm_backward_sums_are_never_an_inputs_rows():
     for p in (X, Y, RES, RSTD, W):
         assert _bwd(dw=p, T=1, yd=F32, sd=F32) == SHAPE and _bwd(dw=p) == SHAPE
+
+
+GATES = dict(i=Y, g=CODES, dg=RSTD)
+
+
+def test_balance_outputs_share_no_memory():
+    E, T, k = 64, 4, 2
+    inputs = dict(X=(X, 4 * T * E), W=(W, 4 * E), V=(VALID, T), Y=(Y, 4 * T * k), C=(CODES, 4 * T * k), R=(RSTD, 4 * T * k))
+    for p, size in inputs.values():
+        last = at(p, size - 4)
+        assert _bal(loss=p, v=VALID, **GATES) == SHAPE and _bal(loss=last, v=VALID, **GATES) == SHAPE
+        assert _bal(ps=p, v=VALID, **GATES) == SHAPE and _bal(ps=last, v=VALID, **GATES) == SHAPE
+        assert _bal(ps=at(p, -4 * E + 4), v=VALID, **GATES) == SHAPE
+        if p is not X:
+            assert _bal(dl=p, v=VALID, **GATES) == SHAPE and _bal(dl=at(p, -4 * T * E + 4), v=VALID, **GATES) == SHAPE
+    # each other
+    assert _bal(ps=SCALES) == SHAPE and _bal(loss=at(SCALES, 4 * E - 4), ps=SCALES) == SHAPE
+    assert _bal(loss=DX) == SHAPE and _bal(loss=at(DX, 4 * T * E - 4)) == SHAPE and _bal(ps=DX) == SHAPE
+    # without tokens loss and prob_sum are written all the same, and the counts read
+    assert _bal(T=0, loss=W) == SHAPE and _bal(T=0, ps=W) == SHAPE and _bal(T=0, ps=SCALES) == SHAPE
