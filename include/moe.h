@@ -542,7 +542,8 @@ moe_status moe_add_rmsnorm_backward(const void *dy, int32_t dy_dtype, int64_t dy
  * with token_valid[t] != 0 (uint8 [T], nullable = all); with accumulate != 0
  * they are added to what counts holds (atomically: calls on several streams may
  * add to the same counts).  Ids outside [0, E) are not counted.
- * T = 0 clears counts unless accumulate is set.  k <= E <= 1024.
+ * T = 0 clears counts unless accumulate is set.  k <= E <= 1024.  counts over
+ * topk_idx or token_valid -> MOE_ERR_SHAPE.
  */
 moe_status moe_expert_counts(const int32_t *topk_idx, int32_t T, int32_t k, int32_t E, const uint8_t *token_valid,
                              int32_t accumulate, uint32_t *counts, void *stream);

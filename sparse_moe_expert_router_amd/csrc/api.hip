@@ -824,6 +824,8 @@ moe_status moe_expert_counts(const int32_t* topk_idx, int32_t T, int32_t k, int3
     if (T == 0 && accumulate) return MOE_OK;
     if (!counts || (T > 0 && !topk_idx)) return MOE_ERR_NULL;
     if ((uintptr_t)topk_idx % 4 || (uintptr_t)counts % 4) return MOE_ERR_UNSUPPORTED;
+    const Rows c(counts, 1, 4, (size_t)E);
+    if (c.meets(Rows(topk_idx, 1, 4, (size_t)T * k)) || c.meets(Rows(token_valid, 1, 1, (size_t)T))) return MOE_ERR_SHAPE;
     return hip_status(moe::launch_expert_counts(topk_idx, T, k, E, token_valid, accumulate != 0, counts,
                                                 static_cast<hipStream_t>(stream)));
 }

@@ -2,6 +2,7 @@
 pointers are never dereferenced)."""
 import ctypes
 
+import sparse_moe_expert_router_amd as moe
 from tests.test_around_abi import CODES, DX, F32, P, RES, RSTD, SCALES, SHAPE, W, X, Y, _bal, _bwd, _norm
 
 VALID = P(12)
@@ -48,3 +49,10 @@ def test_balance_outputs_share_no_memory():
     assert _bal(loss=DX) == SHAPE and _bal(loss=at(DX, 4 * T * E - 4)) == SHAPE and _bal(ps=DX) == SHAPE
     # without tokens loss and prob_sum are written all the same, and the counts read
     assert _bal(T=0, loss=W) == SHAPE and _bal(T=0, ps=W) == SHAPE and _bal(T=0, ps=SCALES) == SHAPE
+
+
+def test_counts_share_no_memory():
+    c = lambda i=X, T=4, k=2, E=8, v=VALID, acc=0, n=Y: moe.lib().moe_expert_counts(i, T, k, E, v, acc, n, None)
+    for acc in (0, 1):
+        assert c(n=X, acc=acc) == SHAPE and c(n=at(X, 28), acc=acc) == SHAPE and c(n=at(X, -28), acc=acc) == SHAPE
+        assert c(n=VALID, acc=acc) == SHAPE and c(n=at(VALID, -28), acc=acc) == SHAPE
