@@ -590,7 +590,7 @@ moe_status moe_balance_loss(const void *logits, int32_t logits_dtype, int64_t lo
  * qweight [K][N/8] int32, qzeros [K/group][N/8] int32, scales [K/group][N] fp16,
  * contiguous; group 32, 64 or 128 inputs.  x [M][K] and y [M][N] (bf16 or fp32
  * by out_dtype) have row strides ldx >= K, ldy >= N in elements; y may not
- * overlap x (MOE_ERR_SHAPE).  The codes enter exactly and the sums are fp32: x
+ * overlap an input (MOE_ERR_SHAPE).  The codes enter exactly and the sums are fp32: x
  * (16 + q) and x (16 + z) are summed and subtracted per 32 inputs, so the sums'
  * roundings are those of values up to 31 |x| (and |x| above about 1e36 overflows).  Every 32 rows read the codes
  * again: any M works, but the call is made for up to about 64 rows.  A row of x

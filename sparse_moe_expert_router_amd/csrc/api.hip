@@ -888,7 +888,11 @@ moe_status moe_awq_matmul(const uint16_t* x, int64_t ldx, const int32_t* qweight
     if (!aligned16(x) || !aligned16(scales) || (uintptr_t)qweight % 4 || (uintptr_t)qzeros % 4 ||
         (uintptr_t)y % (out_dtype == MOE_OUT_F32 ? 4 : 2))
         return MOE_ERR_UNSUPPORTED;
-    if (Rows(y, ldy, out_dtype, M, N).meets(Rows(x, ldx, MOE_OUT_BF16, M, K))) return MOE_ERR_SHAPE;
+    const Rows out(y, ldy, out_dtype, M, N), in[4] = {Rows(x, ldx, MOE_OUT_BF16, M, K), Rows(qweight, 1, 4, (size_t)K * (N / 8)),
+                                                      Rows(qzeros, 1, 4, (size_t)(K / group) * (N / 8)),
+                                                      Rows(scales, 1, 2, (size_t)(K / group) * N)};
+    for (const Rows& r : in)
+        if (out.meets(r)) return MOE_ERR_SHAPE;
     const size_t need = moe::awq_matmul_needs(M, N, K);
     if (ws_bytes < need) return MOE_ERR_WORKSPACE;
     if (need && !ws) return MOE_ERR_NULL;

@@ -56,3 +56,10 @@ def test_counts_share_no_memory():
     for acc in (0, 1):
         assert c(n=X, acc=acc) == SHAPE and c(n=at(X, 28), acc=acc) == SHAPE and c(n=at(X, -28), acc=acc) == SHAPE
         assert c(n=VALID, acc=acc) == SHAPE and c(n=at(VALID, -28), acc=acc) == SHAPE
+
+
+def test_awq_rows_share_no_memory():
+    def mm(x=X, ldx=256, q=W, z=Y, s=SCALES, M=4, N=64, K=256, g=32, dt=F32, y=DX, ldy=64):
+        return moe.lib().moe_awq_matmul(x, ldx, q, z, s, M, N, K, g, dt, y, ldy, None, 0, None)
+    for p, size in ((X, 2 * 4 * 256), (W, 4 * 256 * 8), (Y, 4 * 8 * 8), (SCALES, 2 * 8 * 64)):
+        assert mm(y=p) == SHAPE and mm(y=at(p, size - 4)) == SHAPE and mm(y=at(p, -4 * 4 * 64 + 4)) == SHAPE
