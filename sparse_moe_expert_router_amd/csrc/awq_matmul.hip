@@ -533,12 +533,11 @@ void run_awq_rows(const Awq& a, const Plan& p, hipStream_t s) {
     if (p.mt == 2) hipLaunchKernelGGL((awq_rows_kernel<CW, 2, WV>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((awq_rows_kernel<CW, 1, WV>), grid, block, 0, s, a);
 }
-template <int CW, int WV>
-void run_awq(const Awq& a, const Plan& p, hipStream_t s) {
-    const dim3 grid((p.tiles + 7) / 8 * 8, p.splits, 1), block(64 * WV);
-    if (p.mt) run_awq_rows<CW, WV>(a, p, s);
-    else if (a.M == 1) hipLaunchKernelGGL((awq_few_kernel<CW, 1, WV>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((awq_few_kernel<CW, 4, WV>), grid, block, 0, s, a);
+template <int CW>
+void run_awq_few(const Awq& a, const Plan& p, hipStream_t s) {
+    const dim3 grid((p.tiles + 7) / 8 * 8, p.splits, 1), block(64 * 4);
+    if (a.M == 1) hipLaunchKernelGGL((awq_few_kernel<CW, 1, 4>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((awq_few_kernel<CW, 4, 4>), grid, block, 0, s, a);
 }
 
 }  // namespace
@@ -576,14 +575,18 @@ hipError_t launch_awq_matmul(const uint16_t* x, int64_t ldx, const int32_t* qwei
     const Plan p = plan(M, N, K, N % 16 == 0 && ((uintptr_t)qweight | (uintptr_t)qzeros) % 8 == 0);
     a.part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
     a.tiles = p.tiles;
-    if (p.waves == 8) {
+    if (!p.mt) {  // (four waves)
+        if (p.cw == 16) run_awq_few<16>(a, p, s);
+        else if (p.cw == 8) run_awq_few<8>(a, p, s);
+        else if (p.cw == 4) run_awq_few<4>(a, p, s);
+        else run_awq_few<2>(a, p, s);
+    } else if (p.waves == 8) {  // (large matrices)
         if (p.cw == 16) run_awq_rows<16, 8>(a, p, s);
         else run_awq_rows<8, 8>(a, p, s);
     } else {
-        if (p.cw == 16) run_awq<16, 4>(a, p, s);
-        else if (p.cw == 8) run_awq<8, 4>(a, p, s);
-        else if (p.cw == 4) run_awq<4, 4>(a, p, s);
-        else run_awq<2, 4>(a, p, s);
+        if (p.cw == 8) run_awq_rows<8, 4>(a, p, s);
+        else if (p.cw == 4) run_awq_rows<4, 4>(a, p, s);
+        else run_awq_rows<2, 4>(a, p, s);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
