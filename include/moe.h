@@ -504,8 +504,10 @@ moe_status moe_grouped_ffn_a8(const uint16_t *x, int32_t T, int32_t k, const moe
  * MOE_OUT_BF16 or MOE_OUT_F32.  residual_out and y may be an input of the same
  * type and stride (residual_out = residual, y = x); any other overlap of an output
  * with an input or another output -> MOE_ERR_SHAPE.  A row that holds an infinity or a
- * NaN gives NaN (and 0) in its own row only; squares are summed in fp32, so a row
- * of values above about 1e18 gives zeros.
+ * NaN gives NaN (and 0) in its own row only.  Squares are summed over the row in
+ * fp32 before they are divided by H: a row whose sum of squares reaches 2^128 (all
+ * values near 1.8e19 / sqrt(H): 1.4e17 for H = 16384, 6.5e18 for H = 8) gives
+ * zeros and rstd 0, from which moe_add_rmsnorm_backward makes dx = dres.
  * H % 8 == 0 (with codes H % 16 == 0), H <= 16384, rows of whole 16-byte pieces,
  * x, residuals, weight, y and codes 16-byte aligned, scales and rstd 4-byte
  * (MOE_ERR_UNSUPPORTED otherwise); eps not in (0, 3e38) or gain_offset not

@@ -1,10 +1,10 @@
-"""Edges of the operators around the layer: infinite scales beside a run's end."""
+"""Edges of the operators around the layer: infinite scales beside a run's end, sums of squares near fp32's end."""
 import pytest
 import torch
 
 import sparse_moe_expert_router_amd as moe
 from tests import around_ref as R
-from tests.test_gpu_around import BF, DEV, _awq, _randn
+from tests.test_gpu_around import BF, DEV, F32, _awq, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +43,28 @@ def test_awq_infinite_scale(M, N, K, group):
         fine[at, col] = 0
         ref, lim = R.awq(x, q, z, fine)
         R.check_rows(y[:, rest], ref[:, rest], 0.0, lim[:, rest])
+
+
+# ------------------------------------------------------------------ norm: where the sum of squares ends
+
+@pytest.mark.parametrize("H", [8, 128, 640, 8192, 16384])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_norm_up_to_the_largest_sum_of_squares(H, dtype):
+    """A row of one magnitude: right while its squares' sum is below fp32's end (2^128), zeros beyond."""
+    border = (2.0 ** 128 / H) ** 0.5
+    x = torch.where(_randn(6, H, seed=H) > 0, 1.0, -1.0)
+    x[0] *= border * 0.97
+    x[1] *= border * 1.03
+    x[2] *= border * 1e-3
+    x[3] *= border * 10
+    x = x.to(dtype)
+    w = _randn(H, seed=1, scale=0.1)
+    r = moe.add_rmsnorm(x, w, outputs=("y", "rstd"))
+    fine = [0, 2, 4, 5]
+    v, rstd = R.norm(x[fine], w, 1e-6, 1.0)
+    R.check_rows(r.y[fine], v)
+    assert ((r.rstd[fine].double() - rstd).abs() <= R.NORM_REL * rstd).all()
+    assert (r.y[[1, 3]] == 0).all() and (r.rstd[[1, 3]] == 0).all()
+    dy, dres = _randn(6, H, seed=2, dtype=dtype), _randn(6, H, seed=3, dtype=dtype)
+    dx, _ = moe.add_rmsnorm_backward(dy, x, r.rstd, w, dres=dres)
+    assert torch.equal(dx[[1, 3]], dres[[1, 3]])
