@@ -1,10 +1,11 @@
-"""Edges of the operators around the layer: infinite scales beside a run's end, sums of squares near fp32's end."""
+"""Edges of the operators around the layer: infinite scales beside a run's end, sums of squares near fp32's end,
+long sums over tokens.  Bounds in units of U = 2^-24, half a step of fp32."""
 import pytest
 import torch
 
 import sparse_moe_expert_router_amd as moe
 from tests import around_ref as R
-from tests.test_gpu_around import BF, DEV, F32, _awq, _randn
+from tests.test_gpu_around import BF, DEV, F32, _awq, _gen, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +69,55 @@ def test_norm_up_to_the_largest_sum_of_squares(H, dtype):
     dy, dres = _randn(6, H, seed=2, dtype=dtype), _randn(6, H, seed=3, dtype=dtype)
     dx, _ = moe.add_rmsnorm_backward(dy, x, r.rstd, w, dres=dres)
     assert torch.equal(dx[[1, 3]], dres[[1, 3]])
+
+
+# ------------------------------------------------------------------ balance loss: long sums
+
+def _teams(T, E, k):
+    """The least number of teams that share T tokens; a team adds its tokens' probabilities one after another."""
+    lanes = 16 if E <= 64 and k <= 16 else 32 if E <= 256 and k <= 32 else 64
+    teams = 8 * 64 // lanes
+    need = -(-T // teams)
+    return teams * (1 if need <= 4 else min(need, 256 if E > 512 else 768))
+
+
+def _sums(logits, counts, k, coef):
+    """loss and prob_sum in 64 bits with their bounds, in pieces of rows.
+
+    A probability's relative error, x = v - max: the difference's rounding, the product with log2 e and that constant's
+    own (0.23 U) come to 2.25 |x| U in the exponent; the exponential, the sum over the experts (at most 16 in a lane, then
+    6 steps), the reciprocal and the product below 48 U.  The sum's error is the probabilities' own mean."""
+    T, E = logits.shape
+    C = float(counts.sum())
+    a = coef * E * k / C
+    f = counts.double() / C - 1.0 / E
+    zero = lambda: torch.zeros(E, dtype=torch.float64, device=DEV)
+    S, lim, fp, flim = zero(), zero(), 0.0, 0.0
+    for part in logits.split(50000):
+        x = part.double()
+        x = x - x.amax(1, keepdim=True)
+        p = torch.softmax(x, 1)
+        rel = (48.0 + 2.25 * x.abs()) * R.U
+        err = p * (rel + (p * rel).sum(1, keepdim=True)) + 2.0 ** -126
+        S += p.sum(0)
+        lim += err.sum(0)
+        fp += float((p @ f).sum())
+        # f' to fp32 and the fused sums of f' p: 24 U of the magnitudes
+        flim += float((err @ f.abs()).sum() + 24 * R.U * (p @ f.abs()).sum())
+    # a team's tokens one after another, at most 32 teams of a workgroup, then at most 6 + 7 + 15 additions over workgroups
+    lim += (-(-T // _teams(T, E, k)) + 60) * R.U * S
+    return a * (fp + T / E), abs(a) * flim, S, lim
+
+
+@pytest.mark.parametrize("T,E,k,dtype", [(40000, 1000, 5, F32), (40000, 1024, 8, BF), (30001, 516, 4, F32), (2_200_000, 1024, 2, BF),
+                                         (300_000, 512, 10, F32), (500_000, 61, 6, BF)])
+def test_balance_sums_over_many_tokens(T, E, k, dtype):
+    logits = torch.empty((T, E), dtype=dtype, device=DEV)
+    for i, part in enumerate(logits.split(200_000)):
+        part.copy_(torch.randn(part.shape, generator=_gen(i), device=DEV) * 1.5 + _randn(E, seed=99))
+    counts = torch.randint(1, 1000, (E,), generator=_gen(7), device=DEV, dtype=torch.int32)
+    loss, prob_sum, d = moe.balance_loss(logits, counts, k, 0.01, want_dlogits=False)
+    ref, lim, S, slim = _sums(logits, counts, k, 0.01)
+    assert d is None
+    assert ((prob_sum.double() - S).abs() <= slim + R.U * S).all(), float(((prob_sum.double() - S).abs() / slim).max())
+    assert abs(float(loss) - ref) <= lim + 2 * R.U * abs(ref), (float(loss), ref, lim)
