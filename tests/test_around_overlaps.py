@@ -1,9 +1,9 @@
-"""Memory that the operators around the layer refuse to share between an output and anything else, before any HIP call (the
-pointers are never dereferenced)."""
+"""Memory that the operators around the layer refuse to share between an output and anything else, and
+workspaces that are too small, before any HIP call (the pointers are never dereferenced)."""
 import ctypes
 
 import sparse_moe_expert_router_amd as moe
-from tests.test_around_abi import CODES, DX, F32, P, RES, RSTD, SCALES, SHAPE, W, X, Y, _bal, _bwd, _norm
+from tests.test_around_abi import CODES, DW, DX, F32, NULL, P, RES, RSTD, SCALES, SHAPE, UNSUP, W, WS, X, Y, _bal, _bwd, _norm
 
 VALID = P(12)
 
@@ -63,3 +63,10 @@ def test_awq_rows_share_no_memory():
         return moe.lib().moe_awq_matmul(x, ldx, q, z, s, M, N, K, g, dt, y, ldy, None, 0, None)
     for p, size in ((X, 2 * 4 * 256), (W, 4 * 256 * 8), (Y, 4 * 8 * 8), (SCALES, 2 * 8 * 64)):
         assert mm(y=p) == SHAPE and mm(y=at(p, size - 4)) == SHAPE and mm(y=at(p, -4 * 4 * 64 + 4)) == SHAPE
+
+
+def test_awq_large_matrices_need_a_workspace_and_refuse_without():
+    need = moe.lib().moe_awq_matmul_workspace_bytes(1, 8192, 8192, 128)
+    assert need > 0
+    mm = lambda ws, n: moe.lib().moe_awq_matmul(X, 8192, W, Y, SCALES, 1, 8192, 8192, 128, F32, DX, 8192, ws, n, None)
+    assert mm(DW, need - 1) == WS and mm(None, need) == NULL and mm(at(DW, 8), need) == UNSUP

@@ -1,11 +1,11 @@
 """Edges of the operators around the layer: infinite scales beside a run's end, sums of squares near fp32's end,
-long sums over tokens.  Bounds in units of U = 2^-24, half a step of fp32."""
+long sums over tokens, workspaces of exactly the stated size.  Bounds in units of U = 2^-24, half a step of fp32."""
 import pytest
 import torch
 
 import sparse_moe_expert_router_amd as moe
 from tests import around_ref as R
-from tests.test_gpu_around import BF, DEV, F32, _awq, _gen, _randn
+from tests.test_gpu_around import BF, DEV, F32, _awq, _gen, _randn, _routing
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +121,61 @@ def test_balance_sums_over_many_tokens(T, E, k, dtype):
     assert d is None
     assert ((prob_sum.double() - S).abs() <= slim + R.U * S).all(), float(((prob_sum.double() - S).abs() / slim).max())
     assert abs(float(loss) - ref) <= lim + 2 * R.U * abs(ref), (float(loss), ref, lim)
+
+
+# ------------------------------------------------------------------ workspaces of exactly the stated size
+
+def _guarded(n):
+    buf = torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+    return buf, lambda: bool((buf[n:] == 0xA5).all())
+
+
+def _stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+@pytest.mark.parametrize("N,K", [(8192, 8192), (8192, 4128), (264, 8192), (4104, 8192)])
+def test_awq_workspace_of_the_largest_number_of_rows(N, K):
+    q, z, s = _awq(K, N, 32, 21)
+    x = _randn(65, K, seed=22, dtype=BF)
+    n = moe.lib().moe_awq_matmul_workspace_bytes(65, N, K, 32)
+    assert n > 0
+    ws, untouched = _guarded(n)
+    for M in (65, 64, 48, 33, 32, 20, 17, 16, 5, 4, 3, 1):
+        y = torch.empty((M, N), device=DEV)
+        assert moe.lib().moe_awq_matmul(x.data_ptr(), K, q.data_ptr(), z.data_ptr(), s.data_ptr(), M, N, K, 32, moe.OUT_F32, y.data_ptr(), N,
+                                        ws.data_ptr(), n, _stream()) == 0
+        ref, lim = R.awq(x[:M], q, z, s)
+        R.check_rows(y, ref, 0.0, lim)
+        assert untouched()
+
+
+@pytest.mark.parametrize("H", [72, 264, 2560, 8200])
+def test_norm_backward_workspace_of_the_most_rows(H):
+    most = 4100
+    s, dy, w = _randn(most, H, seed=23), _randn(most, H, seed=24), _randn(H, seed=25, scale=0.1)
+    rstd = moe.add_rmsnorm(s, w, outputs=("y", "rstd")).rstd
+    n = moe.workspace_bytes(moe.OP_ADD_RMSNORM_BACKWARD, most, 1, 1, H)
+    ws, untouched = _guarded(n)
+    for T in (4100, 769, 768, 1):
+        dx, dw = torch.empty((T, H), device=DEV), torch.empty(H, device=DEV)
+        assert moe.lib().moe_add_rmsnorm_backward(dy.data_ptr(), moe.OUT_F32, H, s.data_ptr(), H, moe.OUT_F32, rstd.data_ptr(), w.data_ptr(),
+                                                  moe.OUT_F32, 1.0, None, 0, T, H, dx.data_ptr(), H, dw.data_ptr(), ws.data_ptr(), n, _stream()) == 0
+        rx, lx, rw, lw = R.norm_backward(dy[:T], s[:T], rstd[:T], w, 1.0)
+        R.check_rows(dx, rx, 0.0, lx)
+        assert ((dw.double() - rw).abs() <= lw).all() and untouched()
+
+
+@pytest.mark.parametrize("E,k", [(61, 6), (200, 8), (512, 10), (1000, 4)])
+def test_balance_workspace_of_the_most_tokens(E, k):
+    most = 20000
+    logits, idx, _ = _routing(most, E, k, F32, 26)
+    n = moe.workspace_bytes(moe.OP_BALANCE_LOSS, most, k, E, 0)
+    ws, untouched = _guarded(n)
+    counts = moe.expert_counts(idx, E)
+    for T in (20000, 2000, 65, 1):
+        loss, prob_sum, d = torch.empty(1, device=DEV), torch.empty(E, device=DEV), torch.empty((T, E), device=DEV)
+        assert moe.lib().moe_balance_loss(logits.data_ptr(), moe.OUT_F32, E, T, E, k, counts.data_ptr(), 0.01, None, None, None, None,
+                                          loss.data_ptr(), prob_sum.data_ptr(), d.data_ptr(), moe.OUT_F32, E, ws.data_ptr(), n, _stream()) == 0
+        want = moe.balance_loss(logits[:T], counts, k, 0.01)
+        assert all(torch.equal(a, b) for a, b in zip((loss, prob_sum, d), want)) and untouched()
