@@ -68,7 +68,9 @@ __device__ __forceinline__ float dot2_bf16(uint32_t a, uint32_t b, float c) {
 // (a & m) | c as one v_and_or_b32.  A VOP3 instruction on gfx9 takes no
 // literal operand, so with both constants written as literals the compiler
 // falls back to a separate AND and OR; here the mask travels in a VGPR and
-// the constant in an SGPR.
+// the constant in an SGPR.  The result must not be an MFMA's operand: the
+// compiler does not see a vector instruction in here, and leaves out the two
+// states that an MFMA waits for one (awq_matmul.hip's Bits is the safe form).
 __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t m, uint32_t c) {
     uint32_t r;
     asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(m), "s"(c));
