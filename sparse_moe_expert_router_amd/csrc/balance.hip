@@ -391,10 +391,11 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(const float* __restri
 
 namespace {
 
-// Up to here one launch counts: the host gains 3 to 4 us a call, a captured call
-// loses as much at the end (counts and loss, 8191 tokens to 6 of 61 experts: 19.5
-// against 22.8 us a call, 16.0 against 13.3 in a graph; 6500 to 10 of 512: 23.1
-// against 23.3, and 22.8 against 19.3).
+// Up to here one launch counts.  It spares the host 2.5 us a call, but each of its workgroups reads all pairs; the two
+// launches take 4.0 to 4.8 us in a graph whatever the number.  One launch against two, 61 or 512 experts, us a call: 20000
+// pairs 5.5, 7.9; 49146 7.0, 7.9; 65000 8.5, 7.9 (in a graph 10000 3.9, 4.4; 20000 4.6, 4.3; 49146 7.2, 4.4; 65000 8.7, 4.4).
+// So the border is that of calls outside a graph, which pay for it inside one from about 15000 pairs on.  Below 16 experts
+// there is one workgroup, the slower form from about 28000 pairs on (8 experts: 20000 6.1, 7.8; 49150 11.4, 7.9).
 constexpr uint32_t kCountOwn = 49152;
 
 // Lanes of a token: the sums over them cost as much for few experts as for many, and short rows share a wave (65536
