@@ -564,6 +564,14 @@ def _on(name, device, *tensors):
             raise MoeError(f"{name}: tensors on different devices")
 
 
+def _scratch(name, ws, device, nbytes):
+    """(buffer, bytes) on `device`: of the given workspace, or allocated for the call."""
+    buf, n = (ws or Workspace(device)).get(nbytes)
+    if buf is not None and buf.device != device:
+        raise MoeError(f"{name}: the workspace is on {buf.device}, not on {device}")
+    return buf, n
+
+
 class NormResult(NamedTuple):
     """What add_rmsnorm wrote; None where it was not asked for."""
     y: torch.Tensor | None         # bf16 [T, H]
@@ -650,7 +658,7 @@ def add_rmsnorm_backward(dy, s, rstd, weight, gain_offset: float = 1.0, dres=Non
              "weight must be contiguous bf16 or fp32 [H]")
     _on(name, s.device, dy, rstd, weight, dres, dx, dw)
     d = _Device(s)
-    buf, n = (ws or Workspace(s.device)).get(workspace_bytes(OP_ADD_RMSNORM_BACKWARD, T, 1, 1, H))
+    buf, n = _scratch(name, ws, s.device, workspace_bytes(OP_ADD_RMSNORM_BACKWARD, T, 1, 1, H))
     d.call(name, py, dyt, ldy, ps, lds, ds, pt, weight.data_ptr(), _DTYPES[weight.dtype], gain_offset, pd, ldd, T, H, px, ldx,
            pw, None if buf is None else buf.data_ptr(), n, d.stream)
     return dx, dw
@@ -712,7 +720,7 @@ def balance_loss(logits, counts, k: int, coef: float, token_valid=None, topk_idx
     d = _Device(logits)
     loss = torch.empty(1, dtype=torch.float32, device=dev)
     prob_sum = torch.empty(E, dtype=torch.float32, device=dev)
-    buf, n = (ws or Workspace(dev)).get(workspace_bytes(OP_BALANCE_LOSS, T, k, E, 0))
+    buf, n = _scratch(name, ws, dev, workspace_bytes(OP_BALANCE_LOSS, T, k, E, 0))
     d.call(name, pl, dl, ld, T, E, k, pc, coef, pv, pi, pg, pdg, loss.data_ptr(), prob_sum.data_ptr(), pd, dd, ldd,
            None if buf is None else buf.data_ptr(), n, d.stream)
     return loss, prob_sum, dlogits
@@ -741,7 +749,7 @@ def awq_matmul(x, qweight, qzeros, scales, out_dtype=None, y=None, ws=None):
     _on(name, x.device, qweight, qzeros, scales, y)
     d = _Device(x)
     need = int(lib().moe_awq_matmul_workspace_bytes(M, N, K, K // groups))
-    buf, n = (ws or Workspace(x.device)).get(need) if need else (None, 0)
+    buf, n = _scratch(name, ws, x.device, need) if need else (None, 0)
     d.call(name, px, ldx, pq, pz, psc, M, N, K, K // groups, yt, py, ldy, None if buf is None else buf.data_ptr(), n, d.stream)
     return y
 

@@ -2,6 +2,9 @@
 workspaces that are too small, before any HIP call (the pointers are never dereferenced)."""
 import ctypes
 
+import pytest
+import torch
+
 import sparse_moe_expert_router_amd as moe
 from tests.test_around_abi import CODES, DW, DX, F32, NULL, P, RES, RSTD, SCALES, SHAPE, UNSUP, W, WS, X, Y, _bal, _bwd, _norm
 
@@ -70,3 +73,12 @@ def test_awq_large_matrices_need_a_workspace_and_refuse_without():
     assert need > 0
     mm = lambda ws, n: moe.lib().moe_awq_matmul(X, 8192, W, Y, SCALES, 1, 8192, 8192, 128, F32, DX, 8192, ws, n, None)
     assert mm(DW, need - 1) == WS and mm(None, need) == NULL and mm(at(DW, 8), need) == UNSUP
+
+
+def test_a_workspace_of_another_device_is_refused():
+    from sparse_moe_expert_router_amd import _lib
+    with pytest.raises(moe.MoeError, match="workspace is on cpu"):
+        _lib._scratch("call", moe.Workspace("cpu"), torch.device("meta"), 64)
+    buf, n = _lib._scratch("call", None, torch.device("cpu"), 64)
+    assert buf.device.type == "cpu" and n == 64
+    assert _lib._scratch("call", moe.Workspace("cpu"), torch.device("meta"), 0) == (None, 0)

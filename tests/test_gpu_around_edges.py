@@ -179,3 +179,15 @@ def test_balance_workspace_of_the_most_tokens(E, k):
                                           loss.data_ptr(), prob_sum.data_ptr(), d.data_ptr(), moe.OUT_F32, E, ws.data_ptr(), n, _stream()) == 0
         want = moe.balance_loss(logits[:T], counts, k, 0.01)
         assert all(torch.equal(a, b) for a, b in zip((loss, prob_sum, d), want)) and untouched()
+
+
+def test_workspaces_of_another_device_are_refused():
+    cpu = moe.Workspace("cpu")
+    x, w = _randn(8, 64, seed=27), _randn(64, seed=28)
+    rstd = moe.add_rmsnorm(x, w, outputs=("y", "rstd")).rstd
+    counts = torch.ones(64, dtype=torch.int32, device=DEV)
+    q, z, s = _awq(8192, 8192, 128, 29)
+    for call in (lambda: moe.add_rmsnorm_backward(x, x, rstd, w, ws=cpu), lambda: moe.balance_loss(x, counts, 2, 0.01, ws=cpu),
+                 lambda: moe.awq_matmul(_randn(1, 8192, seed=30, dtype=BF), q, z, s, ws=cpu)):
+        with pytest.raises(moe.MoeError, match="workspace is on cpu"):
+            call()
