@@ -503,7 +503,9 @@ moe_status moe_grouped_ffn_a8(const uint16_t *x, int32_t T, int32_t k, const moe
  * One of y and codes must be given.  x_dtype, res_dtype and w_dtype are
  * MOE_OUT_BF16 or MOE_OUT_F32.  residual_out and y may be an input of the same
  * type and stride (residual_out = residual, y = x); any other overlap of an output
- * with an input or another output -> MOE_ERR_SHAPE.  A row that holds an infinity or a
+ * with an input or another output -> MOE_ERR_SHAPE (here and below, rows of the
+ * same stride in bytes may lie in each other's gaps; of different strides they
+ * overlap where their ranges cross).  A row that holds an infinity or a
  * NaN gives NaN (and 0) in its own row only.  Squares are summed over the row in
  * fp32 before they are divided by H: a row whose sum of squares reaches 2^128 (all
  * values near 1.8e19 / sqrt(H): 1.4e17 for H = 16384, 6.5e18 for H = 8) gives
