@@ -598,9 +598,10 @@ moe_status moe_balance_loss(const void *logits, int32_t logits_dtype, int64_t lo
  * (16 + q) and x (16 + z) are summed and subtracted per 32 inputs, so the sums'
  * roundings are those of values up to 31 |x| (and |x| above about 1e36 overflows).  Every 32 rows read the codes
  * again: any M works, but the call is made for up to about 64 rows.  A row of x
- * that holds an infinity or a NaN gives NaN in that row only.  A scale that is
- * one reaches its column only: an infinite scale multiplies its group's sums of
- * 32 inputs one by one and gives an infinity where they have one sign, else NaN.
+ * that holds an infinity or a NaN gives NaN in that row only.  A
+ * scale that is one of these reaches its own column only: NaN, or for an infinite
+ * scale, which multiplies its group's sums of 32 inputs one by one, an infinity
+ * where they all have one sign.
  * N % 8 == 0, K % group == 0, ldx % 8 == 0, N, K and ldx at most 2^24, M at most
  * 2^20, fewer than 2^20 tiles of 32 rows x 1024 columns; x and scales 16-byte aligned,
  * the rest aligned to its element (MOE_ERR_UNSUPPORTED otherwise).  Workspace:
